@@ -9,6 +9,9 @@ library is not built, every call raises.
     scores, cu_blocks = score_blocks(q_last, k, cu_seqlens, n, G)
     keep, kept_tokens = select_topp(scores, cu_blocks, cu_seqlens, G, p)
     x_out, pos_out, cu_out, total = compact(x, pos, cu_seqlens, G, keep, cu_blocks)
+
+Beside the path, the paged KV cache it reads keys from: append_kv, attend_paged
+and decode_attend over a PagedKV (paged.py).
 """
 from __future__ import annotations
 
@@ -18,12 +21,16 @@ import os
 import torch
 
 from . import _build
+from .paged import (PagedKV, append_kv, attend_paged, attend_paged_workspace, decode_attend,
+                    decode_attend_workspace)
 
 __all__ = ["build", "lib", "UpError", "score_blocks_workspace", "score_blocks",
            "score_blocks_paged", "block_csr", "shard_heads",
            "tp_score_blocks", "select_topp",
            "compact_workspace", "compact", "compact_noalloc", "set_kernel_timing_events",
-           "set_wait_limit", "get_device_error", "Sparsifier", "SELECT_MAX_BLOCKS"]
+           "set_wait_limit", "get_device_error", "Sparsifier", "SELECT_MAX_BLOCKS", "PagedKV",
+           "append_kv", "attend_paged", "attend_paged_workspace", "decode_attend",
+           "decode_attend_workspace"]
 
 SELECT_MAX_BLOCKS = 16384
 _lib = None
@@ -86,6 +93,17 @@ def load_library(path):
     L.up_get_device_error.restype = I
     L.up_measure_ex2_rate.argtypes = [ctypes.POINTER(ctypes.c_double), P]
     L.up_measure_ex2_rate.restype = I
+    F = ctypes.c_uint32
+    L.up_append_kv.argtypes = [P, I64, P, I64, P, I64, P, I, P, P, I, F, P, I64, I, P, P, P]
+    L.up_append_kv.restype = I
+    L.up_attend_paged_workspace.argtypes = [I64, I, I, I, I]
+    L.up_attend_paged_workspace.restype = SZ
+    L.up_attend_paged.argtypes = [P, P, I64, I, P, P, P, P, P, P, SZ, P]
+    L.up_attend_paged.restype = I
+    L.up_decode_attend_workspace.argtypes = [I, I, I, I]
+    L.up_decode_attend_workspace.restype = SZ
+    L.up_decode_attend.argtypes = [P, I, P, P, P, P, P, P, SZ, P]
+    L.up_decode_attend.restype = I
     L.up_set_wait_limit.argtypes = [ctypes.c_uint64]
     L.up_set_wait_limit.restype = I
     return L

@@ -3,22 +3,11 @@
 #include <atomic>
 #include <mutex>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "../../include/up.h"
+#include "api_util.cuh"
 #include "common.cuh"
 
 namespace {
-
-// A named NVTX range around each public call's host work (argument checks and
-// launches), so a timeline profiler shows the three calls of a step; without
-// a profiler attached a push or pop is a check of a null hook.
-struct CallRange {
-    explicit CallRange(const char *name) { nvtxRangePushA(name); }
-    ~CallRange() { nvtxRangePop(); }
-    CallRange(const CallRange &) = delete;
-    CallRange &operator=(const CallRange &) = delete;
-};
 
 // Sticky device error word (UP_DEVERR_* bits), one per device.
 __device__ unsigned int g_up_device_error;
@@ -58,8 +47,6 @@ up_status device_state(DeviceState **out) {
     return UP_OK;
 }
 
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
-
 }  // namespace
 
 namespace up {
@@ -67,13 +54,20 @@ unsigned int *device_error_word() {
     DeviceState *ds = nullptr;
     return device_state(&ds) == UP_OK ? ds->err : nullptr;
 }
+
+up_status device_info(DeviceInfo *out) {
+    DeviceState *ds = nullptr;
+    const up_status st = device_state(&ds);
+    if (st != UP_OK) return st;
+    *out = DeviceInfo{ds->sms, ds->err, g_wait_limit.load()};
+    return UP_OK;
+}
 }  // namespace up
 
 namespace {
 
 bool valid_G(int G) { return G == 16 || G == 32 || G == 64 || G == 128 || G == 256; }
 bool valid_d(int d) { return d == 64 || d == 128 || d == 256; }
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Keys per work unit (a multiple of 256).  The CTAs of the score kernel walk
 // the units round-robin, so the step count of the slowest CTA is
@@ -117,12 +111,12 @@ up::ScoreLayout score_layout(int B, int64_t total, int Hq, int Hk, int d, int n,
     L.max_units = (int64_t)Hk * (((nn + tpt - 1) / tpt + tpu - 1) / tpu) * max_chunks;
     L.max_qrows = ns_sum;
     size_t off = 0;
-    L.seqs = off;     off = align256(off + sizeof(up::SeqInfo) * (size_t)(B > 0 ? B : 1));
-    L.counters = off; off = align256(off + sizeof(up::Counters));
-    L.part = off;     off = align256(off + sizeof(float) * (size_t)L.max_part);
-    L.mref = off;     off = align256(off + sizeof(float) * (size_t)L.max_stat);
-    L.lsum = off;     off = align256(off + sizeof(float) * (size_t)L.max_stat);
-    L.flags = off;    off = align256(off + sizeof(int32_t) * (size_t)(32 * L.max_units + 16));
+    L.seqs = off;     off = up::align256(off + sizeof(up::SeqInfo) * (size_t)(B > 0 ? B : 1));
+    L.counters = off; off = up::align256(off + sizeof(up::Counters));
+    L.part = off;     off = up::align256(off + sizeof(float) * (size_t)L.max_part);
+    L.mref = off;     off = up::align256(off + sizeof(float) * (size_t)L.max_stat);
+    L.lsum = off;     off = up::align256(off + sizeof(float) * (size_t)L.max_stat);
+    L.flags = off;    off = up::align256(off + sizeof(int32_t) * (size_t)(32 * L.max_units + 16));
     L.total = off;
     return L;
 }
@@ -135,9 +129,9 @@ CompactLayout compact_layout(int B, int64_t total, int G) {
     CompactLayout L{};
     const int64_t max_blocks = total / G + B;
     size_t off = 0;
-    L.nkept = off;   off = align256(off + 256);
-    L.list = off;    off = align256(off + sizeof(int4) * (size_t)(max_blocks > 0 ? max_blocks : 1));
-    L.dst_blk = off; off = align256(off + sizeof(int32_t) * (size_t)(max_blocks > 0 ? max_blocks : 1));
+    L.nkept = off;   off = up::align256(off + 256);
+    L.list = off;    off = up::align256(off + sizeof(int4) * (size_t)(max_blocks > 0 ? max_blocks : 1));
+    L.dst_blk = off; off = up::align256(off + sizeof(int32_t) * (size_t)(max_blocks > 0 ? max_blocks : 1));
     L.total = off;
     return L;
 }
@@ -199,7 +193,7 @@ up_status check_score_args(const void *q_last, const void *k, const int32_t *cu_
     if (total_tokens > 0 && (!q_last || !k || !scores)) return UP_ERR_INVALID_ARG;
     if (Hq < 1 || Hk < 1 || Hq % Hk != 0 || n < 1 || d < 1 || G < 1) return UP_ERR_INVALID_ARG;
     if (Hq / Hk > 16 || !valid_d(d) || !valid_G(G) || n > 1024) return UP_ERR_UNSUPPORTED;
-    if (!aligned(q_last, 16) || !aligned(k, 16) || !aligned(scores, 4)) return UP_ERR_INVALID_ARG;
+    if (!up::aligned(q_last, 16) || !up::aligned(k, 16) || !up::aligned(scores, 4)) return UP_ERR_INVALID_ARG;
     return UP_OK;
 }
 
@@ -221,7 +215,7 @@ up_status score_impl(const void *q_last, const void *k, const int32_t *cu_seqlen
     up_status st = check_score_args(q_last, k, cu_seqlens, num_seqs, total_tokens, Hq, Hk, d, n,
                                     G, scores, cu_blocks);
     if (st != UP_OK) return st;
-    if (!workspace || !aligned(workspace, 256) ||
+    if (!workspace || !up::aligned(workspace, 256) ||
         workspace_bytes < score_layout(num_seqs, total_tokens, Hq, Hk, d, n, G, up::kChunkQuantum).total)
         return UP_ERR_WORKSPACE;
     DeviceState *ds = nullptr;
@@ -298,7 +292,7 @@ up_status up_score_blocks(const void *q_last, const void *k, const int32_t *cu_s
                           int num_seqs, int64_t total_tokens, int Hq, int Hk, int d, int n,
                           int G, float *scores, int32_t *cu_blocks, void *workspace,
                           size_t workspace_bytes, up_stream_t stream) {
-    const CallRange range("up_score_blocks");
+    const up::CallRange range("up_score_blocks");
     return score_impl(q_last, k, cu_seqlens, num_seqs, total_tokens, Hq, Hk, d, n, G, Hq,
                       PagedKeys{}, scores, cu_blocks, workspace, workspace_bytes, stream);
 }
@@ -307,7 +301,7 @@ up_status up_score_blocks_shard(const void *q_last, const void *k, const int32_t
                                 int num_seqs, int64_t total_tokens, int Hq, int Hk, int d, int n,
                                 int G, int Hq_total, float *scores, int32_t *cu_blocks,
                                 void *workspace, size_t workspace_bytes, up_stream_t stream) {
-    const CallRange range("up_score_blocks_shard");
+    const up::CallRange range("up_score_blocks_shard");
     if (Hq_total < Hq || Hq_total < 1) return UP_ERR_INVALID_ARG;
     return score_impl(q_last, k, cu_seqlens, num_seqs, total_tokens, Hq, Hk, d, n, G, Hq_total,
                       PagedKeys{}, scores, cu_blocks, workspace, workspace_bytes, stream);
@@ -319,7 +313,7 @@ up_status up_score_blocks_paged(const void *q_last, const void *k_pages, int64_t
                                 int Hq, int Hk, int d, int n, int G, float *scores,
                                 int32_t *cu_blocks, void *workspace, size_t workspace_bytes,
                                 up_stream_t stream) {
-    const CallRange range("up_score_blocks_paged");
+    const up::CallRange range("up_score_blocks_paged");
     if (!block_table || page_size < 128 || page_size % 128 != 0 || num_pages < 1 ||
         max_pages < 1 || Hk < 1 || num_pages * (int64_t)Hk * page_size >= ((int64_t)1 << 31))
         return UP_ERR_INVALID_ARG;
@@ -335,7 +329,7 @@ up_status up_score_blocks_paged(const void *q_last, const void *k_pages, int64_t
 up_status up_select_topp(const float *scores, const int32_t *cu_blocks,
                          const int32_t *cu_seqlens, int num_seqs, int G, double p,
                          uint8_t *keep, int32_t *kept_tokens, up_stream_t stream) {
-    const CallRange range("up_select_topp");
+    const up::CallRange range("up_select_topp");
     if (num_seqs < 0 || G < 1 || !(p > 0.0)) return UP_ERR_INVALID_ARG;
     if (!valid_G(G)) return UP_ERR_UNSUPPORTED;
     if (num_seqs > 0 && (!scores || !cu_blocks || !cu_seqlens || !keep || !kept_tokens))
@@ -354,7 +348,7 @@ up_status up_select_blocks(const float *scores, const int32_t *cu_blocks,
                            const int32_t *cu_seqlens, int num_seqs, int G, up_select_mode mode,
                            double p, int k, uint32_t flags, uint8_t *keep, int32_t *kept_tokens,
                            up_stream_t stream) {
-    const CallRange range("up_select_blocks");
+    const up::CallRange range("up_select_blocks");
     if (num_seqs < 0 || G < 1 || (flags & ~UP_SELECT_KEEP_LAST) != 0) return UP_ERR_INVALID_ARG;
     if (mode == UP_SELECT_TOP_P) {
         if (!(p > 0.0)) return UP_ERR_INVALID_ARG;
@@ -378,7 +372,7 @@ up_status up_select_blocks(const float *scores, const int32_t *cu_blocks,
 
 up_status up_block_csr(const uint8_t *keep, const int32_t *cu_blocks, int num_seqs,
                        int32_t *indptr, int32_t *indices, up_stream_t stream) {
-    const CallRange range("up_block_csr");
+    const up::CallRange range("up_block_csr");
     if (num_seqs < 0 || !keep || !cu_blocks || !indptr || !indices) return UP_ERR_INVALID_ARG;
     DeviceState *ds = nullptr;
     up_status st = device_state(&ds);
@@ -399,16 +393,16 @@ up_status up_compact(const void *x, const int32_t *pos, int hidden, const int32_
                      const int32_t *cu_blocks, void *x_out, int32_t *pos_out,
                      int32_t *cu_seqlens_out, int32_t *src_idx, int32_t *total_kept,
                      void *workspace, size_t workspace_bytes, up_stream_t stream) {
-    const CallRange range("up_compact");
+    const up::CallRange range("up_compact");
     if (num_seqs < 0 || total_tokens < 0 || total_tokens > INT32_MAX || hidden < 1 || G < 1)
         return UP_ERR_INVALID_ARG;
     if (!valid_G(G)) return UP_ERR_UNSUPPORTED;
     if (hidden % 8 != 0) return UP_ERR_UNSUPPORTED;
     if (!cu_seqlens || !cu_blocks || !cu_seqlens_out || !total_kept) return UP_ERR_INVALID_ARG;
     if (total_tokens > 0 && (!x || !pos || !keep || !x_out || !pos_out)) return UP_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(x_out, 16)) return UP_ERR_INVALID_ARG;
+    if (!up::aligned(x, 16) || !up::aligned(x_out, 16)) return UP_ERR_INVALID_ARG;
     const CompactLayout lay = compact_layout(num_seqs, total_tokens, G);
-    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256))
+    if (!workspace || workspace_bytes < lay.total || !up::aligned(workspace, 256))
         return UP_ERR_WORKSPACE;
     DeviceState *ds = nullptr;
     up_status st = device_state(&ds);

@@ -1,0 +1,195 @@
+// append.cu -- rotary positions and the append to the paged cache, in one kernel.
+//
+// Every new token's query, key and value rows are read once and written once:
+// 2 * (Hq + 2*Hk) * d * 2 bytes a token, which is all there is to do beside
+// rot/2 sines and cosines a token; so memory bounds a prompt and latency a step.
+//
+// A block takes a tile of consecutive tokens.  Their angles come first, one
+// thread per (token, frequency), into shared memory: computed once per token and
+// used by its Hq + Hk rows.  Then a thread moves 32 bytes at a time (one "unit"
+// of a row): for a rotated row the 8 dims [8u, 8u+8) and their partners half a
+// rotation away (or 16 adjacent dims when pairs are interleaved), for the rest
+// 16 adjacent dims, so both members of every pair are in one thread and no
+// element is exchanged.
+#include "paged.cuh"
+
+namespace up {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;    // tokens of a tile
+constexpr int kMaxHalf = 128;    // rot / 2
+constexpr int kInFlight = 4;     // units a thread loads before it stores any
+
+// The angle pos * inv_freq as a fraction of half a turn in [-1, 1): inv_freq is
+// taken to turns in 64 bits as a multiple of 2^-64 turns, whose product with the
+// position wraps at whole turns by itself, so the reduction is exact for every
+// 32-bit position.
+__device__ __forceinline__ float half_turns(float inv_freq, int pos) {
+    double t = (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
+    t -= rint(t);
+    const unsigned long long step = (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
+    const unsigned long long at = step * (unsigned long long)(long long)pos;
+    return (float)(int)(at >> 32) * 4.656612873077392578125e-10f;  // 2^-31
+}
+
+template <typename T2>
+__device__ __forceinline__ float2 to_f2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 to_f2<__nv_bfloat162>(uint32_t w) {
+    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&w));
+}
+template <>
+__device__ __forceinline__ float2 to_f2<__half2>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<__half2 *>(&w));
+}
+template <typename T2>
+__device__ __forceinline__ uint32_t from_f2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t from_f2<__nv_bfloat162>(float a, float b) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t from_f2<__half2>(float a, float b) {
+    const __half2 r = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Turns the 8 pairs of a unit: (x[i], y[i]) when split in halves, adjacent
+// elements of x then y when interleaved.  fp32 products, one rounding at the end.
+template <typename T2, bool kInterleaved>
+__device__ __forceinline__ void turn_unit(uint4 &x, uint4 &y, const float *cs, const float *sn) {
+    uint32_t *xw = reinterpret_cast<uint32_t *>(&x), *yw = reinterpret_cast<uint32_t *>(&y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = to_f2<T2>(xw[i]), b = to_f2<T2>(yw[i]);
+        if constexpr (kInterleaved) {
+            xw[i] = from_f2<T2>(a.x * cs[i] - a.y * sn[i], a.y * cs[i] + a.x * sn[i]);
+            yw[i] = from_f2<T2>(b.x * cs[4 + i] - b.y * sn[4 + i], b.y * cs[4 + i] + b.x * sn[4 + i]);
+        } else {
+            xw[i] = from_f2<T2>(a.x * cs[2 * i] - b.x * sn[2 * i],
+                                a.y * cs[2 * i + 1] - b.y * sn[2 * i + 1]);
+            yw[i] = from_f2<T2>(b.x * cs[2 * i] + a.x * sn[2 * i],
+                                b.y * cs[2 * i + 1] + a.y * sn[2 * i + 1]);
+        }
+    }
+}
+
+template <typename T2, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, int tile) {
+    __shared__ __align__(16) float s_cos[kMaxTokens][kMaxHalf], s_sin[kMaxTokens][kMaxHalf];
+    __shared__ int64_t s_row[kMaxTokens];
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * tile, nt = min(tile, a.T - t0);
+    const int half = a.rot >> 1, page_size = a.kv.page_size;
+    pdl_wait();
+    // one thread per token finds its slot and records its position there
+    if (tid < nt) {
+        const int t = t0 + tid;
+        const int s = seq_of_token(a.cu_seqlens, a.kv.num_seqs, t, a.T, a.kv.err);
+        int64_t row = -1;
+        if (s >= 0) {
+            const int end = a.cu_seqlens[s + 1];
+            const int kv = kv_len_of(a.kv, s, end - a.cu_seqlens[s]);
+            if (kv >= 0) {
+                const int slot = kv - (end - t), in_page = slot % page_size;
+                const int pg = page_of(a.kv, s, slot);
+                if (pg >= 0) {
+                    row = (int64_t)pg * a.kv.Hk * page_size + in_page;
+                    if (a.kv.pos) a.kv.pos[(int64_t)pg * page_size + in_page] = a.pos[t];
+                }
+            }
+        }
+        s_row[tid] = row;
+    }
+    for (int i = tid; i < nt * half; i += kThreads) {
+        const int tl = i / half, f = i - tl * half;
+        int ax = a.axes ? a.axes[f] : 0;
+        if (ax < 0 || ax >= a.num_axes) ax = 0;
+        float sn, cs;
+        sincospif(half_turns(a.inv_freq[f], a.pos[(int64_t)ax * a.T + t0 + tl]), &sn, &cs);
+        s_cos[tl][f] = cs;
+        s_sin[tl][f] = sn;
+    }
+    __syncthreads();
+    const int d = a.kv.d, Hq = a.Hq, Hk = a.kv.Hk;
+    const int upr = d >> 4, turned = a.rot >> 4;  // units of a row, those that turn
+    const int R = Hq + 2 * Hk;
+    const int total = nt * R * upr;
+    for (int base = tid; base < total; base += kThreads * kInFlight) {
+        uint4 x[kInFlight], y[kInFlight];
+        uint4 *dst[kInFlight];
+        int xo[kInFlight], yo[kInFlight], ang[kInFlight];
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            const int i = base + k * kThreads;
+            dst[k] = nullptr;
+            if (i < total) {
+                const int u = i % upr, pr = i / upr, tl = pr / R, r = pr - tl * R;
+                const int64_t t = t0 + tl;
+                const uint4 *src;
+                bool rot = u < turned;
+                if (r < Hq) {
+                    src = reinterpret_cast<const uint4 *>(
+                        static_cast<const uint16_t *>(a.q) + t * a.q_stride + (int64_t)r * d);
+                    dst[k] = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.q_out) +
+                                                       (t * Hq + r) * d);
+                } else {
+                    const bool is_k = r < Hq + Hk;
+                    const int j = r - Hq - (is_k ? 0 : Hk);
+                    src = reinterpret_cast<const uint4 *>(
+                        static_cast<const uint16_t *>(is_k ? a.k : a.v) +
+                        t * (is_k ? a.k_stride : a.v_stride) + (int64_t)j * d);
+                    if (s_row[tl] >= 0)
+                        dst[k] = reinterpret_cast<uint4 *>(
+                            static_cast<uint16_t *>(is_k ? a.kv.k : a.kv.v) +
+                            (s_row[tl] + (int64_t)j * page_size) * d);
+                    rot = rot && is_k;
+                }
+                const bool split = u < turned && !kInterleaved;
+                xo[k] = split ? u : 2 * u;
+                yo[k] = split ? u + turned : 2 * u + 1;
+                ang[k] = rot ? tl * kMaxHalf + 8 * u : -1;
+                x[k] = src[xo[k]];
+                y[k] = src[yo[k]];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kInFlight; ++k) {
+            if (!dst[k]) continue;
+            if (ang[k] >= 0) {
+                float cs[8], sn[8];
+                const float4 *c4 = reinterpret_cast<const float4 *>(&s_cos[0][0] + ang[k]);
+                const float4 *s4 = reinterpret_cast<const float4 *>(&s_sin[0][0] + ang[k]);
+                *reinterpret_cast<float4 *>(cs) = c4[0];
+                *reinterpret_cast<float4 *>(cs + 4) = c4[1];
+                *reinterpret_cast<float4 *>(sn) = s4[0];
+                *reinterpret_cast<float4 *>(sn + 4) = s4[1];
+                turn_unit<T2, kInterleaved>(x[k], y[k], cs, sn);
+            }
+            dst[k][xo[k]] = x[k];
+            dst[k][yo[k]] = y[k];
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t st) {
+    // tokens per block: a step's few tokens spread one to a block, a prompt's
+    // fill kMaxTokens once there are four blocks for every SM
+    int tile = a.T / (4 * num_sms);
+    tile = tile < 1 ? 1 : tile > kMaxTokens ? kMaxTokens : tile;
+    const unsigned grid = (unsigned)((a.T + tile - 1) / tile);
+    if (a.kv.fp16)
+        return a.interleaved
+                   ? launch_pdl(append_kernel<__half2, true>, dim3(grid), dim3(kThreads), 0, st, a, tile)
+                   : launch_pdl(append_kernel<__half2, false>, dim3(grid), dim3(kThreads), 0, st, a, tile);
+    return a.interleaved
+               ? launch_pdl(append_kernel<__nv_bfloat162, true>, dim3(grid), dim3(kThreads), 0, st, a, tile)
+               : launch_pdl(append_kernel<__nv_bfloat162, false>, dim3(grid), dim3(kThreads), 0, st, a, tile);
+}
+
+}  // namespace up

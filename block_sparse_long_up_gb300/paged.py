@@ -1,0 +1,279 @@
+"""Paged KV cache: append with rotary positions, attention of new tokens and
+decode attention over it (the paged-cache section of include/up.h).
+
+    cache = PagedKV(k_pages, v_pages, block_table, kv_lens, pos_pages)
+    q = append_kv(q, k, v, pos, cu_seqlens, cache, inv_freq)
+    out, lse = attend_paged(q, cu_seqlens, cache)       # a chunk of new tokens
+    out, lse = decode_attend(q, cache)                  # one new token per sequence
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+ROPE_INTERLEAVED = 0x1
+
+
+class _CKv(ctypes.Structure):
+    """up_paged_kv of include/up.h."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("pos_pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("Hk", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class _CLogits(ctypes.Structure):
+    """up_logits of include/up.h."""
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("slopes", ctypes.c_void_p), ("q_pos", ctypes.c_void_p)]
+
+
+def _up():
+    import block_sparse_long_up_gb300 as up
+    return up
+
+
+def _need(t, name, dtype, device, shape=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+class PagedKV:
+    """A paged KV-head-major cache: k_pages and v_pages [num_pages, Hk, page_size, d]
+    (bf16 or fp16), block_table int32 [num_seqs, max_pages], kv_lens int32
+    [num_seqs] (cached tokens, those of the current call included) and, where
+    positions matter, pos_pages int32 [num_pages, page_size].  Holds the tensors;
+    their contents may change between calls (an engine adds to kv_lens and to
+    block_table in place)."""
+
+    __slots__ = ("k_pages", "v_pages", "block_table", "kv_lens", "pos_pages", "num_seqs", "Hk",
+                 "d", "page_size", "dtype", "device", "_c", "_ref")
+
+    def __init__(self, k_pages, v_pages, block_table, kv_lens, pos_pages=None):
+        if not isinstance(k_pages, torch.Tensor):
+            raise TypeError("k_pages must be a torch.Tensor")
+        dt, dev = k_pages.dtype, k_pages.device
+        if dt not in DTYPES:
+            raise TypeError(f"k_pages must be bfloat16 or float16, got {dt}")
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [num_pages, Hk, page_size, d]")
+        _need(k_pages, "k_pages", dt, None)
+        _need(v_pages, "v_pages", dt, dev, k_pages.shape)
+        _need(block_table, "block_table", torch.int32, dev)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [num_seqs, max_pages]")
+        n, hk, ps, d = k_pages.shape
+        b, mp = block_table.shape
+        _need(kv_lens, "kv_lens", torch.int32, dev, (b,))
+        if pos_pages is not None:
+            _need(pos_pages, "pos_pages", torch.int32, dev, (n, ps))
+        self.k_pages, self.v_pages, self.pos_pages = k_pages, v_pages, pos_pages
+        self.block_table, self.kv_lens = block_table, kv_lens
+        self.num_seqs, self.Hk, self.d, self.page_size = b, hk, d, ps
+        self.dtype, self.device = dt, dev
+        self._c = _CKv(k_pages.data_ptr(), v_pages.data_ptr(),
+                       None if pos_pages is None else pos_pages.data_ptr(),
+                       block_table.data_ptr(), kv_lens.data_ptr(), n, b, mp, ps, hk, d,
+                       DTYPES[dt])
+        self._ref = ctypes.byref(self._c)
+
+
+def _on(stream):
+    """Allocations of a call on `stream` belong to that stream, so a workspace
+    freed on return is not handed to another stream's work while it is in use."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _raw(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _rows(t, name, cache, heads=None):
+    """Token stride of a [tokens, heads, d] tensor whose heads are adjacent (a view
+    of a fused projection is fine)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != cache.dtype:
+        raise TypeError(f"{name} must be {cache.dtype}, got {t.dtype}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, expected {cache.device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.d or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {cache.d}], got {tuple(shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != cache.d and shape[1] > 1):
+        raise ValueError(f"{name}'s heads must be adjacent")
+    return shape[1] * cache.d if shape[0] < 2 else st
+
+
+def append_kv(q, k, v, pos, cu_seqlens, cache, inv_freq, axes=None, interleaved=False, q_out=None,
+              stream=None):
+    """Rotates q and k by their positions, writes k, v and the positions to the
+    cache and returns the rotated q (see up_append_kv).
+
+    q [T, Hq, d] or None, k and v [T, Hk, d] (heads adjacent, any token stride that
+    is a multiple of 8); pos int32 [T] or [num_axes, T]; cu_seqlens int32
+    [num_seqs + 1] over the new tokens; cache a PagedKV whose kv_lens already count
+    them; inv_freq fp32 [rot_dim / 2] (None: no rotation); axes int32 [rot_dim / 2],
+    the row of pos that turns each frequency; interleaved: pairs (2i, 2i+1) instead
+    of (i, i + rot_dim/2); q_out [T, Hq, d] (q itself is allowed)."""
+    up = _up()
+    dev = cache.device
+    ks, vs = _rows(k, "k", cache, cache.Hk), _rows(v, "v", cache, cache.Hk)
+    T, Hq, qs = k.shape[0], 0, 0
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same tokens")
+    if q is not None:
+        qs = _rows(q, "q", cache)
+        Hq = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError("q and k must have the same tokens")
+    _need(pos, "pos", torch.int32, dev)
+    A = 1 if pos.dim() == 1 else pos.shape[0]
+    if pos.dim() not in (1, 2) or pos.shape[-1] != T or A < 1:
+        raise ValueError("pos must be [tokens] or [num_axes, tokens]")
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, (cache.num_seqs + 1,))
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, dev)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rot_dim / 2]")
+        rot = 2 * inv_freq.numel()
+    if axes is not None:
+        _need(axes, "axes", torch.int32, dev, (rot // 2,))
+    with _on(stream):
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty((T, Hq, cache.d), dtype=cache.dtype, device=dev)
+            elif q_out is not q:
+                _need(q_out, "q_out", cache.dtype, dev, q.shape)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        st = up.lib().up_append_kv(
+            None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            pos.data_ptr(), A, None if axes is None else axes.data_ptr(),
+            None if inv_freq is None else inv_freq.data_ptr(), rot,
+            ROPE_INTERLEAVED if interleaved else 0, cu_seqlens.data_ptr(), T, Hq, cache._ref,
+            None if q is None else q_out.data_ptr(), _raw(stream))
+    if st:
+        raise up.UpError("up_append_kv", st)
+    return q_out
+
+
+def _logits(cache, T, Hq, scale, softcap, slopes, q_pos):
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32, cache.device, (Hq,))
+        if q_pos is None or cache.pos_pages is None:
+            raise ValueError("slopes need q_pos and a cache with pos_pages")
+        _need(q_pos, "q_pos", torch.int32, cache.device, (T,))
+        return _CLogits(scale, softcap, slopes.data_ptr(), q_pos.data_ptr())
+    return _CLogits(scale, softcap, None, None)
+
+
+def _outputs(q, cache, out, lse):
+    T, Hq, d = q.shape
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=cache.dtype, device=cache.device)
+    else:
+        _need(out, "out", cache.dtype, cache.device, q.shape)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=cache.device)
+    else:
+        _need(lse, "lse", torch.float32, cache.device, (T, Hq))
+    return out, lse
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace
+
+
+def attend_paged_workspace(total_tokens, num_seqs, Hq, Hk, d) -> int:
+    return int(_up().lib().up_attend_paged_workspace(total_tokens, num_seqs, Hq, Hk, d))
+
+
+def decode_attend_workspace(num_seqs, Hq, Hk, d) -> int:
+    return int(_up().lib().up_decode_attend_workspace(num_seqs, Hq, Hk, d))
+
+
+def attend_paged(q, cu_seqlens, cache, scale=None, softcap=0.0, slopes=None, q_pos=None,
+                 visible=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of the new tokens q [T, Hq, d] (packed by cu_seqlens int32
+    [num_seqs + 1]) over the cache, which holds their own keys too; returns (out
+    [T, Hq, d], lse fp32 [T, Hq]).  See up_attend_paged.
+
+    scale (default d ** -0.5), softcap (0: none); slopes fp32 [Hq] with q_pos int32
+    [T]: a bias of -slope * |q_pos - key position|; visible int32 [T, 2]: the slots
+    [first, end) each query sees (default: causal)."""
+    up = _up()
+    dev = cache.device
+    if _rows(q, "q", cache) != q.shape[1] * cache.d:
+        raise ValueError("q must be contiguous")
+    T, Hq, d = q.shape
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, (cache.num_seqs + 1,))
+    lg = _logits(cache, T, Hq, d ** -0.5 if scale is None else scale, softcap, slopes, q_pos)
+    if visible is not None:
+        _need(visible, "visible", torch.int32, dev, (T, 2))
+    with _on(stream):
+        out, lse = _outputs(q, cache, out, lse)
+        L = up.lib()
+        need = L.up_attend_paged_workspace(T, cache.num_seqs, Hq, cache.Hk, d)
+        ws = _workspace(workspace, need, dev)
+        st = L.up_attend_paged(q.data_ptr(), cu_seqlens.data_ptr(), T, Hq, cache._ref,
+                               ctypes.byref(lg),
+                               None if visible is None else visible.data_ptr(), out.data_ptr(),
+                               lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                               _raw(stream))
+    if st:
+        raise up.UpError("up_attend_paged", st)
+    return out, lse
+
+
+def decode_attend(q, cache, scale=None, softcap=0.0, slopes=None, q_pos=None, kv_start=None,
+                  out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token per sequence, q [num_seqs, Hq, d], over the cache;
+    returns (out, lse fp32 [num_seqs, Hq]).  See up_decode_attend.  kv_start int32
+    [num_seqs]: the first visible slot of each sequence; the other arguments are
+    attend_paged's."""
+    up = _up()
+    dev = cache.device
+    if _rows(q, "q", cache) != q.shape[1] * cache.d:
+        raise ValueError("q must be contiguous")
+    B, Hq, d = q.shape
+    if B != cache.num_seqs:
+        raise ValueError(f"q must hold one token for each of the {cache.num_seqs} sequences")
+    lg = _logits(cache, B, Hq, d ** -0.5 if scale is None else scale, softcap, slopes, q_pos)
+    if kv_start is not None:
+        _need(kv_start, "kv_start", torch.int32, dev, (B,))
+    with _on(stream):
+        out, lse = _outputs(q, cache, out, lse)
+        L = up.lib()
+        need = L.up_decode_attend_workspace(B, Hq, cache.Hk, d)
+        ws = _workspace(workspace, need, dev)
+        st = L.up_decode_attend(q.data_ptr(), Hq, cache._ref, ctypes.byref(lg),
+                                None if kv_start is None else kv_start.data_ptr(),
+                                out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                ws.numel() * ws.element_size(), _raw(stream))
+    if st:
+        raise up.UpError("up_decode_attend", st)
+    return out, lse

@@ -64,6 +64,8 @@ typedef enum {
 #define UP_DEVERR_BAD_CU_BLOCKS 0x10u  /* compaction: cu_blocks[num_seqs] < 0 or > total_tokens/G + num_seqs */
 #define UP_DEVERR_BOUNDS 0x20u         /* checked builds only (compiled with -DUP_CHECK_BOUNDS): an index
                                           range outside its buffer; the access was skipped */
+#define UP_DEVERR_BAD_KV_LENS 0x40u    /* kv_lens[s] negative, below the sequence's new tokens, or above
+                                          max_pages * page_size (the sequence is left out) */
 
 /* Largest nb_s that the selection calls rank on chip (1M tokens at G = 64). */
 #define UP_SELECT_MAX_BLOCKS 16384
@@ -314,6 +316,150 @@ up_status up_compact_noalloc(const void *x, const int32_t *pos, int hidden,
                              const uint8_t *keep, const int32_t *cu_blocks, void *x_out,
                              int32_t *pos_out, int32_t *cu_seqlens_out, int32_t *src_idx,
                              int32_t *total_kept, up_stream_t stream);
+
+/*
+ * Paged KV cache: the cache that up_score_blocks_paged reads its keys from, with
+ * the values and (optionally) the token positions beside them.
+ *
+ * Slot i of sequence s (0 <= i < kv_lens[s]) is row i % page_size of page
+ * block_table[s * max_pages + i / page_size].
+ *   k_pages, v_pages  dtype [num_pages, Hk, page_size, d], 16-byte aligned.
+ *   pos_pages    int32 [num_pages, page_size] or NULL: the position of the token
+ *                in each slot (a compacted batch's slots are denser than its
+ *                positions).  up_append_kv writes it; a distance bias reads it.
+ *   block_table  int32 [num_seqs * max_pages]; entries past a sequence's pages
+ *                are not read.  A page index outside [0, num_pages) sets
+ *                UP_DEVERR_BAD_PAGE: nothing is written there, and its keys,
+ *                values and positions read as zeros.
+ *   kv_lens      int32 [num_seqs]: cached tokens of each sequence, the tokens of
+ *                the current call included.  A length outside [new tokens,
+ *                max_pages * page_size] sets UP_DEVERR_BAD_KV_LENS: the sequence
+ *                is not appended to, and its attention output rows are those of
+ *                an empty mask.
+ *   page_size    a positive multiple of 16 (128 where up_score_blocks_paged reads
+ *                the pages too).
+ *   d            64, 128 or 256.
+ *   dtype        UP_BF16 or UP_FP16 (queries and outputs have the same type).
+ * The struct is read on the host during the call; the caller keeps it.
+ */
+typedef enum { UP_BF16 = 0, UP_FP16 = 1 } up_dtype;
+
+typedef struct {
+    void *k_pages;
+    void *v_pages;
+    int32_t *pos_pages;
+    const int32_t *block_table;
+    const int32_t *kv_lens;
+    int64_t num_pages;
+    int32_t num_seqs;
+    int32_t max_pages;
+    int32_t page_size;
+    int32_t Hk;
+    int32_t d;
+    int32_t dtype; /* up_dtype */
+} up_paged_kv;
+
+/*
+ * Append: rotates the new tokens' queries and keys by their positions and writes
+ * keys, values and positions to the cache, in one kernel.
+ *
+ * Token t of sequence s (cu_seqlens[s] <= t < cu_seqlens[s+1]) goes to slot
+ * kv_lens[s] - (cu_seqlens[s+1] - t).  Frequency i < rot_dim/2 turns its pair of
+ * dims by the angle pos[axes[i] * total_tokens + t] * inv_freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * where (a, b) are dims (i, i + rot_dim/2), or (2i, 2i+1) with
+ * UP_ROPE_INTERLEAVED; dims from rot_dim on are copied.  The angle is reduced
+ * exactly (in 2^-64 turns) before its sine and cosine, so far positions lose
+ * nothing.
+ *
+ *   q, k, v    dtype [total_tokens, Hq | Hk | Hk, d] with token strides q_stride,
+ *              k_stride, v_stride in elements (views of a fused projection are
+ *              fine); heads are adjacent.  16-byte aligned, strides multiples of
+ *              8 and at least the heads' elements.  Hq = 0 with q = q_out = NULL
+ *              appends only.
+ *   pos        int32 [num_axes, total_tokens]; pos_pages receives axis 0.
+ *   axes       int32 [rot_dim/2] in [0, num_axes), or NULL (all 0); an entry
+ *              outside counts as axis 0.
+ *   inv_freq   fp32 [rot_dim/2], radians per position; NULL when rot_dim = 0.
+ *   rot_dim    0, or a multiple of 16 up to d.
+ *   q_out      dtype [total_tokens, Hq, d] contiguous; may be q itself when
+ *              q_stride = Hq * d.
+ * The tokens' pages must not be shared between sequences.  Errors:
+ * UP_ERR_INVALID_ARG for null pointers, sizes, strides or alignments outside the
+ * above; UP_ERR_UNSUPPORTED for a d or dtype outside the cache's list.
+ */
+#define UP_ROPE_INTERLEAVED 0x1u
+
+up_status up_append_kv(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                       const void *v, int64_t v_stride, const int32_t *pos, int num_axes,
+                       const int32_t *axes, const float *inv_freq, int rot_dim, uint32_t flags,
+                       const int32_t *cu_seqlens, int64_t total_tokens, int Hq,
+                       const up_paged_kv *cache, void *q_out, up_stream_t stream);
+
+/*
+ * How attention turns a query-key product into a logit, and what a query sees.
+ *   scale     logits are scale * (q . k) ...
+ *   softcap   ... then softcap * tanh(logit / softcap) when softcap > 0 ...
+ *   slopes    fp32 [Hq] or NULL: ... then minus slopes[h] * |q_pos - pos_pages|
+ *             (needs q_pos and the cache's pos_pages) ...
+ *   q_pos     int32 [queries] or NULL.
+ * Softmax is over the visible slots only; a query that sees none gives zeros and
+ * a log-sum of -infinity.  What is stored in slots from kv_lens[s] on, and in
+ * pages that no visible slot names, has no effect, infinities and NaN included.
+ */
+typedef struct {
+    float scale;
+    float softcap;
+    const float *slopes;
+    const int32_t *q_pos;
+} up_logits;
+
+/*
+ * Attention of new tokens over the paged cache (chunked prefill; the cache
+ * already holds the new tokens' own keys and values).
+ *
+ *   q        dtype [total_tokens, Hq, d], the new tokens of every sequence, packed
+ *            by cu_seqlens (int32 [num_seqs+1]); Hq % Hk == 0, Hq/Hk <= 16; query
+ *            head h reads KV head h / (Hq/Hk).
+ *   visible  int32 [total_tokens, 2] or NULL: query t sees slots visible[t][0] <= i
+ *            < visible[t][1], cut to [0, kv_lens[s]): windows, packed documents and
+ *            bidirectional prefixes are such ranges.  NULL: causal, slots up to the
+ *            token's own.
+ *   out      dtype [total_tokens, Hq, d].
+ *   lse      fp32 [total_tokens, Hq] or NULL: natural log of the softmax's sum.
+ *   workspace  up_attend_paged_workspace(...) bytes, 256-byte aligned; its contents
+ *            on entry do not matter.
+ * A cached value that some query of the call may not see but another one may
+ * has to be finite (its zero weight multiplies it).  Results are deterministic.
+ * Errors: as above; UP_ERR_INVALID_ARG for slopes without q_pos or pos_pages, a
+ * softcap below 0 or a non-finite scale or softcap.
+ */
+size_t up_attend_paged_workspace(int64_t total_tokens, int num_seqs, int Hq, int Hk, int d);
+
+up_status up_attend_paged(const void *q, const int32_t *cu_seqlens, int64_t total_tokens, int Hq,
+                          const up_paged_kv *cache, const up_logits *logits,
+                          const int32_t *visible, void *out, float *lse, void *workspace,
+                          size_t workspace_bytes, up_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the paged cache (decode): every
+ * sequence's length is split over the GPU and the parts are joined.
+ *
+ *   q         dtype [num_seqs, Hq, d].
+ *   kv_start  int32 [num_seqs] or NULL: the first visible slot (a sliding window);
+ *             the query sees slots max(kv_start[s], 0) .. kv_lens[s] - 1.
+ *             A length of 0 (an idle row of the batch) is fine and sees none.
+ *   out, lse  as in up_attend_paged, [num_seqs, Hq, d] and [num_seqs, Hq].
+ *   workspace up_decode_attend_workspace(...) bytes, 256-byte aligned; its contents
+ *             on entry do not matter.
+ * What is stored in a slot that the query does not see has no effect.
+ */
+size_t up_decode_attend_workspace(int num_seqs, int Hq, int Hk, int d);
+
+up_status up_decode_attend(const void *q, int Hq, const up_paged_kv *cache,
+                           const up_logits *logits, const int32_t *kv_start, void *out,
+                           float *lse, void *workspace, size_t workspace_bytes,
+                           up_stream_t stream);
 
 /*
  * Instrumentation: when both events are non-NULL, every later scoring call
