@@ -20,7 +20,7 @@ up_status check_cache(const up_paged_kv *c, int Hq_multiple_of) {
     // page indexes, and the rows of one page over all heads, are 32-bit
     if (c->num_pages > INT32_MAX || (int64_t)c->Hk * c->page_size > INT32_MAX)
         return UP_ERR_INVALID_ARG;
-    if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->pos_pages, 4) ||
+    if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->pos_pages, 16) ||
         !aligned(c->block_table, 4) || !aligned(c->kv_lens, 4))
         return UP_ERR_INVALID_ARG;
     if (c->d != 64 && c->d != 128 && c->d != 256) return UP_ERR_UNSUPPORTED;

@@ -101,12 +101,8 @@ cudaError_t launch_rows(const AttendArgs &a, cudaStream_t st) {
 }  // namespace
 
 size_t attend_workspace(int64_t, int, int, int, int) { return 256; }
-size_t decode_workspace(int, int, int, int) { return 256; }
 
 cudaError_t launch_attend(const AttendArgs &a, int, cudaStream_t st) {
-    return a.kv.fp16 ? launch_rows<true>(a, st) : launch_rows<false>(a, st);
-}
-cudaError_t launch_decode(const AttendArgs &a, int, cudaStream_t st) {
     return a.kv.fp16 ? launch_rows<true>(a, st) : launch_rows<false>(a, st);
 }
 

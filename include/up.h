@@ -324,8 +324,8 @@ up_status up_compact_noalloc(const void *x, const int32_t *pos, int hidden,
  * Slot i of sequence s (0 <= i < kv_lens[s]) is row i % page_size of page
  * block_table[s * max_pages + i / page_size].
  *   k_pages, v_pages  dtype [num_pages, Hk, page_size, d], 16-byte aligned.
- *   pos_pages    int32 [num_pages, page_size] or NULL: the position of the token
- *                in each slot (a compacted batch's slots are denser than its
+ *   pos_pages    int32 [num_pages, page_size], 16-byte aligned, or NULL: the position
+ *                of the token in each slot (a compacted batch's slots are denser than its
  *                positions).  up_append_kv writes it; a distance bias reads it.
  *   block_table  int32 [num_seqs * max_pages]; entries past a sequence's pages
  *                are not read.  A page index outside [0, num_pages) sets
