@@ -20,7 +20,8 @@
 // the 16 rows: at g = 16 they need 109 TFLOP/s at the full memory rate, far
 // below what that instruction reaches, so the wider tensor-core path with its
 // 128 rows has nothing to give here.  The weights are split into a high and a low
-// part of the cache's type, two products each, so rounding them costs nothing.
+// part of the cache's type, two products each, so rounding them costs nothing (up
+// to 8 heads: the low parts are the fragment's other 8 rows, in the same product).
 #include "paged.cuh"
 #include "sm100.cuh"
 
@@ -312,15 +313,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
             __syncwarp();
             load(step + C::kStages - 1);
             const uint32_t st = ring + (step % C::kStages) * C::kStageBytes;
-            float x[2][4] = {};
+            float x[2][4] = {}, x2[2][4] = {};  // two chains of products each
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint32_t b[4];
                 const int r = ((lane >> 4) << 3) + (lane & 7), c = 2 * kk + ((lane >> 3) & 1);
                 ldsm4(st + r * C::kRowBytes + ((c ^ (r & 7)) << 4), b);
-                mma16816<kFp16>(x[0], q[kk], b[0], b[1]);
-                mma16816<kFp16>(x[1], q[kk], b[2], b[3]);
+                mma16816<kFp16>((kk & 1) ? x2[0] : x[0], q[kk], b[0], b[1]);
+                mma16816<kFp16>((kk & 1) ? x2[1] : x[1], q[kk], b[2], b[3]);
             }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 2 * kR; ++i) x[n][i] += x2[n][i];
             const int key = key_a + step * kTile;
             // logits in log2 units
 #pragma unroll
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2 * kR; ++i) o[n][i] *= c[i >> 1];
+                    for (int i = 0; i < 4; ++i) o[n][i] *= c[kFew ? 0 : i >> 1];
             }
             uint32_t hi[4] = {}, lo[4] = {};
 #pragma unroll
@@ -385,10 +390,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
                 uint32_t b[4];
                 const int r = (((lane >> 3) & 1) << 3) + (lane & 7), c8 = 2 * n + (lane >> 4);
                 ldsm4t(st + C::kHalfBytes + r * C::kRowBytes + ((c8 ^ (r & 7)) << 4), b);
-                mma16816<kFp16>(o[2 * n], hi, b[0], b[1]);
-                mma16816<kFp16>(o[2 * n + 1], hi, b[2], b[3]);
-                mma16816<kFp16>(o[2 * n], lo, b[0], b[1]);
-                mma16816<kFp16>(o[2 * n + 1], lo, b[2], b[3]);
+                if constexpr (kFew) {
+                    const uint32_t both[4] = {hi[0], lo[0], hi[2], lo[2]};
+                    mma16816<kFp16>(o[2 * n], both, b[0], b[1]);
+                    mma16816<kFp16>(o[2 * n + 1], both, b[2], b[3]);
+                } else {
+                    mma16816<kFp16>(o[2 * n], hi, b[0], b[1]);
+                    mma16816<kFp16>(o[2 * n + 1], hi, b[2], b[3]);
+                    mma16816<kFp16>(o[2 * n], lo, b[0], b[1]);
+                    mma16816<kFp16>(o[2 * n + 1], lo, b[2], b[3]);
+                }
             }
             __syncwarp();
         }
@@ -408,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)
                 *reinterpret_cast<float2 *>(o_f + (warp * 16 + row + 8 * r) * D + 8 * n + col) =
-                    make_float2(o[n][2 * r], o[n][2 * r + 1]);
+                    kFew ? make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3])
+                         : make_float2(o[n][2 * r], o[n][2 * r + 1]);
         }
         __syncthreads();
         const bool whole = ta == 0 && tb == sp.tiles;
@@ -455,7 +467,8 @@ constexpr int kJoinThreads = 128;
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const AttendArgs a, int grid) {
     __shared__ long long s_scan[kJoinThreads / 32];
-    __shared__ float s_w[2 * kMaxSms * kMaxPerSm];
+    __shared__ float s_w[kMaxSms * kMaxPerSm];
+    __shared__ float4 s_o[kJoinThreads * 4 / D][D / 4];
     const int h = blockIdx.x % a.Hq, s = blockIdx.x / a.Hq;
     const int j = h / a.g, r = h - j * a.g;
     // the lengths are the caller's, older than the kernel before; only the parts are not
@@ -475,27 +488,46 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const AttendA
     const int64_t unit = before + (int64_t)j * sp.tiles;
     const int c0 = share_of(sh, unit), c1 = share_of(sh, unit + sp.tiles - 1);
     if (c0 == c1) return;  // finished by its block
-    // a block's first part is in its slot 0, a later one (this unit's first) in slot 1
-    auto part = [&](int c) { return part_of(a, D, 2 * c + (share_begin(sh, c) < unit)); };
     const int n = c1 - c0 + 1;
-    float M = -INFINITY;
-    for (int i = 0; i < n; ++i) M = fmaxf(M, part(c0 + i)[2 * r]);
+    // a block's first part is in its slot 0, a later one (this unit's first) in slot 1
+    const int slot0 = 2 * c0 + (share_begin(sh, c0) < unit);
+    auto part = [&](int i) { return part_of(a, D, i == 0 ? slot0 : 2 * (c0 + i)); };
+    const int lane = tid & 31;
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[2 * r]);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
     const float ref = M == -INFINITY ? 0.f : M;
-    for (int i = tid; i < n; i += kJoinThreads) s_w[i] = exp2f(part(c0 + i)[2 * r] - ref);
-    __syncthreads();
-    float L = 0.f;
-    for (int i = 0; i < n; ++i) L = fmaf(s_w[i], part(c0 + i)[2 * r + 1], L);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    for (int c = tid; c < D / 4; c += kJoinThreads) {
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < n; ++i) {
-            const float4 v = *reinterpret_cast<const float4 *>(part(c0 + i) + 4 * a.g + r * D + 4 * c);
-            const float e = s_w[i];
-            O.x = fmaf(e, v.x, O.x); O.y = fmaf(e, v.y, O.y);
-            O.z = fmaf(e, v.z, O.z); O.w = fmaf(e, v.w, O.w);
-        }
-        store_row4<kFp16>(a.out, orow * D + 4 * c, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+    for (int i = lane; i < n; i += 32) {
+        const float2 ml = *reinterpret_cast<const float2 *>(part(i) + 2 * r);
+        const float e = exp2f(ml.x - ref);
+        if (tid < 32) s_w[i] = e;
+        L = fmaf(e, ml.y, L);
     }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
+    __syncthreads();
+    // kRows rows of threads take every kRows-th part each, D/4 threads a row
+    constexpr int kCols = D / 4, kRows = kJoinThreads / kCols;
+    const int c = tid % kCols, i0 = tid / kCols;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = i0; i < n; i += kRows) {
+        const float4 v = *reinterpret_cast<const float4 *>(part(i) + 4 * a.g + r * D + 4 * c);
+        const float e = s_w[i];
+        O.x = fmaf(e, v.x, O.x); O.y = fmaf(e, v.y, O.y);
+        O.z = fmaf(e, v.z, O.z); O.w = fmaf(e, v.w, O.w);
+    }
+    if (i0) s_o[i0 - 1][c] = O;
+    __syncthreads();
+    if (i0) return;
+#pragma unroll
+    for (int k = 1; k < kRows; ++k) {
+        const float4 v = s_o[k - 1][c];
+        O.x += v.x; O.y += v.y; O.z += v.z; O.w += v.w;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    store_row4<kFp16>(a.out, orow * D + 4 * c, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
     if (a.lse && tid == 0) a.lse[orow] = (ref + log2f(L)) * kLn2;
 }
 
