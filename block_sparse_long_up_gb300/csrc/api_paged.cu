@@ -17,8 +17,9 @@ up_status check_cache(const up_paged_kv *c, int Hq_multiple_of) {
     if (c->num_seqs > 0 &&
         (!c->k_pages || !c->v_pages || !c->block_table || !c->kv_lens || c->num_pages < 1))
         return UP_ERR_INVALID_ARG;
-    // page indexes, and the rows of one page over all heads, are 32-bit
-    if (c->num_pages > INT32_MAX || (int64_t)c->Hk * c->page_size > INT32_MAX)
+    // page indexes, the rows of one page over all heads and the heads of all pages are 32-bit
+    if (c->num_pages > INT32_MAX || (int64_t)c->Hk * c->page_size > INT32_MAX ||
+        c->num_pages * c->Hk >= INT32_MAX)
         return UP_ERR_INVALID_ARG;
     if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->pos_pages, 16) ||
         !aligned(c->block_table, 4) || !aligned(c->kv_lens, 4))

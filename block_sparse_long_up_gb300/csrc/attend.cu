@@ -1,109 +1,1050 @@
-// attend.cu -- attention over the paged cache, the plainest form: one warp per
-// (new token, query head).  A lane holds d/32 dims of the query and of the
-// output; each visible slot costs one product summed over the warp, and the
-// softmax's maximum and sum run along (everything in fp32, one rounding at the
-// end).  Reads the keys once per query head, so the cache's bandwidth and the
-// shuffles bound it.
-#include "paged.cuh"
+// attend.cu -- attention of new tokens over the paged cache on the sm_103a tensor
+// cores (tcgen05 + TMEM + TMA).
+//
+// out = softmax(logits) V with 4*d flops for every visible (query head, query, slot):
+// the tensor cores bound a chunk or a prompt, the cache's bandwidth or latency a few
+// tokens.  One pass over the keys with a running maximum and sum, the logits and
+// weights never leave the SM.
+//
+// The g query heads of a KV head and 128/g consecutive tokens are the 128 rows of a
+// tile (row = token * g + head), so a key tile in shared memory serves the whole
+// group.  A unit is two tiles (256 rows) of one sequence and KV head, one tile at
+// head_dim 256, against the key tiles of 128 slots that any of its rows sees.  A
+// plan kernel lists the units with their key tiles; all key tiles of all units and
+// KV heads are laid end to end and block c of the grid (one per SM) takes the c-th
+// equal share, so causal, windowed, ragged and few-row batches load every SM alike
+// without the host knowing a length.  A unit cut by a share's end leaves its
+// running maximum, sum and unnormalised output in the workspace for the join kernel
+// (fixed order: results are reproducible); a whole unit is written by its block.
+//
+// Roles of a block:
+//   warp 0      keys and values, TMA into a ring (boxes of the largest power of two
+//               up to 128 that divides the page size, so pages may end inside a tile);
+//   warp 2      queries, TMA, one 3-D box per tile and 64 dims;
+//   warps 1, 3  MMA issuers.  Two tiles: each issues its tile's products, S = Q K^T
+//               then O += P V with P read from TMEM.  One tile: warp 1 the
+//               former, warp 3 the latter, with two S buffers.  Two instruction
+//               streams alternate accumulators, which is what the tensor pipe needs
+//               for its full rate;
+//   warps 4-11  two softmax warpgroups, one per tile (4-7 at head_dim 256).  Thread =
+//               row.  It holds the row's 128 logits in registers, writes the weights
+//               over them in TMEM, and rescales its output row there only when the
+//               maximum has grown by more than 2^8 (weights then stay below 2^8, far
+//               inside both types and fp32), which after the first tiles is rare.
+#include "attend.cuh"
+#include "tma_host.cuh"
 
 namespace up {
 
 namespace {
 
-constexpr int kWarps = 8;
+using namespace sm100;
 
-template <bool kFp16>
-__device__ __forceinline__ float load1(const void *p, int64_t i) {
-    if constexpr (kFp16) return __half2float(static_cast<const __half *>(p)[i]);
-    else return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+constexpr int kRows = 128;        // rows of a tile, keys of a step
+constexpr int kMinTiles = 4;      // shares are not cut finer than this
+constexpr float kSlack = 8.f;     // log2: how far the maximum may grow before a rescale
+constexpr int kPanel = 128 * 128; // 128 rows x 64 elements
+
+template <int D>
+struct Cfg {
+    static constexpr int kTiles = D == 256 ? 1 : 2;
+    static constexpr int kThreads = 128 * (1 + kTiles);
+    static constexpr int kStageDims = D < 128 ? D : 128;          // dims of one ring stage
+    static constexpr int kStagePanels = kStageDims / 64;
+    static constexpr int kStageBytes = kStagePanels * kPanel;
+    static constexpr int kParts = D / kStageDims;                 // stages of a key (value) tile
+    static constexpr int kQTile = D / 64 * kPanel;
+    static constexpr int kQBytes = kTiles * kQTile;
+    static constexpr int kStages = D == 64 ? 8 : 5;
+    static constexpr int kPosBytes = kTiles * 2 * 128 * 4;        // two steps' key positions
+    static constexpr int kPad = 512;  // dynamic shared memory begins at a multiple of 1024 (checked)
+    static constexpr int kSmem = kQBytes + kStages * kStageBytes + kPosBytes + 512 + kPad;
+    static constexpr int kOutCol = 256;                           // S: columns 0..255
+    static constexpr int kUnitRows = kTiles * kRows;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kOutCol + kTiles * D <= 512, "tensor memory");
+};
+
+struct Unit {
+    int s, tok0, ntok;  // sequence, first token (of the batch), tokens
+    int kt0, tiles;     // first key tile and how many
+    int hi0;            // causal end of the first token's slots
+    int kv;             // cached tokens of the sequence
+    int pad;
+    int64_t prefix;     // tiles of the units before this one
+};
+struct Plan {
+    int64_t W;  // tiles of one KV head
+    int units;
+    int pad;
+};
+
+struct Layout {
+    size_t seq_off, units, parts, total;
+    int64_t max_units;
+};
+Layout layout_of(int64_t T, int num_seqs, int Hq, int Hk, int d) {
+    Layout L{};
+    const int g = Hq / Hk, tiles = d == 256 ? 1 : 2, tpu = tiles * (kRows / g);
+    L.max_units = T / tpu + num_seqs;
+    size_t off = 256;
+    auto take = [&](size_t n) { const size_t at = off; off = (off + n + 255) & ~size_t(255); return at; };
+    L.seq_off = take(sizeof(int32_t) * (size_t)(num_seqs + 1));
+    L.units = take(sizeof(Unit) * (size_t)(L.max_units > 0 ? L.max_units : 1));
+    L.parts = take((size_t)2 * kMaxSms * tiles * kRows * (size_t)(d + 4) * sizeof(float));
+    L.total = off;
+    return L;
 }
 
-template <bool kFp16, int kD>
-__global__ void attend_rows_kernel(const AttendArgs a) {
-    constexpr int kE = kD / 32;
+struct Params {
+    AttendArgs a;
+    Plan *plan;
+    int32_t *seq_off;
+    Unit *units;
+    float *parts;
+    int64_t max_units;
+    int tpt;       // tokens of a tile
+    int box;       // rows of a key box
+    int grid;
+};
+
+// ---------------------------------------------------------------- the plan
+
+// [lo, hi) of token t: tl tokens behind the unit's first one.
+__device__ __forceinline__ int2 sees(const AttendArgs &a, const Unit &u, int tl) {
+    if (!a.visible) return make_int2(0, u.hi0 + tl);
+    const int2 v = reinterpret_cast<const int2 *>(a.visible)[u.tok0 + tl];
+    const int lo = max(v.x, 0), hi = min(v.y, u.kv);
+    return lo < hi ? make_int2(lo, hi) : make_int2(INT32_MAX, 0);
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive scan of one value a thread over the block; *total gets the sum.
+__device__ int64_t block_scan(int64_t v, int64_t *total, int64_t *sh) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int64_t inc = v;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, inc, k);
+        if (lane >= k) inc += y;
+    }
+    if (lane == 31) sh[w] = inc;
+    __syncthreads();
+    if (w == 0) {
+        int64_t x = lane < (int)(blockDim.x >> 5) ? sh[lane] : 0;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, k);
+            if (lane >= k) x += y;
+        }
+        sh[lane] = x;
+    }
+    __syncthreads();
+    const int64_t before = (w ? sh[w - 1] : 0) + inc - v;
+    *total = sh[(blockDim.x >> 5) - 1];
+    __syncthreads();
+    return before;
+}
+
+// Lists the units (one block): sequences' unit counts and their scan, then every
+// unit's key tiles (a warp looks at its tokens' ranges) and their scan.
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params p, int tpu) {
+    __shared__ int64_t sh[32];
+    __shared__ int bad;
+    const AttendArgs &a = p.a;
+    const int B = a.kv.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) bad = 0;
     pdl_wait();
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.T * a.Hq) return;
-    const int lane = threadIdx.x & 31, h = (int)(row % a.Hq), t = (int)(row / a.Hq);
-    const int j = h / a.g;
-    int s = t, fresh = 0, back = 1;  // back: tokens of the sequence from this one on
-    if (a.cu_seqlens) {
-        s = seq_of_token(a.cu_seqlens, a.kv.num_seqs, t, a.T, a.kv.err);
-        if (s >= 0) {
-            fresh = a.cu_seqlens[s + 1] - a.cu_seqlens[s];
-            back = a.cu_seqlens[s + 1] - t;
+    pdl_trigger();  // what came before is complete: the main kernel's set-up may overlap
+    __syncthreads();
+    int64_t units = 0;
+    for (int s0 = 0; s0 < B; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int64_t n = 0;
+        if (s < B) {
+            const int c0 = a.cu_seqlens[s], c1 = a.cu_seqlens[s + 1];
+            if (c0 < 0 || c1 < c0 || c1 > a.T || (s == 0 && c0 != 0) || (s == B - 1 && c1 != a.T)) bad = 1;
+            else n = (c1 - c0 + tpu - 1) / tpu;
+        }
+        int64_t total;
+        const int64_t at = units + block_scan(n, &total, sh);
+        if (s < B) p.seq_off[s] = (int)(at < p.max_units ? at : p.max_units);
+        units += total;
+    }
+    __syncthreads();
+    if (bad || units > p.max_units) {  // a malformed cu_seqlens: nothing is computed
+        if (tid == 0) {
+            atomicOr(a.kv.err, kErrCuSeqlens);
+            *p.plan = Plan{0, 0, 0};
+        }
+        return;
+    }
+    for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads / 32) {
+        const int64_t i = u0 + warp;
+        if (i >= units) continue;
+        int lo = 0, hi = B - 1;  // the last sequence with seq_off <= i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.seq_off[mid] <= i) lo = mid; else hi = mid - 1;
+        }
+        const int c0 = a.cu_seqlens[lo], c1 = a.cu_seqlens[lo + 1];
+        Unit u{};
+        u.s = lo;
+        u.tok0 = c0 + (int)(i - p.seq_off[lo]) * tpu;
+        u.ntok = min(tpu, c1 - u.tok0);
+        const int kv = kv_len_of(a.kv, lo, c1 - c0);
+        u.kv = kv;
+        u.hi0 = kv - (c1 - u.tok0) + 1;
+        int first = INT32_MAX, end = 0;
+        if (kv >= 0) {
+            if (!a.visible) {
+                first = 0;
+                end = u.hi0 + u.ntok - 1;
+            } else {
+                for (int t = lane; t < u.ntok; t += 32) {
+                    const int2 r = sees(a, u, t);
+                    first = min(first, r.x);
+                    end = max(end, r.y);
+                }
+#pragma unroll
+                for (int k = 16; k; k >>= 1) {
+                    first = min(first, __shfl_xor_sync(0xffffffffu, first, k));
+                    end = max(end, __shfl_xor_sync(0xffffffffu, end, k));
+                }
+            }
+        }
+        if (first < end) {
+            u.kt0 = first / kRows;
+            u.tiles = (end + kRows - 1) / kRows - u.kt0;
+        }
+        if (lane == 0) p.units[i] = u;
+    }
+    __syncthreads();
+    int64_t W = 0;
+    for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
+        const int64_t i = u0 + tid;
+        int64_t total;
+        const int64_t at = block_scan(i < units ? p.units[i].tiles : 0, &total, sh);
+        if (i < units) p.units[i].prefix = W + at;
+        W += total;
+    }
+    if (tid == 0) *p.plan = Plan{W, (int)units, 0};
+}
+
+// The unit holding tile x (0 <= x < W) of a KV head.
+__device__ __forceinline__ int find_unit(const Unit *units, int n, int64_t x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (units[mid].prefix <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// A block's share, piece by piece: the part of a (KV head, unit) that lies in it.
+struct Pieces {
+    const Params &p;
+    Shares sh;
+    int64_t W1, at, end;
+    int j, ui, n;        // KV head, unit index, units
+    int64_t base;        // tiles of the KV heads before j
+    Unit u;
+    int ta, tb;          // tiles [ta, tb) of the unit
+    int64_t index = -1;  // pieces so far, less one
+
+    __device__ explicit Pieces(const Params &pp) : p(pp) {
+        const Plan pl = *pp.plan;
+        W1 = pl.W;
+        n = pl.units;
+        at = end = 0;
+        if (W1 == 0) return;
+        sh = shares_of(W1 * pp.a.kv.Hk, pp.grid, kMinTiles);
+        if ((int)blockIdx.x >= sh.n) return;
+        at = share_begin(sh, blockIdx.x);
+        end = share_begin(sh, blockIdx.x + 1);
+        j = (int)(at / W1);
+        base = (int64_t)j * W1;
+        ui = find_unit(pp.units, n, at - base);
+    }
+    __device__ bool next() {
+        if (at >= end) return false;
+        u = p.units[ui];
+        while (at - base >= u.prefix + u.tiles) {  // units without tiles, or the last one done
+            if (++ui == n) {
+                ui = 0;
+                ++j;
+                base += W1;
+            }
+            u = p.units[ui];
+        }
+        ta = (int)(at - base - u.prefix);
+        tb = (int)min((int64_t)u.tiles, end - base - u.prefix);
+        at += tb - ta;
+        ++index;
+        return true;
+    }
+    __device__ int steps() const { return tb - ta; }
+    __device__ int tiles_used() const { return u.ntok > p.tpt ? 2 : 1; }  // row tiles with tokens
+    __device__ int key0(int t) const { return (u.kt0 + ta + t) * kRows; }
+};
+
+// ---------------------------------------------------------------- shared state
+
+constexpr int kMaxStages = 8;
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages];  // the ring
+    uint64_t qfull, qempty;
+    // S buffers: one set of barriers for pieces of one row tile, one for those of two
+    uint64_t sfull[2][2];   // the buffer holds logits
+    uint64_t pfull[2][2];   // the buffer holds weights
+    uint64_t pdone[2][2];   // the weights have been multiplied into O
+    uint64_t pos[2];     // a warpgroup's key positions are in shared memory
+    uint64_t fin[2];
+    uint32_t tmem;
+    int abort;
+};
+
+// Uses of the S buffers by all pieces so far: every role walks the same pieces and
+// counts them alike, so barrier parities need no talk.  A parity tells a phase from
+// its neighbours only: whoever waits for a use must know that the one before it is
+// over.  So the second softmax warpgroup, which has no part in pieces of one row
+// tile, shares no barrier with them.
+struct Uses {
+    uint32_t two = 0, one[2] = {0, 0};
+    __device__ void add(int steps, int tiles_used) {
+        if (tiles_used == 2) {
+            two += steps;
+        } else {
+            one[0] += (steps + 1) / 2;
+            one[1] += steps / 2;
         }
     }
-    const int kv = s >= 0 ? kv_len_of(a.kv, s, fresh) : -1;
-    int lo = 0, hi = 0;
-    if (kv >= 0) {
-        hi = kv - back + 1;
-        if (a.kv_start) lo = max(a.kv_start[s], 0);
-        if (a.visible) {
-            lo = max(a.visible[2 * (int64_t)t], 0);
-            hi = min(a.visible[2 * (int64_t)t + 1], kv);
+    // buffer and parity of its use by step t of row tile e
+    __device__ int buf(int t, int e, int tiles_used) const { return tiles_used == 2 ? e : (t & 1); }
+    __device__ uint32_t par(int t, int tiles_used) const {
+        return (tiles_used == 2 ? two + t : one[t & 1] + (t >> 1)) & 1u;
+    }
+};
+
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > 4000000000LL) break;
+}
+
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
+    // MN-major operand (rows of 64 elements along N, one row per k): 8-row groups
+    // 1024 bytes apart, the next 64 elements of N one panel on
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((uint32_t)kPanel >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__host__ __device__ constexpr uint32_t idesc_f32(bool fp16, int M, int N, bool b_mn_major) {
+    return (1u << 4) | ((fp16 ? 0u : 1u) << 7) | ((fp16 ? 0u : 1u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], issued by one thread.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b),
+        "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+        "%13, %14, %15, %16};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+        "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- roles
+
+// One key or value tile into ring stages it, it+1, ... (kParts of them).
+template <int D>
+__device__ bool load_tile(const CUtensorMap *map, const Params &p, Shared &sh, uint32_t ring, uint32_t &it,
+                          const Pieces &w, int key0) {
+    using C = Cfg<D>;
+    const AttendArgs &a = p.a;
+#pragma unroll 1
+    for (int part = 0; part < C::kParts; ++part, ++it) {
+        const int st = it % C::kStages;
+        if (!mbar_wait(smem_u32(&sh.empty[st]), ((it / C::kStages) & 1) ^ 1, &sh.abort, a.wait_limit)) return false;
+        const uint32_t bar = smem_u32(&sh.full[st]);
+        mbar_arrive_expect_tx(bar, C::kStageBytes);
+        for (int r = 0; r < kRows; r += p.box) {
+            // past the cached tokens, or a bad page: a box outside the pool, which reads as zeros
+            const int key = key0 + r;
+            const int pg = key < w.u.kv ? page_of(a.kv, w.u.s, key) : -1;
+            const int z = pg < 0 ? (int)(a.kv.num_pages * a.kv.Hk) : pg * a.kv.Hk + w.j;
+            const int y = pg < 0 ? 0 : key % a.kv.page_size;
+#pragma unroll
+            for (int pn = 0; pn < C::kStagePanels; ++pn)
+                tma_load_3d(ring + st * C::kStageBytes + pn * kPanel + r * 128, map,
+                            part * C::kStageDims + pn * 64, y, z, bar);
         }
     }
-    float q[kE], o[kE], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-        q[e] = load1<kFp16>(a.q, row * kD + e * 32 + lane);
-        o[e] = 0.f;
-    }
-    const float slope = a.slopes ? a.slopes[h] : 0.f;
-    const int qp = a.slopes ? a.q_pos[t] : 0;
-    for (int i = lo; i < hi; ++i) {
-        const int pg = page_of(a.kv, s, i), in_page = i % a.kv.page_size;
-        const int64_t at = (((int64_t)pg * a.kv.Hk + j) * a.kv.page_size + in_page) * kD;
-        float x = 0.f;
-        if (pg >= 0)
-#pragma unroll
-            for (int e = 0; e < kE; ++e) x = fmaf(q[e], load1<kFp16>(a.kv.k, at + e * 32 + lane), x);
-#pragma unroll
-        for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-        x *= a.scale;
-        if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
-        if (a.slopes) {
-            const int kp = pg >= 0 ? a.kv.pos[(int64_t)pg * a.kv.page_size + in_page] : 0;
-            x -= slope * fabsf((float)(qp - kp));
+    return true;
+}
+
+template <int D>
+__device__ void role_kv(const CUtensorMap *km, const CUtensorMap *vm, const Params &p, Shared &sh, uint32_t ring) {
+    using C = Cfg<D>;
+    uint32_t it = 0;
+    bool ok = true;
+    Pieces w(p);
+    while (ok && w.next()) {
+        const int n = w.steps();
+        // the order in which the products need them: one tile runs a step ahead with its keys
+        const int ahead = w.tiles_used() == 2 ? 0 : 1;
+        ok = load_tile<D>(km, p, sh, ring, it, w, w.key0(0));
+        for (int t = 0; ok && t < n; ++t) {
+            if (ahead && t + 1 < n) ok = load_tile<D>(km, p, sh, ring, it, w, w.key0(t + 1));
+            if (ok) ok = load_tile<D>(vm, p, sh, ring, it, w, w.key0(t));
+            if (ok && !ahead && t + 1 < n) ok = load_tile<D>(km, p, sh, ring, it, w, w.key0(t + 1));
         }
-        const float mn = fmaxf(m, x);
-        const float back_m = mn == -INFINITY ? 0.f : mn;
-        const float p = expf(x - back_m), c = expf(m - back_m);
-        l = l * c + p;
-        m = mn;
-#pragma unroll
-        for (int e = 0; e < kE; ++e)
-            o[e] = o[e] * c + (pg >= 0 ? p * load1<kFp16>(a.kv.v, at + e * 32 + lane) : 0.f);
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-        if constexpr (kFp16)
-            static_cast<__half *>(a.out)[row * kD + e * 32 + lane] = __float2half_rn(o[e] * inv);
-        else
-            static_cast<__nv_bfloat16 *>(a.out)[row * kD + e * 32 + lane] =
-                __float2bfloat16_rn(o[e] * inv);
+    if (ok && !*(volatile int *)&sh.abort) return;
+    // nobody consumes what is in flight after an abort: let it land
+    for (uint32_t k = 0; k < (uint32_t)C::kStages && k < it; ++k) {
+        const uint32_t i = it - 1 - k;
+        drain(smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1);
     }
-    if (a.lse && lane == 0) a.lse[row] = (m == -INFINITY ? 0.f : m) + logf(l);
+}
+
+template <int D>
+__device__ void role_q(const CUtensorMap *qm, const Params &p, Shared &sh, uint32_t q) {
+    using C = Cfg<D>;
+    uint32_t n = 0;
+    bool ok = true;
+    Pieces w(p);
+    while (w.next()) {
+        ok = mbar_wait(smem_u32(&sh.qempty), (n & 1) ^ 1, &sh.abort, p.a.wait_limit);
+        if (!ok) break;
+        const int used = C::kTiles == 1 ? 1 : w.tiles_used();
+        const uint32_t bar = smem_u32(&sh.qfull);
+        mbar_arrive_expect_tx(bar, (uint32_t)(used * (D / 64) * 128 * p.a.g * p.tpt));
+        for (int e = 0; e < used; ++e)
+            for (int pn = 0; pn < D / 64; ++pn)
+                tma_load_3d(q + e * C::kQTile + pn * kPanel, qm, pn * 64, w.j * p.a.g, w.u.tok0 + e * p.tpt, bar);
+        ++n;
+    }
+    if (*(volatile int *)&sh.abort && n) drain(smem_u32(&sh.qfull), (n - 1) & 1);
+}
+
+// Zeros the rows of a value tile in shared memory from slot kv on (what the last page
+// holds there may be anything, and its zero weights would multiply it).
+template <int D>
+__device__ __forceinline__ void clear_tail(uint32_t stage, int rows_from) {
+    using C = Cfg<D>;
+    const int lane = threadIdx.x & 31;
+    for (int pn = 0; pn < C::kStagePanels; ++pn)
+        for (int i = rows_from * 8 + lane; i < kRows * 8; i += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stage + pn * kPanel + i * 16), "r"(0)
+                         : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
+// MMA issuer x (0: warp 1, 1: warp 3).  The whole warp walks the loop and one elected
+// lane issues.  With two row tiles both issuers read every stage and each releases
+// it; with one, the keys' issuer and the values' issuer each release a stage twice.
+template <bool kFp16, int D>
+__device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring, uint32_t tmem, int x) {
+    using C = Cfg<D>;
+    constexpr uint32_t id_s = idesc_f32(kFp16, kRows, kRows, false);
+    constexpr uint32_t id_o = idesc_f32(kFp16, kRows, C::kStageDims, true);
+    const long long lim = p.a.wait_limit;
+    int *ab = &sh.abort;
+    const bool leader = elect_one();
+    uint32_t it = 0, nq = 0;
+    Uses use;
+    Pieces w(p);
+    auto wait_stage = [&](uint32_t i) {
+        return mbar_wait_warp(smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1, ab, lim);
+    };
+    auto release = [&](uint32_t i, int times) {
+        if (leader)
+            for (int k = 0; k < times; ++k) mma_commit(smem_u32(&sh.empty[i % C::kStages]));
+        __syncwarp();
+    };
+    // S[buf] = Q[e] K^T with the keys in stages i .. i + kParts - 1, seen full
+    auto qk = [&](int e, int buf, uint32_t i, int set) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 0; part < C::kParts; ++part) {
+            const uint32_t kb = ring + ((i + part) % C::kStages) * C::kStageBytes;
+            const uint32_t qb = q + e * C::kQTile + part * C::kStageBytes;
+            if (leader) {
+#pragma unroll
+                for (int pn = 0; pn < C::kStagePanels; ++pn)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16(tmem + buf * kRows, smem_desc_sw128(qb + pn * kPanel) + 2 * ks,
+                                 smem_desc_sw128(kb + pn * kPanel) + 2 * ks, id_s, (part | pn | ks) != 0);
+            }
+            __syncwarp();
+        }
+        if (leader) mma_commit(smem_u32(&sh.sfull[set][buf]));
+        __syncwarp();
+    };
+    // O[e] += P[buf] V
+    auto pv = [&](int e, int buf, uint32_t i, bool first, int set) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 0; part < C::kParts; ++part) {
+            const uint64_t vd = desc_mn_sw128(ring + ((i + part) % C::kStages) * C::kStageBytes);
+            if (leader) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)  // 16 keys: 8 columns of P, two 8-row groups of V
+                    mma_ts(tmem + C::kOutCol + e * D + part * C::kStageDims, tmem + buf * kRows + 8 * ks,
+                           vd + 128 * ks, id_o, !first || ks != 0);
+            }
+            __syncwarp();
+        }
+        if (leader) mma_commit(smem_u32(&sh.pdone[set][buf]));
+        __syncwarp();
+    };
+    auto ready_v = [&](uint32_t i, int t) {  // the value tile of step t, its tail cleared
+        for (int part = 0; part < C::kParts; ++part)
+            if (!wait_stage(i + part)) return false;
+        const int from = w.u.kv - w.key0(t);
+        if (from < kRows)
+            for (int part = 0; part < C::kParts; ++part)
+                clear_tail<D>(ring + ((i + part) % C::kStages) * C::kStageBytes, max(from, 0));
+        return true;
+    };
+    while (w.next()) {
+        const int n = w.steps(), used = C::kTiles == 1 ? 1 : w.tiles_used();
+        // the queries are loaded once both issuers' products of the pieces before are
+        // complete, so this piece may use both S buffers at once
+        if (!mbar_wait_warp(smem_u32(&sh.qfull), nq & 1, ab, lim)) goto out;
+        ++nq;
+        if (used == 2) {
+            // stages: K0, V0, K1, V1, ...
+            if (!wait_stage(it)) goto out;
+            qk(x, x, it, 1);
+            release(it, 1);
+            for (int t = 0; t < n; ++t) {
+                const uint32_t iv = it + 1 + 2 * t, ik = iv + 1;
+                if (!ready_v(iv, t)) goto out;
+                if (!mbar_wait_warp(smem_u32(&sh.pfull[1][x]), use.par(t, 2), ab, lim)) goto out;
+                pv(x, x, iv, t == 0, 1);
+                release(iv, 1);
+                if (t + 1 < n) {
+                    if (!wait_stage(ik)) goto out;
+                    qk(x, x, ik, 1);
+                    release(ik, 1);
+                }
+            }
+            it += 2 * n;
+            if (leader) mma_commit(smem_u32(&sh.qempty));
+            __syncwarp();
+        } else {
+            // stages: K0, K1, V0, K2, V1, ..., V(n-1): kParts each
+            constexpr int P = C::kParts;
+            auto at_k = [&](int t) { return it + P * (t < 2 ? t : 2 * t - 1); };
+            auto at_v = [&](int t) { return it + P * (t + 1 < n ? 2 * t + 2 : 2 * t + 1); };
+            for (int t = 0; t < n; ++t) {
+                if (x == 0) {
+                    const uint32_t i = at_k(t);
+                    for (int part = 0; part < P; ++part)
+                        if (!wait_stage(i + part)) goto out;
+                    // the buffer's weights of two steps ago have been multiplied
+                    if (t >= 2 && !mbar_wait_warp(smem_u32(&sh.pdone[0][t & 1]), use.par(t - 2, 1), ab, lim)) goto out;
+                    qk(0, t & 1, i, 0);
+                    for (int part = 0; part < P; ++part) release(i + part, 2);
+                } else {
+                    const uint32_t i = at_v(t);
+                    if (!ready_v(i, t)) goto out;
+                    if (!mbar_wait_warp(smem_u32(&sh.pfull[0][t & 1]), use.par(t, 1), ab, lim)) goto out;
+                    pv(0, t & 1, i, t == 0, 0);
+                    for (int part = 0; part < P; ++part) release(i + part, 2);
+                }
+            }
+            it += 2 * n * P;
+            if (leader) mma_commit(smem_u32(&sh.qempty));
+            __syncwarp();
+        }
+        use.add(n, used);
+    }
+out:
+    if (leader) mma_commit(smem_u32(&sh.fin[x]));
+    __syncwarp();
+    drain(smem_u32(&sh.fin[x]), 0);
 }
 
 template <bool kFp16>
-cudaError_t launch_rows(const AttendArgs &a, cudaStream_t st) {
-    const dim3 grid((unsigned)(((int64_t)a.T * a.Hq + kWarps - 1) / kWarps)), block(32 * kWarps);
-    switch (a.kv.d) {
-        case 64: return launch_pdl(attend_rows_kernel<kFp16, 64>, grid, block, 0, st, a);
-        case 128: return launch_pdl(attend_rows_kernel<kFp16, 128>, grid, block, 0, st, a);
-        default: return launch_pdl(attend_rows_kernel<kFp16, 256>, grid, block, 0, st, a);
+__device__ __forceinline__ uint32_t pack_pair(float x, float y) {
+    if constexpr (kFp16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
+}
+
+template <bool kFp16, int D, bool kMore>
+__device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t tmem, int e) {
+    using C = Cfg<D>;
+    const AttendArgs &a = p.a;
+    const int tid = threadIdx.x & 127, quarter = (threadIdx.x >> 5) & 3;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const int tl = tid / a.g, h = tid - tl * a.g;  // token and head of this row
+    const float sc = a.scale * kLog2e;
+    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap * a.scale : 0.f;
+    const float cap = a.softcap * kLog2e;
+    const uint32_t ocol = tmem + lane_base + C::kOutCol + e * D;
+    uint32_t pos_steps = 0;
+    Uses use;
+    Pieces w(p);
+    while (w.next()) {
+        const int n = w.steps(), used = C::kTiles == 1 ? 1 : w.tiles_used();
+        if (e >= used) {
+            use.add(n, used);
+            continue;
+        }
+        const int tok = e * p.tpt + tl;  // of the unit
+        const bool valid = tl < p.tpt && tok < w.u.ntok;
+        int2 vis = make_int2(INT32_MIN, INT32_MAX);  // a row nobody reads needs no mask
+        if (valid) vis = sees(a, w.u, tok);
+        const int head = w.j * a.g + h;
+        float slope = 0.f;
+        int qp = 0;
+        if constexpr (kMore) {
+            if (a.slopes && valid) {
+                slope = a.slopes[head] * kLog2e;
+                qp = a.q_pos[w.u.tok0 + tok];
+            }
+        }
+        float m = -INFINITY, l = 0.f;
+        int kp = 0, kp0 = 0;  // positions of this thread's key of the next step and of the step's first
+        auto position = [&](int key) {
+            const int pg = key < w.u.kv ? page_of(a.kv, w.u.s, key) : -1;
+            return pg < 0 ? 0 : a.kv.pos[(int64_t)pg * a.kv.page_size + key % a.kv.page_size];
+        };
+        auto fetch_pos = [&](int t) {
+            if constexpr (kMore) {
+                if (a.slopes && t < n) {
+                    kp = position(w.key0(t) + tid);
+                    kp0 = position(w.key0(t));
+                }
+            }
+        };
+        fetch_pos(0);
+        for (int t = 0; t < n; ++t) {
+            const int buf = use.buf(t, e, used), k0 = w.key0(t);
+            float at = 0.f;  // this row's position relative to the step's first key
+            const float *sp = s_pos + (2 * e + (pos_steps & 1)) * 128;
+            if constexpr (kMore) {
+                if (a.slopes) {
+                    // positions relative to the step's first one: exact in fp32, and so are
+                    // their distances, up to 2^24.  Two buffers: a thread writes one again
+                    // only when all have come past the step between.
+                    const_cast<float *>(sp)[tid] = (float)(kp - kp0);
+                    at = (float)(qp - kp0);
+                    mbar_arrive(smem_u32(&sh.pos[e]));
+                    const bool ok = mbar_wait(smem_u32(&sh.pos[e]), pos_steps & 1, &sh.abort, a.wait_limit);
+                    __syncwarp();
+                    if (!__all_sync(0xffffffffu, ok)) return;
+                    ++pos_steps;
+                    fetch_pos(t + 1);
+                }
+            }
+            {
+                const bool ok = mbar_wait(smem_u32(&sh.sfull[used - 1][buf]), use.par(t, used), &sh.abort, a.wait_limit);
+                __syncwarp();
+                if (!__all_sync(0xffffffffu, ok)) return;
+            }
+            tc_fence_after();
+            const uint32_t sb = tmem + lane_base + buf * kRows;
+            float v[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(sb + 32 * c, v[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait_ld_dep(v[c]);
+            if constexpr (kMore) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[c][i] = a.softcap > 0.f ? capped(v[c][i], cap_in, cap) : v[c][i] * sc;
+                if (a.slopes) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 k4 = reinterpret_cast<const float4 *>(sp)[8 * c + i];
+                            v[c][4 * i] = fmaf(-slope, fabsf(at - k4.x), v[c][4 * i]);
+                            v[c][4 * i + 1] = fmaf(-slope, fabsf(at - k4.y), v[c][4 * i + 1]);
+                            v[c][4 * i + 2] = fmaf(-slope, fabsf(at - k4.z), v[c][4 * i + 2]);
+                            v[c][4 * i + 3] = fmaf(-slope, fabsf(at - k4.w), v[c][4 * i + 3]);
+                        }
+                }
+            }
+            if (!__all_sync(0xffffffffu, vis.x <= k0 && vis.y >= k0 + kRows)) {
+                // this tile's visible columns [lo, hi): the range relative to its first slot
+                const int lo = vis.x <= k0 ? 0 : vis.x >= k0 + kRows ? kRows : vis.x - k0;
+                const int hi = vis.y >= k0 + kRows ? kRows : vis.y <= k0 ? 0 : vis.y - k0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * c + i < lo || 32 * c + i >= hi) v[c][i] = -INFINITY;
+            }
+            float mx[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                mx[c] = fmaxf(v[c][0], v[c][1]);
+#pragma unroll
+                for (int i = 2; i < 32; i += 2) mx[c] = max3(mx[c], v[c][i], v[c][i + 1]);
+            }
+            float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if constexpr (!kMore) mt *= sc;
+            const bool grew = mt > m + kSlack;
+            if (__any_sync(0xffffffffu, grew)) {
+                const float f = grew ? exp2f(m - mt) : 1.f;
+                if (grew) m = mt;
+                l *= f;
+                if (t > 0) {
+                    const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t - 1, e, used)]), use.par(t - 1, used),
+                                              &sh.abort, a.wait_limit);
+                    __syncwarp();
+                    if (!__all_sync(0xffffffffu, ok)) return;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t r[16];
+                        asm volatile(
+                            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+                            "%11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                            : "r"(ocol + c)
+                            : "memory");
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                        tmem_st16(ocol + c, r);
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            const uint64_t sc2 = pack2(kMore ? 1.f : sc, kMore ? 1.f : sc), ref2 = pack2(-ref, -ref);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float z0, z1;
+                    unpack2(fma2(pack2(v[c][2 * i], v[c][2 * i + 1]), sc2, ref2), z0, z1);
+                    z0 = ex2_approx(z0);
+                    z1 = ex2_approx(z1);
+                    sum[i & 1] = add2(sum[i & 1], pack2(z0, z1));
+                    pk[i] = pack_pair<kFp16>(z0, z1);
+                }
+                tmem_st16(sb + 16 * c, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh.pfull[used - 1][buf]));
+            float x, y;
+            unpack2(add2(sum[0], sum[1]), x, y);
+            l += x + y;
+        }
+        {
+            const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(n - 1, e, used)]), use.par(n - 1, used),
+                                      &sh.abort, a.wait_limit);
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, ok)) return;
+        }
+        tc_fence_after();
+        const bool whole = w.ta == 0 && w.tb == w.u.tiles;
+        const int64_t orow = (int64_t)(w.u.tok0 + tok) * a.Hq + head;
+        float *part = p.parts + (int64_t)(2 * blockIdx.x + (w.index ? 1 : 0)) * C::kUnitRows * (D + 4);
+        const int prow = e * kRows + tid;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (valid) {
+            if (!whole) {
+                part[2 * prow] = m;
+                part[2 * prow + 1] = l;
+            } else if (a.lse) {
+                a.lse[orow] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+            }
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(ocol + c, o);
+            tmem_wait_ld_dep(o);
+            if (valid) {
+                if (whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + orow * D + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float x = o[8 * i + 2 * k], y = o[8 * i + 2 * k + 1];
+                            r[k] = l == 0.f ? 0u : pack_pair<kFp16>(x * inv, y * inv);
+                        }
+                        dst[i] = make_uint4(r[0], r[1], r[2], r[3]);
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(part + 4 * C::kUnitRows + (int64_t)prow * D + c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+        }
+        tc_fence_before();  // the reads end before the next piece's first product is let in
+        use.add(n, used);
+    }
+}
+
+template <bool kFp16, int D, bool kMore>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
+                  const __grid_constant__ CUtensorMap vm, const Params p) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    uint8_t *mem = raw + (base - smem_u32(raw));
+    const uint32_t q = base, ring = base + C::kQBytes;
+    float *s_pos = reinterpret_cast<float *>(mem + C::kQBytes + C::kStages * C::kStageBytes);
+    Shared &sh = *reinterpret_cast<Shared *>(mem + C::kQBytes + C::kStages * C::kStageBytes + C::kPosBytes);
+    static_assert(sizeof(Shared) <= 512, "Shared");
+    if (base - smem_u32(raw) > C::kPad) {  // cannot be; nothing has been touched yet
+        if (threadIdx.x == 0) atomicOr(p.a.kv.err, kErrTimeout);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), 2);
+        }
+        mbar_init(smem_u32(&sh.qfull), 1);
+        mbar_init(smem_u32(&sh.qempty), 2);
+        for (int i = 0; i < 2; ++i) {
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&sh.sfull[i][b]), 1);
+                mbar_init(smem_u32(&sh.pfull[i][b]), 128);
+                mbar_init(smem_u32(&sh.pdone[i][b]), 1);
+            }
+            mbar_init(smem_u32(&sh.pos[i]), 128);
+            mbar_init(smem_u32(&sh.fin[i]), 1);
+        }
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&sh.tmem), 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 64) {
+        tma_prefetch_desc(&qm);
+        tma_prefetch_desc(&km);
+        tma_prefetch_desc(&vm);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    pdl_wait();
+    if (warp < 4) {
+        if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0) {
+            if (lane == 0) role_kv<D>(&km, &vm, p, sh, ring);
+        } else if (warp == 2) {
+            if (lane == 0) role_q<D>(&qm, p, sh, q);
+        } else {
+            role_mma<kFp16, D>(p, sh, q, ring, tmem, warp == 1 ? 0 : 1);
+        }
+        __syncwarp();
+    } else {
+        // 128 * 72 + 256 * 208 <= 384 * 168
+        if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        role_softmax<kFp16, D, kMore>(p, sh, s_pos, tmem, (warp - 4) >> 2);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (threadIdx.x == 0 && sh.abort) atomicOr(p.a.kv.err, kErrTimeout);
+}
+
+// ---------------------------------------------------------------- the join
+
+constexpr int kJoinThreads = 128, kJoinRows = 16;
+
+// Block (c, y): the unit that the end of share c cuts, if c is the first to cut it,
+// rows [16y, 16y + 16): a warp takes a row's parts in the order of its slots.  All
+// blocks together also write the rows of the units without a visible slot.
+template <bool kFp16, int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params p) {
+    using C = Cfg<D>;
+    constexpr int kV = D / 32;  // outputs of a lane
+    const AttendArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    const Plan pl = *p.plan;
+    const int nb = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
+    for (int i = me; i < pl.units; i += nb) {
+        const Unit u = p.units[i];
+        if (u.tiles) continue;
+        const int64_t r0 = (int64_t)u.tok0 * a.Hq, nr = (int64_t)u.ntok * a.Hq;
+        for (int64_t k = tid; k < nr * D / 8; k += kJoinThreads)
+            reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + r0 * D)[k] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int64_t k = tid; k < nr; k += kJoinThreads) a.lse[r0 + k] = -INFINITY;
+    }
+    if (pl.W == 0) return;
+    const Shares sh = shares_of(pl.W * a.kv.Hk, p.grid, kMinTiles);
+    const int c0 = blockIdx.x;
+    if (c0 + 1 >= sh.n) return;
+    const int64_t cut = share_begin(sh, c0 + 1);
+    const int j = (int)(cut / pl.W);
+    const int64_t base = (int64_t)j * pl.W;
+    const Unit u = p.units[find_unit(p.units, pl.units, cut - base)];
+    const int64_t ub = base + u.prefix, ue = ub + u.tiles;
+    if (cut <= ub || cut >= ue) return;                 // not inside a unit
+    if (c0 > 0 && share_begin(sh, c0) > ub) return;     // an earlier share cuts it first
+    int n = 1;
+    while (c0 + n < sh.n && share_begin(sh, c0 + n) < ue) ++n;
+    // a block's first piece is in its slot 0, a later one (this unit's first) in slot 1
+    const int slot0 = 2 * c0 + (share_begin(sh, c0) < ub);
+    auto part = [&](int i) { return p.parts + (int64_t)(i == 0 ? slot0 : 2 * (c0 + i)) * C::kUnitRows * (D + 4); };
+    for (int k = warp; k < kJoinRows; k += kJoinThreads / 32) {
+        const int r = blockIdx.y * kJoinRows + k, e = r / kRows, rr = r % kRows;
+        const int tl = rr / a.g, tok = e * p.tpt + tl;
+        if (tl >= p.tpt || tok >= u.ntok) continue;
+        float M = -INFINITY, L = 0.f, O[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) O[i] = 0.f;
+        for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[2 * r]);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        const float ref = M == -INFINITY ? 0.f : M;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane;
+            float ew = 0.f;
+            if (i < n) {
+                const float2 ml = *reinterpret_cast<const float2 *>(part(i) + 2 * r);
+                ew = exp2f(ml.x - ref);
+                L = fmaf(ew, ml.y, L);
+            }
+            const int m = min(32, n - i0);
+#pragma unroll 4
+            for (int x = 0; x < m; ++x) {
+                const float f = __shfl_sync(0xffffffffu, ew, x);
+                const float *src = part(i0 + x) + 4 * C::kUnitRows + (int64_t)r * D + kV * lane;
+                float o[kV];
+                if constexpr (kV == 2) *reinterpret_cast<float2 *>(o) = *reinterpret_cast<const float2 *>(src);
+                else
+#pragma unroll
+                    for (int y = 0; y < kV; y += 4)
+                        *reinterpret_cast<float4 *>(o + y) = *reinterpret_cast<const float4 *>(src + y);
+#pragma unroll
+                for (int y = 0; y < kV; ++y) O[y] = fmaf(f, o[y], O[y]);
+            }
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int64_t orow = (int64_t)(u.tok0 + tok) * a.Hq + j * a.g + rr - tl * a.g;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + orow * D + kV * lane);
+#pragma unroll
+        for (int y = 0; y < kV / 2; ++y) dst[y] = L == 0.f ? 0u : pack_pair<kFp16>(O[2 * y] * inv, O[2 * y + 1] * inv);
+        if (a.lse && lane == 0) a.lse[orow] = (ref + log2f(L)) * kLn2;
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+bool encode_maps(const AttendArgs &a, int tpt, int box, CUtensorMap *qm, CUtensorMap *km, CUtensorMap *vm) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const CUtensorMapDataType dt = a.kv.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint64_t D = (cuuint64_t)a.kv.d;
+    {
+        const cuuint64_t dims[3] = {D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+        const cuuint64_t strides[2] = {D * 2, D * 2 * (cuuint64_t)a.Hq};
+        const cuuint32_t bx[3] = {64, (cuuint32_t)a.g, (cuuint32_t)tpt};
+        if (enc(qm, dt, 3, const_cast<void *>(a.q), dims, strides, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    const cuuint64_t dims[3] = {D, (cuuint64_t)a.kv.page_size, (cuuint64_t)(a.kv.num_pages * a.kv.Hk)};
+    const cuuint64_t strides[2] = {D * 2, D * 2 * (cuuint64_t)a.kv.page_size};
+    const cuuint32_t bx[3] = {64, (cuuint32_t)box, 1};
+    for (int i = 0; i < 2; ++i)
+        if (enc(i ? vm : km, dt, 3, i ? a.kv.v : a.kv.k, dims, strides, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
+}
+
+template <bool kFp16, int D>
+cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
+    using C = Cfg<D>;
+    Params p{};
+    p.a = a;
+    p.tpt = kRows / a.g;
+    p.box = 128;
+    while (a.kv.page_size % p.box) p.box >>= 1;  // 16 at least: page_size is a multiple of it
+    p.grid = num_sms < kMaxSms ? num_sms : kMaxSms;
+    const Layout L = layout_of(a.T, a.kv.num_seqs, a.Hq, a.kv.Hk, D);
+    char *ws = static_cast<char *>(a.workspace);
+    p.plan = reinterpret_cast<Plan *>(ws);
+    p.seq_off = reinterpret_cast<int32_t *>(ws + L.seq_off);
+    p.units = reinterpret_cast<Unit *>(ws + L.units);
+    p.parts = reinterpret_cast<float *>(ws + L.parts);
+    p.max_units = L.max_units;
+    CUtensorMap qm, km, vm;
+    if (!encode_maps(a, p.tpt, p.box, &qm, &km, &vm)) return cudaErrorInvalidValue;
+    // a scale that is not positive turns the maximum around: the general path
+    // scales before it compares
+    const bool more = a.softcap > 0.f || a.slopes || !(a.scale > 0.f);
+    auto kernel = more ? attend_kernel<kFp16, D, true> : attend_kernel<kFp16, D, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, C::kTiles * p.tpt);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kernel, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmem, st, qm, km, vm, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attend_join_kernel<kFp16, D>, dim3((unsigned)p.grid, C::kUnitRows / kJoinRows),
+                      dim3(kJoinThreads), 0, st, p);
 }
 
 }  // namespace
 
-size_t attend_workspace(int64_t, int, int, int, int) { return 256; }
+size_t attend_workspace(int64_t T, int num_seqs, int Hq, int Hk, int d) {
+    return layout_of(T, num_seqs, Hq, Hk, d).total;
+}
 
-cudaError_t launch_attend(const AttendArgs &a, int, cudaStream_t st) {
-    return a.kv.fp16 ? launch_rows<true>(a, st) : launch_rows<false>(a, st);
+cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st) {
+    switch (a.kv.d) {
+        case 64: return a.kv.fp16 ? launch_type<true, 64>(a, num_sms, st) : launch_type<false, 64>(a, num_sms, st);
+        case 128: return a.kv.fp16 ? launch_type<true, 128>(a, num_sms, st) : launch_type<false, 128>(a, num_sms, st);
+        default: return a.kv.fp16 ? launch_type<true, 256>(a, num_sms, st) : launch_type<false, 256>(a, num_sms, st);
+    }
 }
 
 }  // namespace up

@@ -22,8 +22,7 @@
 // 128 rows has nothing to give here.  The weights are split into a high and a low
 // part of the cache's type, two products each, so rounding them costs nothing (up
 // to 8 heads: the low parts are the fragment's other 8 rows, in the same product).
-#include "paged.cuh"
-#include "sm100.cuh"
+#include "attend.cuh"
 
 namespace up {
 
@@ -35,10 +34,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;               // slots of a warp's step
 constexpr int kTile = kGroup * kWarps;   // slots of a block's step
-constexpr int kMaxSms = 160;             // the workspace is sized for this many
 constexpr int kMaxPerSm = 3;
 constexpr int kMinTiles = 2;             // shares are not cut finer than this
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Cfg {
@@ -68,24 +65,6 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int s) {
     r.first = r.lo & ~(kGroup - 1);
     r.tiles = (r.hi - r.first + kTile - 1) / kTile;
     return r;
-}
-
-// The shares: block c takes tiles [W*c/n, W*(c+1)/n) of the W in all.
-struct Shares {
-    int64_t W;
-    int n;
-};
-__device__ __forceinline__ Shares shares_of(int64_t W, int grid) {
-    const int64_t most = (W + kMinTiles - 1) / kMinTiles;
-    return Shares{W, (int)(most < grid ? most : grid)};
-}
-__device__ __forceinline__ int64_t share_begin(const Shares &h, int c) { return h.W * c / h.n; }
-// the block whose share holds tile x
-__device__ __forceinline__ int share_of(const Shares &h, int64_t x) {
-    int c = (int)(x * h.n / h.W);
-    while (c + 1 < h.n && share_begin(h, c + 1) <= x) ++c;
-    while (c > 0 && share_begin(h, c) > x) --c;
-    return c;
 }
 
 // Tiles of one KV head of the sequences before `upto`, summed by the whole block;
@@ -178,30 +157,10 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     }
 }
 
-template <bool kFp16>
-__device__ __forceinline__ void store_row4(void *out, int64_t at, float4 v) {
-    uint2 w;
-    if constexpr (kFp16) {
-        const __half2 x = __floats2half2_rn(v.x, v.y), y = __floats2half2_rn(v.z, v.w);
-        w = make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-    } else {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
-        w = make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-    }
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) = w;
-}
-
 // A part in the workspace: g rows of (maximum in log2 units, sum, D outputs); the
 // outputs begin on a 16-byte boundary behind all rows' statistics.
 __device__ __forceinline__ float *part_of(const AttendArgs &a, int D, int slot) {
     return static_cast<float *>(a.workspace) + (int64_t)slot * a.g * (D + 4);
-}
-
-// softcap * tanh(x / softcap) as softcap * (1 - 2 / (e^(2x/softcap) + 1)): exact at
-// both ends, off by about 2^-22 of softcap in between.
-__device__ __forceinline__ float capped(float x, float two_log2e_over_cap, float cap) {
-    const float e = ex2_approx(x * two_log2e_over_cap);
-    return cap - __fdividef(2.f * cap, e + 1.f);
 }
 
 template <bool kFp16, int D, bool kFew, bool kMore>
@@ -220,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
     const int Hk = a.kv.Hk, g = a.g;
     const int64_t W = total_tiles<kThreads>(a, a.kv.num_seqs, s_scan) * Hk;
     if (W == 0) return;
-    const Shares sh = shares_of(W, gridDim.x);
+    const Shares sh = shares_of(W, gridDim.x, kMinTiles);
     if ((int)blockIdx.x >= sh.n) return;
     int64_t at = share_begin(sh, blockIdx.x);
     const int64_t end = share_begin(sh, blockIdx.x + 1);
@@ -484,7 +443,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const AttendA
         if (a.lse && tid == 0) a.lse[orow] = -INFINITY;
         return;
     }
-    const Shares sh = shares_of(W, grid);
+    const Shares sh = shares_of(W, grid, kMinTiles);
     const int64_t unit = before + (int64_t)j * sp.tiles;
     const int c0 = share_of(sh, unit), c1 = share_of(sh, unit + sp.tiles - 1);
     if (c0 == c1) return;  // finished by its block
