@@ -41,7 +41,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kRows = 128;        // rows of a tile, keys of a step
-constexpr int kMinTiles = 4;      // shares are not cut finer than this
+constexpr int kMinTiles = 2;      // shares are not cut finer than this
 constexpr float kSlack = 8.f;     // log2: how far the maximum may grow before a rescale
 constexpr int kPanel = 128 * 128; // 128 rows x 64 elements
 
@@ -79,8 +79,13 @@ struct Plan {
     int pad;
 };
 
+// What a block's share leaves unfinished at its end: a unit that begins in it.
+struct Cut {
+    int parted, j, unit, pad;
+};
+
 struct Layout {
-    size_t seq_off, units, parts, total;
+    size_t seq_off, units, cuts, parts, total;
     int64_t max_units;
 };
 Layout layout_of(int64_t T, int num_seqs, int Hq, int Hk, int d) {
@@ -91,6 +96,7 @@ Layout layout_of(int64_t T, int num_seqs, int Hq, int Hk, int d) {
     auto take = [&](size_t n) { const size_t at = off; off = (off + n + 255) & ~size_t(255); return at; };
     L.seq_off = take(sizeof(int32_t) * (size_t)(num_seqs + 1));
     L.units = take(sizeof(Unit) * (size_t)(L.max_units > 0 ? L.max_units : 1));
+    L.cuts = take(sizeof(Cut) * kMaxSms);
     L.parts = take((size_t)2 * kMaxSms * tiles * kRows * (size_t)(d + 4) * sizeof(float));
     L.total = off;
     return L;
@@ -101,6 +107,7 @@ struct Params {
     Plan *plan;
     int32_t *seq_off;
     Unit *units;
+    Cut *cuts;
     float *parts;
     int64_t max_units;
     int tpt;       // tokens of a tile
@@ -148,7 +155,7 @@ __device__ int64_t block_scan(int64_t v, int64_t *total, int64_t *sh) {
 }
 
 // Lists the units (one block): sequences' unit counts and their scan, then every
-// unit's key tiles (a warp looks at its tokens' ranges) and their scan.
+// unit's key tiles and their scan.
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params p, int tpu) {
     __shared__ int64_t sh[32];
     __shared__ int bad;
@@ -180,9 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         }
         return;
     }
-    for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads / 32) {
-        const int64_t i = u0 + warp;
-        if (i >= units) continue;
+    for (int64_t i = tid; i < units; i += kPlanThreads) {
         int lo = 0, hi = B - 1;  // the last sequence with seq_off <= i
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -193,32 +198,32 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         u.s = lo;
         u.tok0 = c0 + (int)(i - p.seq_off[lo]) * tpu;
         u.ntok = min(tpu, c1 - u.tok0);
-        const int kv = kv_len_of(a.kv, lo, c1 - c0);
-        u.kv = kv;
-        u.hi0 = kv - (c1 - u.tok0) + 1;
-        int first = INT32_MAX, end = 0;
-        if (kv >= 0) {
-            if (!a.visible) {
-                first = 0;
-                end = u.hi0 + u.ntok - 1;
-            } else {
+        u.kv = kv_len_of(a.kv, lo, c1 - c0);
+        u.hi0 = u.kv - (c1 - u.tok0) + 1;
+        if (u.kv >= 0 && !a.visible) u.tiles = (u.hi0 + u.ntok - 1 + kRows - 1) / kRows;
+        p.units[i] = u;
+    }
+    if (a.visible) {
+        __syncthreads();
+        // a warp looks at its unit's ranges, lane by token; units are independent, so
+        // several units' loads are in flight
+#pragma unroll 4
+        for (int64_t i = warp; i < units; i += kPlanThreads / 32) {
+            const Unit u = p.units[i];
+            int first = INT32_MAX, end = 0;
+            if (u.kv >= 0)
                 for (int t = lane; t < u.ntok; t += 32) {
                     const int2 r = sees(a, u, t);
                     first = min(first, r.x);
                     end = max(end, r.y);
                 }
-#pragma unroll
-                for (int k = 16; k; k >>= 1) {
-                    first = min(first, __shfl_xor_sync(0xffffffffu, first, k));
-                    end = max(end, __shfl_xor_sync(0xffffffffu, end, k));
-                }
+            first = __reduce_min_sync(0xffffffffu, first);
+            end = __reduce_max_sync(0xffffffffu, end);
+            if (lane == 0 && first < end) {
+                p.units[i].kt0 = first / kRows;
+                p.units[i].tiles = (end + kRows - 1) / kRows - first / kRows;
             }
         }
-        if (first < end) {
-            u.kt0 = first / kRows;
-            u.tiles = (end + kRows - 1) / kRows - u.kt0;
-        }
-        if (lane == 0) p.units[i] = u;
     }
     __syncthreads();
     int64_t W = 0;
@@ -282,6 +287,8 @@ struct Pieces {
         tb = (int)min((int64_t)u.tiles, end - base - u.prefix);
         at += tb - ta;
         ++index;
+        // the next unit's description, on its way while this one is worked on
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.units + (ui + 1 < n ? ui + 1 : 0)));
         return true;
     }
     __device__ int steps() const { return tb - ta; }
@@ -295,6 +302,7 @@ constexpr int kMaxStages = 8;
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];  // the ring
     uint64_t qfull, qempty;
+    uint64_t pieces;        // a piece's products are complete
     // S buffers: one set of barriers for pieces of one row tile, one for those of two
     uint64_t sfull[2][2];   // the buffer holds logits
     uint64_t pfull[2][2];   // the buffer holds weights
@@ -309,21 +317,15 @@ struct Shared {
 // counts them alike, so barrier parities need no talk.  A parity tells a phase from
 // its neighbours only: whoever waits for a use must know that the one before it is
 // over.  So the second softmax warpgroup, which has no part in pieces of one row
-// tile, shares no barrier with them.
+// tile, shares no barrier with them.  Pieces of one tile take the buffers in turn,
+// across pieces too.
 struct Uses {
-    uint32_t two = 0, one[2] = {0, 0};
-    __device__ void add(int steps, int tiles_used) {
-        if (tiles_used == 2) {
-            two += steps;
-        } else {
-            one[0] += (steps + 1) / 2;
-            one[1] += steps / 2;
-        }
-    }
+    uint32_t two = 0, one = 0;
+    __device__ void add(int steps, int tiles_used) { (tiles_used == 2 ? two : one) += steps; }
     // buffer and parity of its use by step t of row tile e
-    __device__ int buf(int t, int e, int tiles_used) const { return tiles_used == 2 ? e : (t & 1); }
+    __device__ int buf(int t, int e, int tiles_used) const { return tiles_used == 2 ? e : (int)((one + t) & 1u); }
     __device__ uint32_t par(int t, int tiles_used) const {
-        return (tiles_used == 2 ? two + t : one[t & 1] + (t >> 1)) & 1u;
+        return (tiles_used == 2 ? two + t : (one + t) >> 1) & 1u;
     }
 };
 
@@ -371,29 +373,32 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 // ---------------------------------------------------------------- roles
 
-// One key or value tile into ring stages it, it+1, ... (kParts of them).
+// One key or value tile into ring stages it, it+1, ... (kParts of them), by the whole
+// warp: lane l loads the l-th box of 128 / box, from page pg (-1, past the cached
+// tokens or a bad page: a box outside the pool, which reads as zeros).
 template <int D>
 __device__ bool load_tile(const CUtensorMap *map, const Params &p, Shared &sh, uint32_t ring, uint32_t &it,
-                          const Pieces &w, int key0) {
+                          const Pieces &w, int key0, int pg) {
     using C = Cfg<D>;
     const AttendArgs &a = p.a;
+    const int r = (threadIdx.x & 31) * p.box;
+    const int z = pg < 0 ? (int)(a.kv.num_pages * a.kv.Hk) : pg * a.kv.Hk + w.j;
+    const int y = pg < 0 ? 0 : (key0 + r) % a.kv.page_size;
 #pragma unroll 1
     for (int part = 0; part < C::kParts; ++part, ++it) {
         const int st = it % C::kStages;
-        if (!mbar_wait(smem_u32(&sh.empty[st]), ((it / C::kStages) & 1) ^ 1, &sh.abort, a.wait_limit)) return false;
+        if (!mbar_wait_warp(smem_u32(&sh.empty[st]), ((it / C::kStages) & 1) ^ 1, &sh.abort, a.wait_limit))
+            return false;
         const uint32_t bar = smem_u32(&sh.full[st]);
-        mbar_arrive_expect_tx(bar, C::kStageBytes);
-        for (int r = 0; r < kRows; r += p.box) {
-            // past the cached tokens, or a bad page: a box outside the pool, which reads as zeros
-            const int key = key0 + r;
-            const int pg = key < w.u.kv ? page_of(a.kv, w.u.s, key) : -1;
-            const int z = pg < 0 ? (int)(a.kv.num_pages * a.kv.Hk) : pg * a.kv.Hk + w.j;
-            const int y = pg < 0 ? 0 : key % a.kv.page_size;
+        if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(bar, C::kStageBytes);
+        __syncwarp();
+        if (r < kRows) {
 #pragma unroll
             for (int pn = 0; pn < C::kStagePanels; ++pn)
                 tma_load_3d(ring + st * C::kStageBytes + pn * kPanel + r * 128, map,
                             part * C::kStageDims + pn * 64, y, z, bar);
         }
+        __syncwarp();
     }
     return true;
 }
@@ -404,15 +409,25 @@ __device__ void role_kv(const CUtensorMap *km, const CUtensorMap *vm, const Para
     uint32_t it = 0;
     bool ok = true;
     Pieces w(p);
+    const int r = (threadIdx.x & 31) * p.box;
     while (ok && w.next()) {
         const int n = w.steps();
+        // the page of this lane's box, looked up two steps ahead
+        auto page = [&](int t) {
+            const int key = w.key0(t) + r;
+            return t < n && r < kRows && key < w.u.kv ? page_of(p.a.kv, w.u.s, key) : -1;
+        };
+        int p0 = page(0), p1 = page(1), p2 = page(2);
         // the order in which the products need them: one tile runs a step ahead with its keys
-        const int ahead = w.tiles_used() == 2 ? 0 : 1;
-        ok = load_tile<D>(km, p, sh, ring, it, w, w.key0(0));
+        const int ahead = C::kTiles == 1 || w.tiles_used() == 1;
+        ok = load_tile<D>(km, p, sh, ring, it, w, w.key0(0), p0);
         for (int t = 0; ok && t < n; ++t) {
-            if (ahead && t + 1 < n) ok = load_tile<D>(km, p, sh, ring, it, w, w.key0(t + 1));
-            if (ok) ok = load_tile<D>(vm, p, sh, ring, it, w, w.key0(t));
-            if (ok && !ahead && t + 1 < n) ok = load_tile<D>(km, p, sh, ring, it, w, w.key0(t + 1));
+            if (ahead && t + 1 < n) ok = load_tile<D>(km, p, sh, ring, it, w, w.key0(t + 1), p1);
+            if (ok) ok = load_tile<D>(vm, p, sh, ring, it, w, w.key0(t), p0);
+            if (ok && !ahead && t + 1 < n) ok = load_tile<D>(km, p, sh, ring, it, w, w.key0(t + 1), p1);
+            p0 = p1;
+            p1 = p2;
+            p2 = page(t + 3);
         }
     }
     if (ok && !*(volatile int *)&sh.abort) return;
@@ -429,7 +444,9 @@ __device__ void role_q(const CUtensorMap *qm, const Params &p, Shared &sh, uint3
     uint32_t n = 0;
     bool ok = true;
     Pieces w(p);
+    Cut cut{0, 0, 0, 0};
     while (w.next()) {
+        cut = Cut{w.ta == 0 && w.tb < w.u.tiles, w.j, w.ui, 0};
         ok = mbar_wait(smem_u32(&sh.qempty), (n & 1) ^ 1, &sh.abort, p.a.wait_limit);
         if (!ok) break;
         const int used = C::kTiles == 1 ? 1 : w.tiles_used();
@@ -440,6 +457,7 @@ __device__ void role_q(const CUtensorMap *qm, const Params &p, Shared &sh, uint3
                 tma_load_3d(q + e * C::kQTile + pn * kPanel, qm, pn * 64, w.j * p.a.g, w.u.tok0 + e * p.tpt, bar);
         ++n;
     }
+    p.cuts[blockIdx.x] = cut;  // of the last piece
     if (*(volatile int *)&sh.abort && n) drain(smem_u32(&sh.qfull), (n - 1) & 1);
 }
 
@@ -525,17 +543,26 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
                 clear_tail<D>(ring + ((i + part) % C::kStages) * C::kStageBytes, max(from, 0));
         return true;
     };
+    int before = 0;  // row tiles of the piece before
     while (w.next()) {
         const int n = w.steps(), used = C::kTiles == 1 ? 1 : w.tiles_used();
-        // the queries are loaded once both issuers' products of the pieces before are
-        // complete, so this piece may use both S buffers at once
         if (!mbar_wait_warp(smem_u32(&sh.qfull), nq & 1, ab, lim)) goto out;
+        // Between two pieces of two tiles each issuer's own order keeps its S buffer
+        // safe, between two of one tile the buffers' turns do; where the kind
+        // changes, the first issuer's logits would overwrite weights that the other one
+        // still multiplies.  (The queries came after both had finished the piece
+        // before the last, so that piece's phase cannot be mistaken for this one.)
+        if (x == 0 && before && before != used &&
+            !mbar_wait_warp(smem_u32(&sh.pieces), (nq - 1) & 1, ab, lim))
+            goto out;
+        before = used;
         ++nq;
         if (used == 2) {
             // stages: K0, V0, K1, V1, ...
             if (!wait_stage(it)) goto out;
             qk(x, x, it, 1);
             release(it, 1);
+            if (n == 1 && leader) mma_commit(smem_u32(&sh.qempty));
             for (int t = 0; t < n; ++t) {
                 const uint32_t iv = it + 1 + 2 * t, ik = iv + 1;
                 if (!ready_v(iv, t)) goto out;
@@ -546,37 +573,41 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
                     if (!wait_stage(ik)) goto out;
                     qk(x, x, ik, 1);
                     release(ik, 1);
+                    // after the last logits the queries' place is free
+                    if (t + 2 == n && leader) mma_commit(smem_u32(&sh.qempty));
                 }
             }
             it += 2 * n;
-            if (leader) mma_commit(smem_u32(&sh.qempty));
-            __syncwarp();
         } else {
             // stages: K0, K1, V0, K2, V1, ..., V(n-1): kParts each
             constexpr int P = C::kParts;
             auto at_k = [&](int t) { return it + P * (t < 2 ? t : 2 * t - 1); };
             auto at_v = [&](int t) { return it + P * (t + 1 < n ? 2 * t + 2 : 2 * t + 1); };
+            if (x == 1 && leader) mma_commit(smem_u32(&sh.qempty));  // it reads no queries
             for (int t = 0; t < n; ++t) {
+                const int buf = use.buf(t, 0, 1);
                 if (x == 0) {
                     const uint32_t i = at_k(t);
                     for (int part = 0; part < P; ++part)
                         if (!wait_stage(i + part)) goto out;
                     // the buffer's weights of two steps ago have been multiplied
-                    if (t >= 2 && !mbar_wait_warp(smem_u32(&sh.pdone[0][t & 1]), use.par(t - 2, 1), ab, lim)) goto out;
-                    qk(0, t & 1, i, 0);
+                    if (use.one + t >= 2 && !mbar_wait_warp(smem_u32(&sh.pdone[0][buf]), use.par(t - 2, 1), ab, lim))
+                        goto out;
+                    qk(0, buf, i, 0);
                     for (int part = 0; part < P; ++part) release(i + part, 2);
                 } else {
                     const uint32_t i = at_v(t);
                     if (!ready_v(i, t)) goto out;
-                    if (!mbar_wait_warp(smem_u32(&sh.pfull[0][t & 1]), use.par(t, 1), ab, lim)) goto out;
-                    pv(0, t & 1, i, t == 0, 0);
+                    if (!mbar_wait_warp(smem_u32(&sh.pfull[0][buf]), use.par(t, 1), ab, lim)) goto out;
+                    pv(0, buf, i, t == 0, 0);
                     for (int part = 0; part < P; ++part) release(i + part, 2);
                 }
             }
             it += 2 * n * P;
-            if (leader) mma_commit(smem_u32(&sh.qempty));
-            __syncwarp();
+            if (x == 0 && leader) mma_commit(smem_u32(&sh.qempty));
         }
+        if (leader) mma_commit(smem_u32(&sh.pieces));
+        __syncwarp();
         use.add(n, used);
     }
 out:
@@ -604,8 +635,8 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const int tl = tid / a.g, h = tid - tl * a.g;  // token and head of this row
     const float sc = a.scale * kLog2e;
-    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap * a.scale : 0.f;
-    const float cap = a.softcap * kLog2e;
+    Cap cap;
+    if constexpr (kMore) cap.set(a.scale, a.softcap > 0.f ? a.softcap : 1.f);
     const uint32_t ocol = tmem + lane_base + C::kOutCol + e * D;
     uint32_t pos_steps = 0;
     Uses use;
@@ -619,7 +650,12 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
         const int tok = e * p.tpt + tl;  // of the unit
         const bool valid = tl < p.tpt && tok < w.u.ntok;
         int2 vis = make_int2(INT32_MIN, INT32_MAX);  // a row nobody reads needs no mask
-        if (valid) vis = sees(a, w.u, tok);
+        if (valid) {
+            vis = sees(a, w.u, tok);
+            // the next unit's, if it is this sequence's too
+            const int64_t nt = (int64_t)w.u.tok0 + w.u.ntok + tok;
+            if (a.visible && nt < a.T) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.visible + 2 * nt));
+        }
         const int head = w.j * a.g + h;
         float slope = 0.f;
         int qp = 0;
@@ -676,10 +712,33 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_wait_ld_dep(v[c]);
             if constexpr (kMore) {
+                if (a.softcap > 0.f) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        float up = fmaxf(v[c][0], v[c][1]), dn = fminf(v[c][0], v[c][1]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[c][i] = a.softcap > 0.f ? capped(v[c][i], cap_in, cap) : v[c][i] * sc;
+                        for (int i = 2; i < 32; i += 2) {
+                            up = max3(up, v[c][i], v[c][i + 1]);
+                            dn = min3(dn, v[c][i], v[c][i + 1]);
+                        }
+                        const float most = fmaxf(up, -dn) * fabsf(cap.in);
+                        if (__all_sync(0xffffffffu, most < 0.2f)) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) cap.small<4>(v[c][i], v[c][i + 1]);
+                        } else if (__all_sync(0xffffffffu, most < 0.5f)) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) cap.small<8>(v[c][i], v[c][i + 1]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[c][i] = cap.any(v[c][i]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[c][i] *= sc;
+                }
                 if (a.slopes) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -839,6 +898,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         mbar_init(smem_u32(&sh.qfull), 1);
         mbar_init(smem_u32(&sh.qempty), 2);
+        mbar_init(smem_u32(&sh.pieces), 2);
         for (int i = 0; i < 2; ++i) {
             for (int b = 0; b < 2; ++b) {
                 mbar_init(smem_u32(&sh.sfull[i][b]), 1);
@@ -868,7 +928,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (warp < 4) {
         if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
-            if (lane == 0) role_kv<D>(&km, &vm, p, sh, ring);
+            role_kv<D>(&km, &vm, p, sh, ring);
         } else if (warp == 2) {
             if (lane == 0) role_q<D>(&qm, p, sh, q);
         } else {
@@ -889,10 +949,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
 // ---------------------------------------------------------------- the join
 
-constexpr int kJoinThreads = 128, kJoinRows = 16;
+constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 32;  // a warp a row
 
 // Block (c, y): the unit that the end of share c cuts, if c is the first to cut it,
-// rows [16y, 16y + 16): a warp takes a row's parts in the order of its slots.  All
+// kJoinRows rows from kJoinRows*y on: a warp takes a row's parts in the order of its slots.  All
 // blocks together also write the rows of the units without a visible slot.
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params p) {
@@ -916,22 +976,19 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params 
     const Shares sh = shares_of(pl.W * a.kv.Hk, p.grid, kMinTiles);
     const int c0 = blockIdx.x;
     if (c0 + 1 >= sh.n) return;
-    const int64_t cut = share_begin(sh, c0 + 1);
-    const int j = (int)(cut / pl.W);
-    const int64_t base = (int64_t)j * pl.W;
-    const Unit u = p.units[find_unit(p.units, pl.units, cut - base)];
-    const int64_t ub = base + u.prefix, ue = ub + u.tiles;
-    if (cut <= ub || cut >= ue) return;                 // not inside a unit
-    if (c0 > 0 && share_begin(sh, c0) > ub) return;     // an earlier share cuts it first
-    int n = 1;
-    while (c0 + n < sh.n && share_begin(sh, c0 + n) < ue) ++n;
+    const Cut cut = p.cuts[c0];
+    if (!cut.parted) return;
+    const Unit u = p.units[cut.unit];
+    const int j = cut.j;
+    const int64_t ub = (int64_t)j * pl.W + u.prefix, ue = ub + u.tiles;
+    const int n = share_of(sh, ue - 1) - c0 + 1;
     // a block's first piece is in its slot 0, a later one (this unit's first) in slot 1
     const int slot0 = 2 * c0 + (share_begin(sh, c0) < ub);
     auto part = [&](int i) { return p.parts + (int64_t)(i == 0 ? slot0 : 2 * (c0 + i)) * C::kUnitRows * (D + 4); };
-    for (int k = warp; k < kJoinRows; k += kJoinThreads / 32) {
-        const int r = blockIdx.y * kJoinRows + k, e = r / kRows, rr = r % kRows;
+    {
+        const int r = blockIdx.y * kJoinRows + warp, e = r / kRows, rr = r % kRows;
         const int tl = rr / a.g, tok = e * p.tpt + tl;
-        if (tl >= p.tpt || tok >= u.ntok) continue;
+        if (tl >= p.tpt || tok >= u.ntok) return;
         float M = -INFINITY, L = 0.f, O[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) O[i] = 0.f;
@@ -1015,6 +1072,7 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     p.plan = reinterpret_cast<Plan *>(ws);
     p.seq_off = reinterpret_cast<int32_t *>(ws + L.seq_off);
     p.units = reinterpret_cast<Unit *>(ws + L.units);
+    p.cuts = reinterpret_cast<Cut *>(ws + L.cuts);
     p.parts = reinterpret_cast<float *>(ws + L.parts);
     p.max_units = L.max_units;
     CUtensorMap qm, km, vm;
@@ -1023,7 +1081,8 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     // scales before it compares
     const bool more = a.softcap > 0.f || a.slopes || !(a.scale > 0.f);
     auto kernel = more ? attend_kernel<kFp16, D, true> : attend_kernel<kFp16, D, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaError_t e = more ? allow_smem<attend_kernel<kFp16, D, true>>(C::kSmem)
+                         : allow_smem<attend_kernel<kFp16, D, false>>(C::kSmem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, C::kTiles * p.tpt);
     if (e != cudaSuccess) return e;

@@ -2,6 +2,8 @@
 // shares, the capped logit and the output rows.
 #pragma once
 
+#include <atomic>
+
 #include "paged.cuh"
 #include "sm100.cuh"
 
@@ -29,12 +31,36 @@ __device__ __forceinline__ int share_of(const Shares &h, int64_t x) {
     return c;
 }
 
-// softcap * tanh(x / softcap) as softcap * (1 - 2 / (e^(2x/softcap) + 1)): exact at
-// both ends, off by about 2^-22 of softcap in between.
-__device__ __forceinline__ float capped(float x, float two_log2e_over_cap, float cap) {
-    const float e = sm100::ex2_approx(x * two_log2e_over_cap);
-    return cap - __fdividef(2.f * cap, e + 1.f);
-}
+// A capped logit, softcap * tanh(scale * x / softcap), in log2 units.  Where the
+// argument of tanh is small (most logits of most models) its Taylor series: 4 terms up
+// to 0.2 and 8 up to 0.5 leave less than 2^-23 of the result; elsewhere
+// (1 - t) / (1 + t) with t = e^(-2|y|), off by about 2^-23 of softcap.
+struct Cap {
+    float in, out;  // scale / softcap, softcap * log2(e)
+    uint64_t in2;
+    uint64_t c[8];  // the series' factors times out, for two logits at once
+    __device__ __forceinline__ void set(float scale, float softcap) {
+        constexpr float k[8] = {1.f, -1.f / 3.f, 2.f / 15.f, -17.f / 315.f, 62.f / 2835.f, -1382.f / 155925.f,
+                                21844.f / 6081075.f, -929569.f / 638512875.f};
+        in = scale / softcap;
+        out = softcap * kLog2e;
+        in2 = sm100::pack2(in, in);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = sm100::pack2(k[i] * out, k[i] * out);
+    }
+    template <int kTerms>
+    __device__ __forceinline__ void small(float &x, float &y) const {
+        const uint64_t t = sm100::mul2(sm100::pack2(x, y), in2), t2 = sm100::mul2(t, t);
+        uint64_t r = c[kTerms - 1];
+#pragma unroll
+        for (int i = kTerms - 2; i >= 0; --i) r = sm100::fma2(r, t2, c[i]);
+        sm100::unpack2(sm100::mul2(r, t), x, y);
+    }
+    __device__ __forceinline__ float any(float x) const {
+        const float t = sm100::ex2_approx(fabsf(x * in) * (-2.f * kLog2e));
+        return copysignf(__fdividef(1.f - t, 1.f + t) * out, x * in);
+    }
+};
 
 template <bool kFp16>
 __device__ __forceinline__ void store_row4(void *out, int64_t at, float4 v) {
@@ -47,6 +73,20 @@ __device__ __forceinline__ void store_row4(void *out, int64_t at, float4 v) {
         w = make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
     }
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) = w;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};  // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 }  // namespace up

@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
     if (s >= a.kv.num_seqs) return;
     const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
     const float scale2 = a.scale * kLog2e;
-    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap * a.scale : 0.f;
+    Cap cap;
+    if constexpr (kMore) cap.set(a.scale, a.softcap > 0.f ? a.softcap : 1.f);
     bool first_part = true;
     Span sp = span_of(a, s);
     while (at < end) {
@@ -287,22 +288,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
                 for (int i = 0; i < 2 * kR; ++i) x[n][i] += x2[n][i];
             const int key = key_a + step * kTile;
             // logits in log2 units
+            if constexpr (kMore) {
+                if (a.softcap > 0.f) {
+                    float most = 0.f;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2 * kR; ++i) most = fmaxf(most, fabsf(x[n][i]));
+                    const bool small = __all_sync(0xffffffffu, most * fabsf(cap.in) < 0.5f);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2 * kR; i += 2) {
+                            if (small) {
+                                cap.small<8>(x[n][i], x[n][i + 1]);
+                            } else {
+                                x[n][i] = cap.any(x[n][i]);
+                                x[n][i + 1] = cap.any(x[n][i + 1]);
+                            }
+                        }
+                }
+            }
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 0; i < 2 * kR; ++i) {
+                    if (!kMore || !(a.softcap > 0.f)) x[n][i] *= scale2;
                     if constexpr (kMore) {
-                        float z = a.softcap > 0.f ? capped(x[n][i], cap_in, a.softcap * kLog2e)
-                                                  : x[n][i] * scale2;
                         if (a.slopes) {
                             int kp;
                             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(kp)
                                          : "r"(st + 2 * C::kHalfBytes + 4 * (8 * n + col + (i & 1))) : "memory");
-                            z -= slope[i >> 1] * fabsf((float)(qp - kp));
+                            x[n][i] -= slope[i >> 1] * fabsf((float)(qp - kp));
                         }
-                        x[n][i] = z;
-                    } else {
-                        x[n][i] *= scale2;
                     }
                 }
             if (key < sp.lo || key + kGroup > sp.hi) {
@@ -494,8 +512,7 @@ template <bool kFp16, int D, bool kFew, bool kMore>
 cudaError_t launch_variant(const AttendArgs &a, int num_sms, cudaStream_t st) {
     using C = Cfg<D>;
     const int grid = (num_sms < kMaxSms ? num_sms : kMaxSms) * C::kPerSm;
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<kFp16, D, kFew, kMore>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaError_t e = allow_smem<decode_kernel<kFp16, D, kFew, kMore>>(C::kSmem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(decode_kernel<kFp16, D, kFew, kMore>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, st, a);
     if (e != cudaSuccess) return e;

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -33,12 +34,25 @@ class _CLogits(ctypes.Structure):
                 ("slopes", ctypes.c_void_p), ("q_pos", ctypes.c_void_p)]
 
 
-def _up():
-    import block_sparse_long_up_gb300 as up
-    return up
+_lib = None
 
 
-def _need(t, name, dtype, device, shape=None):
+def _L():
+    """The loaded library (looked up once: a decode step's calls are short)."""
+    global _lib
+    if _lib is None:
+        from . import lib
+        _lib = lib()
+    return _lib
+
+
+def _error(where, status):
+    from . import UpError
+    return UpError(where, status)
+
+
+def _refuse(t, name, dtype, device, shape=None):
+    """Raises what is wrong with tensor t."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -49,8 +63,13 @@ def _need(t, name, dtype, device, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need(t, name, dtype, device, shape=None):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (device is None or t.device == device) and (shape is None or t.shape == shape)):
+        _refuse(t, name, dtype, device, shape)
 
 
 class PagedKV:
@@ -96,11 +115,18 @@ class PagedKV:
 def _on(stream):
     """Allocations of a call on `stream` belong to that stream, so a workspace
     freed on return is not handed to another stream's work while it is in use."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
-def _raw(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+_HERE = contextlib.nullcontext()
+
+
+def _raw(stream, device):
+    if torch._C._cuda_getDevice() != device.index:
+        raise ValueError(f"the current device is not the tensors' {device}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
 
 
 def _rows(t, name, cache, heads=None):
@@ -132,7 +158,6 @@ def append_kv(q, k, v, pos, cu_seqlens, cache, inv_freq, axes=None, interleaved=
     them; inv_freq fp32 [rot_dim / 2] (None: no rotation); axes int32 [rot_dim / 2],
     the row of pos that turns each frequency; interleaved: pairs (2i, 2i+1) instead
     of (i, i + rot_dim/2); q_out [T, Hq, d] (q itself is allowed)."""
-    up = _up()
     dev = cache.device
     ks, vs = _rows(k, "k", cache, cache.Hk), _rows(v, "v", cache, cache.Hk)
     T, Hq, qs = k.shape[0], 0, 0
@@ -164,25 +189,31 @@ def append_kv(q, k, v, pos, cu_seqlens, cache, inv_freq, axes=None, interleaved=
                 _need(q_out, "q_out", cache.dtype, dev, q.shape)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        st = up.lib().up_append_kv(
+        st = _L().up_append_kv(
             None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
             pos.data_ptr(), A, None if axes is None else axes.data_ptr(),
             None if inv_freq is None else inv_freq.data_ptr(), rot,
             ROPE_INTERLEAVED if interleaved else 0, cu_seqlens.data_ptr(), T, Hq, cache._ref,
-            None if q is None else q_out.data_ptr(), _raw(stream))
+            None if q is None else q_out.data_ptr(), _raw(stream, dev))
     if st:
-        raise up.UpError("up_append_kv", st)
+        raise _error("up_append_kv", st)
     return q_out
 
 
+@functools.lru_cache(maxsize=64)
+def _plain_logits(scale, softcap):
+    lg = _CLogits(scale, softcap, None, None)  # read by the library during a call, never written
+    return ctypes.byref(lg)
+
+
 def _logits(cache, T, Hq, scale, softcap, slopes, q_pos):
-    if slopes is not None:
-        _need(slopes, "slopes", torch.float32, cache.device, (Hq,))
-        if q_pos is None or cache.pos_pages is None:
-            raise ValueError("slopes need q_pos and a cache with pos_pages")
-        _need(q_pos, "q_pos", torch.int32, cache.device, (T,))
-        return _CLogits(scale, softcap, slopes.data_ptr(), q_pos.data_ptr())
-    return _CLogits(scale, softcap, None, None)
+    if slopes is None:
+        return _plain_logits(scale, softcap)
+    _need(slopes, "slopes", torch.float32, cache.device, (Hq,))
+    if q_pos is None or cache.pos_pages is None:
+        raise ValueError("slopes need q_pos and a cache with pos_pages")
+    _need(q_pos, "q_pos", torch.int32, cache.device, (T,))
+    return ctypes.byref(_CLogits(scale, softcap, slopes.data_ptr(), q_pos.data_ptr()))
 
 
 def _outputs(q, cache, out, lse):
@@ -209,11 +240,11 @@ def _workspace(workspace, need, device):
 
 
 def attend_paged_workspace(total_tokens, num_seqs, Hq, Hk, d) -> int:
-    return int(_up().lib().up_attend_paged_workspace(total_tokens, num_seqs, Hq, Hk, d))
+    return int(_L().up_attend_paged_workspace(total_tokens, num_seqs, Hq, Hk, d))
 
 
 def decode_attend_workspace(num_seqs, Hq, Hk, d) -> int:
-    return int(_up().lib().up_decode_attend_workspace(num_seqs, Hq, Hk, d))
+    return int(_L().up_decode_attend_workspace(num_seqs, Hq, Hk, d))
 
 
 def attend_paged(q, cu_seqlens, cache, scale=None, softcap=0.0, slopes=None, q_pos=None,
@@ -225,7 +256,6 @@ def attend_paged(q, cu_seqlens, cache, scale=None, softcap=0.0, slopes=None, q_p
     scale (default d ** -0.5), softcap (0: none); slopes fp32 [Hq] with q_pos int32
     [T]: a bias of -slope * |q_pos - key position|; visible int32 [T, 2]: the slots
     [first, end) each query sees (default: causal)."""
-    up = _up()
     dev = cache.device
     if _rows(q, "q", cache) != q.shape[1] * cache.d:
         raise ValueError("q must be contiguous")
@@ -236,16 +266,16 @@ def attend_paged(q, cu_seqlens, cache, scale=None, softcap=0.0, slopes=None, q_p
         _need(visible, "visible", torch.int32, dev, (T, 2))
     with _on(stream):
         out, lse = _outputs(q, cache, out, lse)
-        L = up.lib()
+        L = _L()
         need = L.up_attend_paged_workspace(T, cache.num_seqs, Hq, cache.Hk, d)
         ws = _workspace(workspace, need, dev)
         st = L.up_attend_paged(q.data_ptr(), cu_seqlens.data_ptr(), T, Hq, cache._ref,
-                               ctypes.byref(lg),
+                               lg,
                                None if visible is None else visible.data_ptr(), out.data_ptr(),
                                lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                               _raw(stream))
+                               _raw(stream, dev))
     if st:
-        raise up.UpError("up_attend_paged", st)
+        raise _error("up_attend_paged", st)
     return out, lse
 
 
@@ -255,7 +285,6 @@ def decode_attend(q, cache, scale=None, softcap=0.0, slopes=None, q_pos=None, kv
     returns (out, lse fp32 [num_seqs, Hq]).  See up_decode_attend.  kv_start int32
     [num_seqs]: the first visible slot of each sequence; the other arguments are
     attend_paged's."""
-    up = _up()
     dev = cache.device
     if _rows(q, "q", cache) != q.shape[1] * cache.d:
         raise ValueError("q must be contiguous")
@@ -267,13 +296,13 @@ def decode_attend(q, cache, scale=None, softcap=0.0, slopes=None, q_pos=None, kv
         _need(kv_start, "kv_start", torch.int32, dev, (B,))
     with _on(stream):
         out, lse = _outputs(q, cache, out, lse)
-        L = up.lib()
+        L = _L()
         need = L.up_decode_attend_workspace(B, Hq, cache.Hk, d)
         ws = _workspace(workspace, need, dev)
-        st = L.up_decode_attend(q.data_ptr(), Hq, cache._ref, ctypes.byref(lg),
+        st = L.up_decode_attend(q.data_ptr(), Hq, cache._ref, lg,
                                 None if kv_start is None else kv_start.data_ptr(),
                                 out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                ws.numel() * ws.element_size(), _raw(stream))
+                                ws.numel() * ws.element_size(), _raw(stream, dev))
     if st:
-        raise up.UpError("up_decode_attend", st)
+        raise _error("up_decode_attend", st)
     return out, lse
