@@ -305,7 +305,7 @@ struct Shared {
     uint64_t pieces;        // a piece's products are complete
     // S buffers: one set of barriers for pieces of one row tile, one for those of two
     uint64_t sfull[2][2];   // the buffer holds logits
-    uint64_t pfull[2][2];   // the buffer holds weights
+    uint64_t pfull[2][2][2];  // the buffer holds the weights of the first, the second 64 keys
     uint64_t pdone[2][2];   // the weights have been multiplied into O
     uint64_t pos[2];     // a warpgroup's key positions are in shared memory
     uint64_t fin[2];
@@ -518,21 +518,28 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
         __syncwarp();
     };
     // O[e] += P[buf] V
-    auto pv = [&](int e, int buf, uint32_t i, bool first, int set) {
-        tc_fence_after();
+    auto pv = [&](int e, int buf, uint32_t i, bool first, int set, uint32_t parity) {
 #pragma unroll 1
-        for (int part = 0; part < C::kParts; ++part) {
-            const uint64_t vd = desc_mn_sw128(ring + ((i + part) % C::kStages) * C::kStageBytes);
-            if (leader) {
+        for (int half = 0; half < 2; ++half) {
+            if (!mbar_wait_warp(smem_u32(&sh.pfull[set][buf][half]), parity, ab, lim)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int part = 0; part < C::kParts; ++part) {
+                const uint64_t vd = desc_mn_sw128(ring + ((i + part) % C::kStages) * C::kStageBytes);
+                if (leader) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)  // 16 keys: 8 columns of P, two 8-row groups of V
-                    mma_ts(tmem + C::kOutCol + e * D + part * C::kStageDims, tmem + buf * kRows + 8 * ks,
-                           vd + 128 * ks, id_o, !first || ks != 0);
+                    for (int k = 0; k < 4; ++k) {  // 16 keys: 8 columns of P, two 8-row groups of V
+                        const int ks = 4 * half + k;
+                        mma_ts(tmem + C::kOutCol + e * D + part * C::kStageDims, tmem + buf * kRows + 8 * ks,
+                               vd + 128 * ks, id_o, !first || ks != 0);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         if (leader) mma_commit(smem_u32(&sh.pdone[set][buf]));
         __syncwarp();
+        return true;
     };
     auto ready_v = [&](uint32_t i, int t) {  // the value tile of step t, its tail cleared
         for (int part = 0; part < C::kParts; ++part)
@@ -566,8 +573,7 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
             for (int t = 0; t < n; ++t) {
                 const uint32_t iv = it + 1 + 2 * t, ik = iv + 1;
                 if (!ready_v(iv, t)) goto out;
-                if (!mbar_wait_warp(smem_u32(&sh.pfull[1][x]), use.par(t, 2), ab, lim)) goto out;
-                pv(x, x, iv, t == 0, 1);
+                if (!pv(x, x, iv, t == 0, 1, use.par(t, 2))) goto out;
                 release(iv, 1);
                 if (t + 1 < n) {
                     if (!wait_stage(ik)) goto out;
@@ -598,8 +604,7 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
                 } else {
                     const uint32_t i = at_v(t);
                     if (!ready_v(i, t)) goto out;
-                    if (!mbar_wait_warp(smem_u32(&sh.pfull[0][buf]), use.par(t, 1), ab, lim)) goto out;
-                    pv(0, buf, i, t == 0, 0);
+                    if (!pv(0, buf, i, t == 0, 0, use.par(t, 1))) goto out;
                     for (int part = 0; part < P; ++part) release(i + part, 2);
                 }
             }
@@ -815,10 +820,12 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
                     pk[i] = pack_pair<kFp16>(z0, z1);
                 }
                 tmem_st16(sb + 16 * c, pk);
+                if (c & 1) {  // the first half's products start while the second is computed
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&sh.pfull[used - 1][buf][c >> 1]));
+                }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(smem_u32(&sh.pfull[used - 1][buf]));
             float x, y;
             unpack2(add2(sum[0], sum[1]), x, y);
             l += x + y;
@@ -837,35 +844,63 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (valid) {
             if (!whole) {
-                part[2 * prow] = m;
-                part[2 * prow + 1] = l;
+                part[prow] = m;
+                part[C::kUnitRows + prow] = l;
             } else if (a.lse) {
                 a.lse[orow] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
             }
         }
+        const int lane = tid & 31, row_at = valid ? (int)orow : -1;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(ocol + c, o);
-            tmem_wait_ld_dep(o);
-            if (valid) {
-                if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + orow * D + c);
+        for (int c = 0; c < D; c += 64) {
+            float o[2][32];
+            tmem_ld32(ocol + c, o[0]);
+            tmem_ld32(ocol + c + 32, o[1]);
+            tmem_wait_ld_dep(o[0]);
+            tmem_wait_ld_dep(o[1]);
+            if (whole) {
+                uint4 pc[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t *r = reinterpret_cast<uint32_t *>(&pc[k]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint32_t r[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float x = o[8 * i + 2 * k], y = o[8 * i + 2 * k + 1];
-                            r[k] = l == 0.f ? 0u : pack_pair<kFp16>(x * inv, y * inv);
-                        }
-                        dst[i] = make_uint4(r[0], r[1], r[2], r[3]);
+                        const float *src = &o[k >> 2][(k & 3) * 8 + 2 * i];
+                        r[i] = l == 0.f ? 0u : pack_pair<kFp16>(src[0] * inv, src[1] * inv);
                     }
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(part + 4 * C::kUnitRows + (int64_t)prow * D + c);
+                }
+                // 16-byte pieces exchanged among 8 lanes, so that 8 lanes store 128
+                // adjacent bytes of a row: a store of 16 bytes to each of 32 rows takes
+                // the load-store unit 8 times as long, and everybody's loads with it
+                // (4000 cycles a piece, against a step's 3000)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int x = 1; x < 8; x <<= 1)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (k & x) continue;
+                        const bool up = lane & x;
+                        uint32_t *lo = reinterpret_cast<uint32_t *>(&pc[k]);
+                        uint32_t *hi = reinterpret_cast<uint32_t *>(&pc[k | x]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t y = __shfl_xor_sync(0xffffffffu, up ? lo[i] : hi[i], x);
+                            if (up) lo[i] = y; else hi[i] = y;
+                        }
+                    }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int at = __shfl_sync(0xffffffffu, row_at, (lane & 24) + k);
+                    if (at >= 0)
+                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (int64_t)at * D + c +
+                                                   8 * (lane & 7)) = pc[k];
+                }
+            } else if (valid) {
+                // in fours of columns, rows adjacent
+                float4 *dst = reinterpret_cast<float4 *>(part + 4 * C::kUnitRows) + (c / 4) * C::kUnitRows + prow;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float *src = &o[i >> 3][(i & 7) * 4];
+                    dst[i * C::kUnitRows] = make_float4(src[0], src[1], src[2], src[3]);
                 }
             }
         }
@@ -902,7 +937,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             for (int b = 0; b < 2; ++b) {
                 mbar_init(smem_u32(&sh.sfull[i][b]), 1);
-                mbar_init(smem_u32(&sh.pfull[i][b]), 128);
+                mbar_init(smem_u32(&sh.pfull[i][b][0]), 128);
+                mbar_init(smem_u32(&sh.pfull[i][b][1]), 128);
                 mbar_init(smem_u32(&sh.pdone[i][b]), 1);
             }
             mbar_init(smem_u32(&sh.pos[i]), 128);
@@ -949,15 +985,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
 // ---------------------------------------------------------------- the join
 
-constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 32;  // a warp a row
+constexpr int kJoinThreads = 256, kJoinRows = 32;
 
 // Block (c, y): the unit that the end of share c cuts, if c is the first to cut it,
-// kJoinRows rows from kJoinRows*y on: a warp takes a row's parts in the order of its slots.  All
+// rows [32y, 32y + 32): a lane takes a row, a warp every eighth four of its columns, the
+// parts in the order of their slots.  All
 // blocks together also write the rows of the units without a visible slot.
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params p) {
     using C = Cfg<D>;
-    constexpr int kV = D / 32;  // outputs of a lane
     const AttendArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
@@ -985,48 +1021,52 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params 
     // a block's first piece is in its slot 0, a later one (this unit's first) in slot 1
     const int slot0 = 2 * c0 + (share_begin(sh, c0) < ub);
     auto part = [&](int i) { return p.parts + (int64_t)(i == 0 ? slot0 : 2 * (c0 + i)) * C::kUnitRows * (D + 4); };
-    {
-        const int r = blockIdx.y * kJoinRows + warp, e = r / kRows, rr = r % kRows;
-        const int tl = rr / a.g, tok = e * p.tpt + tl;
-        if (tl >= p.tpt || tok >= u.ntok) return;
-        float M = -INFINITY, L = 0.f, O[kV];
+    constexpr int kC = D / 32;  // fours of columns of a warp
+    __shared__ __align__(16) uint32_t s_out[kJoinRows][D / 2 + 4];
+    __shared__ int s_row[kJoinRows];
+    const int r = blockIdx.y * kJoinRows + lane, e = r / kRows, rr = r % kRows;
+    const int tl = rr / a.g, tok = e * p.tpt + tl;
+    const bool valid = tl < p.tpt && tok < u.ntok;
+    float M = -INFINITY, L = 0.f;
+    float4 O[kC];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) O[i] = 0.f;
-        for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[2 * r]);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        const float ref = M == -INFINITY ? 0.f : M;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const int i = i0 + lane;
-            float ew = 0.f;
-            if (i < n) {
-                const float2 ml = *reinterpret_cast<const float2 *>(part(i) + 2 * r);
-                ew = exp2f(ml.x - ref);
-                L = fmaf(ew, ml.y, L);
-            }
-            const int m = min(32, n - i0);
+    for (int k = 0; k < kC; ++k) O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (valid) {
 #pragma unroll 4
-            for (int x = 0; x < m; ++x) {
-                const float f = __shfl_sync(0xffffffffu, ew, x);
-                const float *src = part(i0 + x) + 4 * C::kUnitRows + (int64_t)r * D + kV * lane;
-                float o[kV];
-                if constexpr (kV == 2) *reinterpret_cast<float2 *>(o) = *reinterpret_cast<const float2 *>(src);
-                else
+        for (int i = 0; i < n; ++i) M = fmaxf(M, part(i)[r]);
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float *src = part(i);
+            const float w = exp2f(src[r] - ref);
+            L = fmaf(w, src[C::kUnitRows + r], L);
+            const float4 *o = reinterpret_cast<const float4 *>(src + 4 * C::kUnitRows) + r;
 #pragma unroll
-                    for (int y = 0; y < kV; y += 4)
-                        *reinterpret_cast<float4 *>(o + y) = *reinterpret_cast<const float4 *>(src + y);
-#pragma unroll
-                for (int y = 0; y < kV; ++y) O[y] = fmaf(f, o[y], O[y]);
+            for (int k = 0; k < kC; ++k) {
+                const float4 v = o[(warp + 8 * k) * C::kUnitRows];
+                O[k].x = fmaf(w, v.x, O[k].x); O[k].y = fmaf(w, v.y, O[k].y);
+                O[k].z = fmaf(w, v.z, O[k].z); O[k].w = fmaf(w, v.w, O[k].w);
             }
         }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-        for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int64_t orow = (int64_t)(u.tok0 + tok) * a.Hq + j * a.g + rr - tl * a.g;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + orow * D + kV * lane);
-#pragma unroll
-        for (int y = 0; y < kV / 2; ++y) dst[y] = L == 0.f ? 0u : pack_pair<kFp16>(O[2 * y] * inv, O[2 * y + 1] * inv);
-        if (a.lse && lane == 0) a.lse[orow] = (ref + log2f(L)) * kLn2;
+    for (int k = 0; k < kC; ++k) {
+        uint32_t *dst = &s_out[lane][2 * (warp + 8 * k)];
+        dst[0] = L == 0.f ? 0u : pack_pair<kFp16>(O[k].x * inv, O[k].y * inv);
+        dst[1] = L == 0.f ? 0u : pack_pair<kFp16>(O[k].z * inv, O[k].w * inv);
+    }
+    if (warp == 0) {
+        const int orow = (u.tok0 + tok) * a.Hq + j * a.g + rr - tl * a.g;
+        s_row[lane] = valid ? orow : -1;
+        if (valid && a.lse) a.lse[orow] = ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
+    }
+    __syncthreads();
+    for (int i = tid; i < kJoinRows * D / 8; i += kJoinThreads) {
+        const int k = i / (D / 8), c = i - k * (D / 8);
+        if (s_row[k] >= 0)
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (int64_t)s_row[k] * D + 8 * c) =
+                *reinterpret_cast<const uint4 *>(&s_out[k][4 * c]);
     }
 }
 
