@@ -26,11 +26,12 @@
 //               former, warp 3 the latter, with two S buffers.  Two instruction
 //               streams alternate accumulators, which is what the tensor pipe needs
 //               for its full rate;
-//   warps 4-11  two softmax warpgroups, one per tile (4-7 at head_dim 256).  Thread =
-//               row.  It holds the row's 128 logits in registers, writes the weights
-//               over them in TMEM, and rescales its output row there only when the
-//               maximum has grown by more than 2^8 (weights then stay below 2^8, far
-//               inside both types and fp32), which after the first tiles is rare.
+//   warps 4-11  two softmax warpgroups, one per tile (at head_dim 256 one per 64 keys of
+//               the only tile).  Thread = row.  It holds the row's logits in registers,
+//               writes the weights over them in TMEM, and rescales its output row
+//               there only when the maximum has grown by more than 2^8 (weights then
+//               stay below 2^8, far inside both types and fp32), which after the first
+//               tiles is rare.
 #include "attend.cuh"
 #include "tma_host.cuh"
 
@@ -48,17 +49,20 @@ constexpr int kPanel = 128 * 128; // 128 rows x 64 elements
 template <int D>
 struct Cfg {
     static constexpr int kTiles = D == 256 ? 1 : 2;
-    static constexpr int kThreads = 128 * (1 + kTiles);
+    static constexpr int kThreads = 384;
     static constexpr int kStageDims = D < 128 ? D : 128;          // dims of one ring stage
     static constexpr int kStagePanels = kStageDims / 64;
     static constexpr int kStageBytes = kStagePanels * kPanel;
     static constexpr int kParts = D / kStageDims;                 // stages of a key (value) tile
     static constexpr int kQTile = D / 64 * kPanel;
     static constexpr int kQBytes = kTiles * kQTile;
-    static constexpr int kStages = D == 64 ? 8 : 5;
+    static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 5;
+    static constexpr int kOutBytes = D == 256 ? 0 : 8 * 4096;      // the warps' output rows on their way
     static constexpr int kPosBytes = kTiles * 2 * 128 * 4;        // two steps' key positions
+    static constexpr int kXchBytes = kTiles == 1 ? 1024 : 0;      // what the threads of a row tell one another
+    static constexpr int kTail = kQBytes + kStages * kStageBytes; // where these begin
     static constexpr int kPad = 512;  // dynamic shared memory begins at a multiple of 1024 (checked)
-    static constexpr int kSmem = kQBytes + kStages * kStageBytes + kPosBytes + 512 + kPad;
+    static constexpr int kSmem = kTail + kOutBytes + kPosBytes + kXchBytes + 512 + kPad;
     static constexpr int kOutCol = 256;                           // S: columns 0..255
     static constexpr int kUnitRows = kTiles * kRows;
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -271,10 +275,10 @@ struct Pieces {
         j = (int)(at / W1);
         base = (int64_t)j * W1;
         ui = find_unit(pp.units, n, at - base);
+        u = pp.units[ui];
     }
     __device__ bool next() {
         if (at >= end) return false;
-        u = p.units[ui];
         while (at - base >= u.prefix + u.tiles) {  // units without tiles, or the last one done
             if (++ui == n) {
                 ui = 0;
@@ -307,6 +311,8 @@ struct Shared {
     uint64_t sfull[2][2];   // the buffer holds logits
     uint64_t pfull[2][2][2];  // the buffer holds the weights of the first, the second 64 keys
     uint64_t pdone[2][2];   // the weights have been multiplied into O
+    uint64_t turn[2];    // a softmax warpgroup may take its exponentials
+    uint64_t xch[4];     // the two warps of 32 rows have met (one row tile)
     uint64_t pos[2];     // a warpgroup's key positions are in shared memory
     uint64_t fin[2];
     uint32_t tmem;
@@ -633,26 +639,40 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
 }
 
 template <bool kFp16, int D, bool kMore>
-__device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t tmem, int e) {
+__device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float *s_pos, uint8_t *s_xch, uint32_t tmem,
+                             int e) {
     using C = Cfg<D>;
+    constexpr bool kSplit = C::kTiles == 1;      // the warpgroups share a row tile, 64 columns each
+    constexpr int kCh = kSplit ? 2 : 4;          // chunks of 32 columns of a thread
+    const int et = kSplit ? 0 : e;               // row tile
+    const int ch0 = kSplit ? 2 * e : 0;          // first chunk
     const AttendArgs &a = p.a;
-    const int tid = threadIdx.x & 127, quarter = (threadIdx.x >> 5) & 3;
+    const int tid = threadIdx.x & 127, lane = tid & 31, quarter = (threadIdx.x >> 5) & 3;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const int tl = tid / a.g, h = tid - tl * a.g;  // token and head of this row
     const float sc = a.scale * kLog2e;
     Cap cap;
     if constexpr (kMore) cap.set(a.scale, a.softcap > 0.f ? a.softcap : 1.f);
-    const uint32_t ocol = tmem + lane_base + C::kOutCol + e * D;
-    uint32_t pos_steps = 0;
+    const uint32_t ocol = tmem + lane_base + C::kOutCol + et * D;
+    uint32_t pos_steps = 0, turns = 0, swaps = 0;
+    // the two threads of a row meet (the pair of warps does): false after an abort
+    auto meet = [&]() {
+        const uint32_t bar = smem_u32(&sh.xch[quarter]);
+        mbar_arrive(bar);
+        const bool ok = mbar_wait(bar, swaps & 1, &sh.abort, a.wait_limit);
+        __syncwarp();
+        ++swaps;
+        return (bool)__all_sync(0xffffffffu, ok);
+    };
     Uses use;
     Pieces w(p);
     while (w.next()) {
-        const int n = w.steps(), used = C::kTiles == 1 ? 1 : w.tiles_used();
-        if (e >= used) {
+        const int n = w.steps(), used = kSplit ? 1 : w.tiles_used();
+        if (et >= used) {
             use.add(n, used);
             continue;
         }
-        const int tok = e * p.tpt + tl;  // of the unit
+        const int tok = et * p.tpt + tl;  // of the unit
         const bool valid = tl < p.tpt && tok < w.u.ntok;
         int2 vis = make_int2(INT32_MIN, INT32_MAX);  // a row nobody reads needs no mask
         if (valid) {
@@ -679,25 +699,27 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
         auto fetch_pos = [&](int t) {
             if constexpr (kMore) {
                 if (a.slopes && t < n) {
-                    kp = position(w.key0(t) + tid);
+                    if (!kSplit || e == 0) kp = position(w.key0(t) + tid);
                     kp0 = position(w.key0(t));
                 }
             }
         };
         fetch_pos(0);
         for (int t = 0; t < n; ++t) {
-            const int buf = use.buf(t, e, used), k0 = w.key0(t);
+            const int buf = use.buf(t, et, used), k0 = w.key0(t);
             float at = 0.f;  // this row's position relative to the step's first key
-            const float *sp = s_pos + (2 * e + (pos_steps & 1)) * 128;
+            const float *sp = s_pos + (2 * et + (pos_steps & 1)) * 128;
             if constexpr (kMore) {
                 if (a.slopes) {
                     // positions relative to the step's first one: exact in fp32, and so are
                     // their distances, up to 2^24.  Two buffers: a thread writes one again
                     // only when all have come past the step between.
-                    const_cast<float *>(sp)[tid] = (float)(kp - kp0);
                     at = (float)(qp - kp0);
-                    mbar_arrive(smem_u32(&sh.pos[e]));
-                    const bool ok = mbar_wait(smem_u32(&sh.pos[e]), pos_steps & 1, &sh.abort, a.wait_limit);
+                    if (!kSplit || e == 0) {
+                        const_cast<float *>(sp)[tid] = (float)(kp - kp0);
+                        mbar_arrive(smem_u32(&sh.pos[et]));
+                    }
+                    const bool ok = mbar_wait(smem_u32(&sh.pos[et]), pos_steps & 1, &sh.abort, a.wait_limit);
                     __syncwarp();
                     if (!__all_sync(0xffffffffu, ok)) return;
                     ++pos_steps;
@@ -711,15 +733,15 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
             }
             tc_fence_after();
             const uint32_t sb = tmem + lane_base + buf * kRows;
-            float v[4][32];
+            float v[kCh][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(sb + 32 * c, v[c]);
+            for (int c = 0; c < kCh; ++c) tmem_ld32(sb + 32 * (ch0 + c), v[c]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_wait_ld_dep(v[c]);
+            for (int c = 0; c < kCh; ++c) tmem_wait_ld_dep(v[c]);
             if constexpr (kMore) {
                 if (a.softcap > 0.f) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < kCh; ++c) {
                         float up = fmaxf(v[c][0], v[c][1]), dn = fminf(v[c][0], v[c][1]);
 #pragma unroll
                         for (int i = 2; i < 32; i += 2) {
@@ -740,16 +762,16 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < kCh; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[c][i] *= sc;
                 }
                 if (a.slopes) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < kCh; ++c)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float4 k4 = reinterpret_cast<const float4 *>(sp)[8 * c + i];
+                            const float4 k4 = reinterpret_cast<const float4 *>(sp)[8 * (ch0 + c) + i];
                             v[c][4 * i] = fmaf(-slope, fabsf(at - k4.x), v[c][4 * i]);
                             v[c][4 * i + 1] = fmaf(-slope, fabsf(at - k4.y), v[c][4 * i + 1]);
                             v[c][4 * i + 2] = fmaf(-slope, fabsf(at - k4.z), v[c][4 * i + 2]);
@@ -762,33 +784,46 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
                 const int lo = vis.x <= k0 ? 0 : vis.x >= k0 + kRows ? kRows : vis.x - k0;
                 const int hi = vis.y >= k0 + kRows ? kRows : vis.y <= k0 ? 0 : vis.y - k0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < kCh; ++c)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (32 * c + i < lo || 32 * c + i >= hi) v[c][i] = -INFINITY;
+                        if (32 * (ch0 + c) + i < lo || 32 * (ch0 + c) + i >= hi) v[c][i] = -INFINITY;
             }
-            float mx[4];
+            float mt = -INFINITY;
+            {
+                float mx[kCh];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mx[c] = fmaxf(v[c][0], v[c][1]);
+                for (int c = 0; c < kCh; ++c) {
+                    mx[c] = fmaxf(v[c][0], v[c][1]);
 #pragma unroll
-                for (int i = 2; i < 32; i += 2) mx[c] = max3(mx[c], v[c][i], v[c][i + 1]);
+                    for (int i = 2; i < 32; i += 2) mx[c] = max3(mx[c], v[c][i], v[c][i + 1]);
+                    mt = fmaxf(mt, mx[c]);
+                }
             }
-            float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             if constexpr (!kMore) mt *= sc;
+            if constexpr (kSplit) {
+                // both threads of the row need one reference: the larger of their maxima,
+                // rounded to 16 bits (any value near the maximum does)
+                __nv_bfloat16 *x = reinterpret_cast<__nv_bfloat16 *>(s_xch) + (swaps & 1) * 256;
+                x[e * 128 + tid] = __float2bfloat16_rn(mt);
+                if (!meet()) return;
+                mt = fmaxf(__bfloat162float(x[tid]), __bfloat162float(x[128 + tid]));
+            }
             const bool grew = mt > m + kSlack;
             if (__any_sync(0xffffffffu, grew)) {
                 const float f = grew ? exp2f(m - mt) : 1.f;
                 if (grew) m = mt;
                 l *= f;
                 if (t > 0) {
-                    const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t - 1, e, used)]), use.par(t - 1, used),
+                    const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t - 1, et, used)]), use.par(t - 1, used),
                                               &sh.abort, a.wait_limit);
                     __syncwarp();
                     if (!__all_sync(0xffffffffu, ok)) return;
                     tc_fence_after();
+                    constexpr int kScaled = kSplit ? D / 2 : D;
+                    const uint32_t from = ocol + (kSplit ? e * kScaled : 0);
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
+                    for (int c = 0; c < kScaled; c += 16) {
                         uint32_t r[16];
                         asm volatile(
                             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -796,19 +831,38 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
                             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
                               "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
                               "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                            : "r"(ocol + c)
+                            : "r"(from + c)
                             : "memory");
 #pragma unroll
                         for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-                        tmem_st16(ocol + c, r);
+                        tmem_st16(from + c, r);
+                    }
+                    if constexpr (kSplit) {
+                        // the first half's product adds to all of the row: both halves of it
+                        // are rescaled before either warpgroup hands over its weights
+                        tmem_wait_st();
+                        tc_fence_before();
+                        if (!meet()) return;
+                        tc_fence_after();
                     }
                 }
+            }
+            if (used == 2) {
+                // The warpgroups take their exponentials in turn, so that one computes
+                // while the other's products run: left alone they fall into step, and
+                // the tensor cores idle while both wait for the same units (2048 tokens
+                // over 16K: 471 us without the turns, 407 with them).
+                const bool ok = (turns == 0 && e == 0) || mbar_wait(smem_u32(&sh.turn[e]), (turns + (e ^ 1)) & 1,
+                                                                    &sh.abort, a.wait_limit);
+                __syncwarp();
+                if (!__all_sync(0xffffffffu, ok)) return;
+                ++turns;
             }
             const float ref = m == -INFINITY ? 0.f : m;
             const uint64_t sc2 = pack2(kMore ? 1.f : sc, kMore ? 1.f : sc), ref2 = pack2(-ref, -ref);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < kCh; ++c) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -819,11 +873,12 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
                     sum[i & 1] = add2(sum[i & 1], pack2(z0, z1));
                     pk[i] = pack_pair<kFp16>(z0, z1);
                 }
-                tmem_st16(sb + 16 * c, pk);
+                tmem_st16(sb + 16 * (ch0 + c), pk);
+                if (c == 2 && used == 2) mbar_arrive(smem_u32(&sh.turn[e ^ 1]));
                 if (c & 1) {  // the first half's products start while the second is computed
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(smem_u32(&sh.pfull[used - 1][buf][c >> 1]));
+                    mbar_arrive(smem_u32(&sh.pfull[used - 1][buf][(ch0 + c) >> 1]));
                 }
             }
             float x, y;
@@ -831,18 +886,25 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
             l += x + y;
         }
         {
-            const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(n - 1, e, used)]), use.par(n - 1, used),
+            const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(n - 1, et, used)]), use.par(n - 1, used),
                                       &sh.abort, a.wait_limit);
             __syncwarp();
             if (!__all_sync(0xffffffffu, ok)) return;
         }
         tc_fence_after();
+        if constexpr (kSplit) {  // the row's sum is both threads'
+            float *x = reinterpret_cast<float *>(s_xch);
+            x[e * 128 + tid] = l;
+            if (!meet()) return;
+            l = x[tid] + x[128 + tid];
+            if (!meet()) return;  // read before the place is written again
+        }
         const bool whole = w.ta == 0 && w.tb == w.u.tiles;
         const int64_t orow = (int64_t)(w.u.tok0 + tok) * a.Hq + head;
         float *part = p.parts + (int64_t)(2 * blockIdx.x + (w.index ? 1 : 0)) * C::kUnitRows * (D + 4);
-        const int prow = e * kRows + tid;
+        const int prow = et * kRows + tid;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (valid) {
+        if (valid && (!kSplit || e == 0)) {
             if (!whole) {
                 part[prow] = m;
                 part[C::kUnitRows + prow] = l;
@@ -850,9 +912,11 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
                 a.lse[orow] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
             }
         }
-        const int lane = tid & 31, row_at = valid ? (int)orow : -1;
+        const int row_at = valid ? (int)orow : -1;
+        constexpr int kCols = kSplit ? D / 2 : D;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
+        for (int c0 = 0; c0 < kCols; c0 += 64) {
+            const int c = c0 + (kSplit ? e * kCols : 0);
             float o[2][32];
             tmem_ld32(ocol + c, o[0]);
             tmem_ld32(ocol + c + 32, o[1]);
@@ -869,30 +933,48 @@ __device__ void role_softmax(const Params &p, Shared &sh, float *s_pos, uint32_t
                         r[i] = l == 0.f ? 0u : pack_pair<kFp16>(src[0] * inv, src[1] * inv);
                     }
                 }
-                // 16-byte pieces exchanged among 8 lanes, so that 8 lanes store 128
-                // adjacent bytes of a row: a store of 16 bytes to each of 32 rows takes
-                // the load-store unit 8 times as long, and everybody's loads with it
-                // (4000 cycles a piece, against a step's 3000)
+                // 16-byte pieces change lanes, so that 8 lanes store 128 adjacent bytes of
+                // a row: a store of 16 bytes to each of 32 rows takes the load-store
+                // unit 8 times as long, and everybody's loads with it (4000 cycles a
+                // piece, against a step's 3000)
+                if constexpr (C::kOutBytes > 0) {
+                    uint8_t *st = s_out + ((threadIdx.x >> 5) - 4) * 4096;  // 32 rows x 128 bytes
 #pragma unroll
-                for (int x = 1; x < 8; x <<= 1)
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4 *>(st + lane * 128 + ((k ^ (lane & 7)) << 4)) = pc[k];
+                    __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        if (k & x) continue;
-                        const bool up = lane & x;
-                        uint32_t *lo = reinterpret_cast<uint32_t *>(&pc[k]);
-                        uint32_t *hi = reinterpret_cast<uint32_t *>(&pc[k | x]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t y = __shfl_xor_sync(0xffffffffu, up ? lo[i] : hi[i], x);
-                            if (up) lo[i] = y; else hi[i] = y;
-                        }
+                        const int r = (lane >> 3) + 4 * k;
+                        const int at = __shfl_sync(0xffffffffu, row_at, r);
+                        const uint4 x = *reinterpret_cast<const uint4 *>(st + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                        if (at >= 0)
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (int64_t)at * D + c +
+                                                       8 * (lane & 7)) = x;
                     }
+                    __syncwarp();
+                } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int at = __shfl_sync(0xffffffffu, row_at, (lane & 24) + k);
-                    if (at >= 0)
-                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (int64_t)at * D + c +
-                                                   8 * (lane & 7)) = pc[k];
+                    for (int x = 1; x < 8; x <<= 1)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            if (k & x) continue;
+                            const bool up = lane & x;
+                            uint32_t *lo = reinterpret_cast<uint32_t *>(&pc[k]);
+                            uint32_t *hi = reinterpret_cast<uint32_t *>(&pc[k | x]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t y = __shfl_xor_sync(0xffffffffu, up ? lo[i] : hi[i], x);
+                                if (up) lo[i] = y; else hi[i] = y;
+                            }
+                        }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int at = __shfl_sync(0xffffffffu, row_at, (lane & 24) + k);
+                        if (at >= 0)
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (int64_t)at * D + c +
+                                                       8 * (lane & 7)) = pc[k];
+                    }
                 }
             } else if (valid) {
                 // in fours of columns, rows adjacent
@@ -918,8 +1000,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     uint8_t *mem = raw + (base - smem_u32(raw));
     const uint32_t q = base, ring = base + C::kQBytes;
-    float *s_pos = reinterpret_cast<float *>(mem + C::kQBytes + C::kStages * C::kStageBytes);
-    Shared &sh = *reinterpret_cast<Shared *>(mem + C::kQBytes + C::kStages * C::kStageBytes + C::kPosBytes);
+    uint8_t *s_out = mem + C::kTail, *s_xch = s_out + C::kOutBytes + C::kPosBytes;
+    float *s_pos = reinterpret_cast<float *>(s_out + C::kOutBytes);
+    Shared &sh = *reinterpret_cast<Shared *>(s_xch + C::kXchBytes);
     static_assert(sizeof(Shared) <= 512, "Shared");
     if (base - smem_u32(raw) > C::kPad) {  // cannot be; nothing has been touched yet
         if (threadIdx.x == 0) atomicOr(p.a.kv.err, kErrTimeout);
@@ -934,6 +1017,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         mbar_init(smem_u32(&sh.qfull), 1);
         mbar_init(smem_u32(&sh.qempty), 2);
         mbar_init(smem_u32(&sh.pieces), 2);
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.xch[i]), 64);
         for (int i = 0; i < 2; ++i) {
             for (int b = 0; b < 2; ++b) {
                 mbar_init(smem_u32(&sh.sfull[i][b]), 1);
@@ -941,6 +1025,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 mbar_init(smem_u32(&sh.pfull[i][b][1]), 128);
                 mbar_init(smem_u32(&sh.pdone[i][b]), 1);
             }
+            mbar_init(smem_u32(&sh.turn[i]), 128);
             mbar_init(smem_u32(&sh.pos[i]), 128);
             mbar_init(smem_u32(&sh.fin[i]), 1);
         }
@@ -962,7 +1047,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t tmem = sh.tmem;
     pdl_wait();
     if (warp < 4) {
-        if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
             role_kv<D>(&km, &vm, p, sh, ring);
         } else if (warp == 2) {
@@ -973,8 +1058,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         __syncwarp();
     } else {
         // 128 * 72 + 256 * 208 <= 384 * 168
-        if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        role_softmax<kFp16, D, kMore>(p, sh, s_pos, tmem, (warp - 4) >> 2);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        role_softmax<kFp16, D, kMore>(p, sh, s_out, s_pos, s_xch, tmem, (warp - 4) >> 2);
     }
     tc_fence_before();
     __syncthreads();

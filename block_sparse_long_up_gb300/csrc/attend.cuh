@@ -36,21 +36,23 @@ __device__ __forceinline__ int share_of(const Shares &h, int64_t x) {
 // to 0.2 and 8 up to 0.5 leave less than 2^-23 of the result; elsewhere
 // (1 - t) / (1 + t) with t = e^(-2|y|), off by about 2^-23 of softcap.
 struct Cap {
-    float in, out;  // scale / softcap, softcap * log2(e)
-    uint64_t in2;
-    uint64_t c[8];  // the series' factors times out, for two logits at once
+    float in, out;   // scale / softcap, softcap * log2(e)
+    uint64_t c[8];   // the series in powers of x, for two logits at once
     __device__ __forceinline__ void set(float scale, float softcap) {
         constexpr float k[8] = {1.f, -1.f / 3.f, 2.f / 15.f, -17.f / 315.f, 62.f / 2835.f, -1382.f / 155925.f,
                                 21844.f / 6081075.f, -929569.f / 638512875.f};
         in = scale / softcap;
         out = softcap * kLog2e;
-        in2 = sm100::pack2(in, in);
+        float f = scale * kLog2e;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = sm100::pack2(k[i] * out, k[i] * out);
+        for (int i = 0; i < 8; ++i) {
+            c[i] = sm100::pack2(k[i] * f, k[i] * f);
+            f *= in * in;
+        }
     }
     template <int kTerms>
     __device__ __forceinline__ void small(float &x, float &y) const {
-        const uint64_t t = sm100::mul2(sm100::pack2(x, y), in2), t2 = sm100::mul2(t, t);
+        const uint64_t t = sm100::pack2(x, y), t2 = sm100::mul2(t, t);
         uint64_t r = c[kTerms - 1];
 #pragma unroll
         for (int i = kTerms - 2; i >= 0; --i) r = sm100::fma2(r, t2, c[i]);
