@@ -216,34 +216,28 @@ def _logits(cache, T, Hq, scale, softcap, slopes, q_pos):
     return ctypes.byref(_CLogits(scale, softcap, slopes.data_ptr(), q_pos.data_ptr()))
 
 
-def _outputs(q, cache, out, lse):
-    T, Hq, d = q.shape
-    if out is None:
-        out = torch.empty((T, Hq, d), dtype=cache.dtype, device=cache.device)
-    else:
-        _need(out, "out", cache.dtype, cache.device, q.shape)
-    if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=cache.device)
-    else:
-        _need(lse, "lse", torch.float32, cache.device, (T, Hq))
-    return out, lse
+def _given(out, lse, workspace, cache, shape):
+    """Checks the buffers that the caller brought."""
+    if out is not None:
+        _need(out, "out", cache.dtype, cache.device, shape)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, cache.device, shape[:2])
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch.Tensor")
+        if workspace.device != cache.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {cache.device}")
 
 
-def _workspace(workspace, need, device):
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if not isinstance(workspace, torch.Tensor):
-        raise TypeError("workspace must be a torch.Tensor")
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
-    return workspace
-
-
+@functools.lru_cache(maxsize=256)
 def attend_paged_workspace(total_tokens, num_seqs, Hq, Hk, d) -> int:
+    """Bytes of attend_paged's workspace (0: sizes it does not take)."""
     return int(_L().up_attend_paged_workspace(total_tokens, num_seqs, Hq, Hk, d))
 
 
+@functools.lru_cache(maxsize=256)
 def decode_attend_workspace(num_seqs, Hq, Hk, d) -> int:
+    """Bytes of decode_attend's workspace (0: sizes it does not take)."""
     return int(_L().up_decode_attend_workspace(num_seqs, Hq, Hk, d))
 
 
@@ -264,16 +258,22 @@ def attend_paged(q, cu_seqlens, cache, scale=None, softcap=0.0, slopes=None, q_p
     lg = _logits(cache, T, Hq, d ** -0.5 if scale is None else scale, softcap, slopes, q_pos)
     if visible is not None:
         _need(visible, "visible", torch.int32, dev, (T, 2))
+    if out is not None or lse is not None or workspace is not None:
+        _given(out, lse, workspace, cache, q.shape)
     with _on(stream):
-        out, lse = _outputs(q, cache, out, lse)
-        L = _L()
-        need = L.up_attend_paged_workspace(T, cache.num_seqs, Hq, cache.Hk, d)
-        ws = _workspace(workspace, need, dev)
-        st = L.up_attend_paged(q.data_ptr(), cu_seqlens.data_ptr(), T, Hq, cache._ref,
-                               lg,
-                               None if visible is None else visible.data_ptr(), out.data_ptr(),
-                               lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                               _raw(stream, dev))
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=cache.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            size = attend_paged_workspace(T, cache.num_seqs, Hq, cache.Hk, d)
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        else:
+            size = workspace.numel() * workspace.element_size()
+        st = _L().up_attend_paged(q.data_ptr(), cu_seqlens.data_ptr(), T, Hq, cache._ref, lg,
+                             None if visible is None else visible.data_ptr(),
+                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
+                             _raw(stream, dev))
     if st:
         raise _error("up_attend_paged", st)
     return out, lse
@@ -294,15 +294,22 @@ def decode_attend(q, cache, scale=None, softcap=0.0, slopes=None, q_pos=None, kv
     lg = _logits(cache, B, Hq, d ** -0.5 if scale is None else scale, softcap, slopes, q_pos)
     if kv_start is not None:
         _need(kv_start, "kv_start", torch.int32, dev, (B,))
+    if out is not None or lse is not None or workspace is not None:
+        _given(out, lse, workspace, cache, q.shape)
     with _on(stream):
-        out, lse = _outputs(q, cache, out, lse)
-        L = _L()
-        need = L.up_decode_attend_workspace(B, Hq, cache.Hk, d)
-        ws = _workspace(workspace, need, dev)
-        st = L.up_decode_attend(q.data_ptr(), Hq, cache._ref, lg,
-                                None if kv_start is None else kv_start.data_ptr(),
-                                out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                                ws.numel() * ws.element_size(), _raw(stream, dev))
+        if out is None:
+            out = torch.empty((B, Hq, d), dtype=cache.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            size = decode_attend_workspace(B, Hq, cache.Hk, d)
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        else:
+            size = workspace.numel() * workspace.element_size()
+        st = _L().up_decode_attend(q.data_ptr(), Hq, cache._ref, lg,
+                             None if kv_start is None else kv_start.data_ptr(),
+                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
+                             _raw(stream, dev))
     if st:
         raise _error("up_decode_attend", st)
     return out, lse
