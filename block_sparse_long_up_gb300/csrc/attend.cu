@@ -121,12 +121,16 @@ struct Params {
 
 // ---------------------------------------------------------------- the plan
 
-// [lo, hi) of token t: tl tokens behind the unit's first one.
+// [lo, hi) of a token from its entry in `visible`, cut to the cached slots.
+__device__ __forceinline__ int2 cut_range(int2 v, int kv) {
+    const int lo = max(v.x, 0), hi = min(v.y, kv);
+    return lo < hi ? make_int2(lo, hi) : make_int2(INT32_MAX, 0);
+}
+
+// [lo, hi) of the token tl tokens behind the unit's first one.
 __device__ __forceinline__ int2 sees(const AttendArgs &a, const Unit &u, int tl) {
     if (!a.visible) return make_int2(0, u.hi0 + tl);
-    const int2 v = reinterpret_cast<const int2 *>(a.visible)[u.tok0 + tl];
-    const int lo = max(v.x, 0), hi = min(v.y, u.kv);
-    return lo < hi ? make_int2(lo, hi) : make_int2(INT32_MAX, 0);
+    return cut_range(reinterpret_cast<const int2 *>(a.visible)[u.tok0 + tl], u.kv);
 }
 
 constexpr int kPlanThreads = 1024;
@@ -258,7 +262,8 @@ struct Pieces {
     int64_t W1, at, end;
     int j, ui, n;        // KV head, unit index, units
     int64_t base;        // tiles of the KV heads before j
-    Unit u;
+    Unit u, behind;
+    int after = -1;      // the index of `behind`
     int ta, tb;          // tiles [ta, tb) of the unit
     int64_t index = -1;  // pieces so far, less one
 
@@ -285,14 +290,15 @@ struct Pieces {
                 ++j;
                 base += W1;
             }
-            u = p.units[ui];
+            u = ui == after ? behind : p.units[ui];
         }
         ta = (int)(at - base - u.prefix);
         tb = (int)min((int64_t)u.tiles, end - base - u.prefix);
         at += tb - ta;
         ++index;
         // the next unit's description, on its way while this one is worked on
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.units + (ui + 1 < n ? ui + 1 : 0)));
+        after = ui + 1 < n ? ui + 1 : 0;
+        behind = p.units[after];
         return true;
     }
     __device__ int steps() const { return tb - ta; }
@@ -655,6 +661,8 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
     if constexpr (kMore) cap.set(a.scale, a.softcap > 0.f ? a.softcap : 1.f);
     const uint32_t ocol = tmem + lane_base + C::kOutCol + et * D;
     uint32_t pos_steps = 0, turns = 0, swaps = 0;
+    int ahead_tok = -1;  // the token whose range `ahead` is
+    int2 ahead = make_int2(0, 0);
     // the two threads of a row meet (the pair of warps does): false after an abort
     auto meet = [&]() {
         const uint32_t bar = smem_u32(&sh.xch[quarter]);
@@ -676,10 +684,14 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
         const bool valid = tl < p.tpt && tok < w.u.ntok;
         int2 vis = make_int2(INT32_MIN, INT32_MAX);  // a row nobody reads needs no mask
         if (valid) {
-            vis = sees(a, w.u, tok);
-            // the next unit's, if it is this sequence's too
+            if (a.visible && w.u.tok0 + tok == ahead_tok) vis = cut_range(ahead, w.u.kv);
+            else vis = sees(a, w.u, tok);
+        }
+        if (a.visible) {
+            // the same row of the unit behind this one: read now, used if that one is next
             const int64_t nt = (int64_t)w.u.tok0 + w.u.ntok + tok;
-            if (a.visible && nt < a.T) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.visible + 2 * nt));
+            ahead_tok = nt < a.T ? (int)nt : -1;
+            if (ahead_tok >= 0) ahead = reinterpret_cast<const int2 *>(a.visible)[nt];
         }
         const int head = w.j * a.g + h;
         float slope = 0.f;
@@ -780,14 +792,19 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                 }
             }
             if (!__all_sync(0xffffffffu, vis.x <= k0 && vis.y >= k0 + kRows)) {
-                // this tile's visible columns [lo, hi): the range relative to its first slot
+                // the rows of a warp are a few tokens', so their ranges begin and end close
+                // together, and most of its chunks are seen by all of them
                 const int lo = vis.x <= k0 ? 0 : vis.x >= k0 + kRows ? kRows : vis.x - k0;
                 const int hi = vis.y >= k0 + kRows ? kRows : vis.y <= k0 ? 0 : vis.y - k0;
 #pragma unroll
-                for (int c = 0; c < kCh; ++c)
+                for (int c = 0; c < kCh; ++c) {
+                    const int from = lo - 32 * (ch0 + c), to = hi - 32 * (ch0 + c);
+                    if (!__all_sync(0xffffffffu, from <= 0 && to >= 32)) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * (ch0 + c) + i < lo || 32 * (ch0 + c) + i >= hi) v[c][i] = -INFINITY;
+                        for (int i = 0; i < 32; ++i)
+                            if (i < from || i >= to) v[c][i] = -INFINITY;
+                    }
+                }
             }
             float mt = -INFINITY;
             {
@@ -1047,7 +1064,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t tmem = sh.tmem;
     pdl_wait();
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
             role_kv<D>(&km, &vm, p, sh, ring);
         } else if (warp == 2) {
@@ -1057,7 +1074,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         __syncwarp();
     } else {
-        // 128 * 72 + 256 * 208 <= 384 * 168
+        // 128 * 88 + 256 * 208 <= 384 * 168
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         role_softmax<kFp16, D, kMore>(p, sh, s_out, s_pos, s_xch, tmem, (warp - 4) >> 2);
     }
