@@ -18,18 +18,22 @@ namespace up {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;    // tokens of a tile
+constexpr int kMaxTokens = 32;   // tokens of a tile
 constexpr int kMaxHalf = 128;    // rot / 2
+constexpr int kAngles = 2048;    // angles of a tile
+constexpr int kUnits = 3072;     // units of a tile: 12 a thread
 constexpr int kInFlight = 4;     // units a thread loads before it stores any
 
-// The angle pos * inv_freq as a fraction of half a turn in [-1, 1): inv_freq is
-// taken to turns in 64 bits as a multiple of 2^-64 turns, whose product with the
-// position wraps at whole turns by itself, so the reduction is exact for every
-// 32-bit position.
-__device__ __forceinline__ float half_turns(float inv_freq, int pos) {
+// inv_freq in turns a position, as a multiple of 2^-64 turns; its product with a
+// position wraps at whole turns by itself, so the angle is reduced exactly for every
+// 32-bit position.  (Once a frequency and block: 64-bit floats are slow here.)
+__device__ __forceinline__ unsigned long long turn_step(float inv_freq) {
     double t = (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
     t -= rint(t);
-    const unsigned long long step = (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
+    return (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
+}
+// The angle at a position as a fraction of half a turn in [-1, 1).
+__device__ __forceinline__ float half_turns(unsigned long long step, int pos) {
     const unsigned long long at = step * (unsigned long long)(long long)pos;
     return (float)(int)(at >> 32) * 4.656612873077392578125e-10f;  // 2^-31
 }
@@ -78,16 +82,19 @@ __device__ __forceinline__ void turn_unit(uint4 &x, uint4 &y, const float *cs, c
 }
 
 template <typename T2, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, int tile) {
-    __shared__ __align__(16) float s_cos[kMaxTokens][kMaxHalf], s_sin[kMaxTokens][kMaxHalf];
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendArgs a, int tile) {
+    __shared__ __align__(16) float s_cos[kAngles], s_sin[kAngles];
+    __shared__ unsigned long long s_step[kMaxHalf];
     __shared__ int64_t s_row[kMaxTokens];
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * tile, nt = min(tile, a.T - t0);
     const int half = a.rot >> 1, page_size = a.kv.page_size;
     pdl_wait();
-    // one thread per token finds its slot and records its position there
-    if (tid < nt) {
-        const int t = t0 + tid;
+    for (int f = tid; f < half; f += kThreads) s_step[f] = turn_step(a.inv_freq[f]);
+    // one thread per token (the last warp's) finds its slot and records its position there
+    const int finder = kThreads - 1 - tid;
+    if (finder < nt) {
+        const int t = t0 + finder;
         const int s = seq_of_token(a.cu_seqlens, a.kv.num_seqs, t, a.T, a.kv.err);
         int64_t row = -1;
         if (s >= 0) {
@@ -102,16 +109,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
                 }
             }
         }
-        s_row[tid] = row;
+        s_row[finder] = row;
     }
+    __syncthreads();
     for (int i = tid; i < nt * half; i += kThreads) {
         const int tl = i / half, f = i - tl * half;
         int ax = a.axes ? a.axes[f] : 0;
         if (ax < 0 || ax >= a.num_axes) ax = 0;
         float sn, cs;
-        sincospif(half_turns(a.inv_freq[f], a.pos[(int64_t)ax * a.T + t0 + tl]), &sn, &cs);
-        s_cos[tl][f] = cs;
-        s_sin[tl][f] = sn;
+        sincospif(half_turns(s_step[f], a.pos[(int64_t)ax * a.T + t0 + tl]), &sn, &cs);
+        s_cos[i] = cs;
+        s_sin[i] = sn;
     }
     __syncthreads();
     const int d = a.kv.d, Hq = a.Hq, Hk = a.kv.Hk;
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
                 const bool split = u < turned && !kInterleaved;
                 xo[k] = split ? u : 2 * u;
                 yo[k] = split ? u + turned : 2 * u + 1;
-                ang[k] = rot ? tl * kMaxHalf + 8 * u : -1;
+                ang[k] = rot ? tl * half + 8 * u : -1;
                 x[k] = src[xo[k]];
                 y[k] = src[yo[k]];
             }
@@ -161,8 +169,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
             if (!dst[k]) continue;
             if (ang[k] >= 0) {
                 float cs[8], sn[8];
-                const float4 *c4 = reinterpret_cast<const float4 *>(&s_cos[0][0] + ang[k]);
-                const float4 *s4 = reinterpret_cast<const float4 *>(&s_sin[0][0] + ang[k]);
+                const float4 *c4 = reinterpret_cast<const float4 *>(s_cos + ang[k]);
+                const float4 *s4 = reinterpret_cast<const float4 *>(s_sin + ang[k]);
                 *reinterpret_cast<float4 *>(cs) = c4[0];
                 *reinterpret_cast<float4 *>(cs + 4) = c4[1];
                 *reinterpret_cast<float4 *>(sn) = s4[0];
@@ -178,9 +186,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a, in
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs &a, int num_sms, cudaStream_t st) {
-    // tokens per block: a step's few tokens spread one to a block, a prompt's
-    // fill kMaxTokens once there are four blocks for every SM
-    int tile = a.T / (4 * num_sms);
+    // tokens per block: a step's few tokens spread one to a block; a prompt's fill a block
+    // (kUnits or kAngles of them) once there are four blocks for every SM.  Eight tokens
+    // of 12 rows of 64 left blocks that were all lookups: 21 us for 19K tokens against
+    // 15 with 32.
+    int tile = (a.T + 4 * num_sms - 1) / (4 * num_sms);
+    const int units = (a.Hq + 2 * a.kv.Hk) * (a.kv.d >> 4);
+    if (tile > kUnits / units) tile = kUnits / units;
+    if (a.rot > 0 && tile > kAngles / (a.rot >> 1)) tile = kAngles / (a.rot >> 1);
     tile = tile < 1 ? 1 : tile > kMaxTokens ? kMaxTokens : tile;
     const unsigned grid = (unsigned)((a.T + tile - 1) / tile);
     if (a.kv.fp16)
