@@ -331,7 +331,7 @@ struct Shared {
     uint64_t sfull[2][2];   // the buffer holds logits
     uint64_t pfull[2][2][2];  // the buffer holds the weights of the first, the second 64 keys
     uint64_t pdone[2][2];   // the weights have been multiplied into O
-    uint64_t turn[2];    // a softmax warpgroup may take its exponentials
+    uint64_t turn[2];    // an issuer may issue its step's products
     uint64_t xch[4];     // the two warps of 32 rows have met (one row tile)
     uint64_t pos[2];     // a warpgroup's key positions are in shared memory
     uint64_t fin[2];
@@ -512,7 +512,7 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
     const long long lim = p.a.wait_limit;
     int *ab = &sh.abort;
     const bool leader = elect_one();
-    uint32_t it = 0, nq = 0;
+    uint32_t it = 0, nq = 0, turns = 0;
     Uses use;
     Pieces w(p);
     auto wait_stage = [&](uint32_t i) {
@@ -599,11 +599,22 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
             for (int t = 0; t < n; ++t) {
                 const uint32_t iv = it + 1 + 2 * t, ik = iv + 1;
                 if (!ready_v(iv, t)) goto out;
+                // The issuers take turns, a step's products each: one tile's softmax then
+                // runs while the other's products do.  Left alone the tiles fall into step
+                // and the tensor cores idle while both wait for the same units; turns
+                // of the softmax warpgroups do less (2048 tokens over 16K: 471 us
+                // with neither, 400 with those, 381 with these).
+                if (!(turns == 0 && x == 0) &&
+                    !mbar_wait_warp(smem_u32(&sh.turn[x]), (turns + (x ^ 1)) & 1, ab, lim))
+                    goto out;
+                ++turns;
                 if (!pv(x, x, iv, t == 0, 1, use.par(t, 2))) goto out;
                 release(iv, 1);
+                if (t + 1 == n && leader) mbar_arrive(smem_u32(&sh.turn[x ^ 1]));
                 if (t + 1 < n) {
                     if (!wait_stage(ik)) goto out;
                     qk(x, x, ik, 1);
+                    if (leader) mbar_arrive(smem_u32(&sh.turn[x ^ 1]));
                     release(ik, 1);
                     // after the last logits the queries' place is free
                     if (t + 2 == n && leader) mma_commit(smem_u32(&sh.qempty));
@@ -674,7 +685,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
     Cap cap;
     if constexpr (kMore) cap.set(a.scale, a.softcap > 0.f ? a.softcap : 1.f);
     const uint32_t ocol = tmem + lane_base + C::kOutCol + et * D;
-    uint32_t pos_steps = 0, turns = 0, swaps = 0;
+    uint32_t pos_steps = 0, swaps = 0;
     int ahead_tok = -1;  // the token whose range `ahead` is
     int2 ahead = make_int2(0, 0);
     // the two threads of a row meet (the pair of warps does): false after an abort
@@ -878,17 +889,6 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                     }
                 }
             }
-            if (used == 2) {
-                // The warpgroups take their exponentials in turn, so that one computes
-                // while the other's products run: left alone they fall into step, and
-                // the tensor cores idle while both wait for the same units (2048 tokens
-                // over 16K: 471 us without the turns, 407 with them).
-                const bool ok = (turns == 0 && e == 0) || mbar_wait(smem_u32(&sh.turn[e]), (turns + (e ^ 1)) & 1,
-                                                                    &sh.abort, a.wait_limit);
-                __syncwarp();
-                if (!__all_sync(0xffffffffu, ok)) return;
-                ++turns;
-            }
             const float ref = m == -INFINITY ? 0.f : m;
             const uint64_t sc2 = pack2(kMore ? 1.f : sc, kMore ? 1.f : sc), ref2 = pack2(-ref, -ref);
             uint64_t sum[2] = {0, 0};
@@ -905,7 +905,6 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                     pk[i] = pack_pair<kFp16>(z0, z1);
                 }
                 tmem_st16(sb + 16 * (ch0 + c), pk);
-                if (c == 2 && used == 2) mbar_arrive(smem_u32(&sh.turn[e ^ 1]));
                 if (c & 1) {  // the first half's products start while the second is computed
                     tmem_wait_st();
                     tc_fence_before();
@@ -1056,7 +1055,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 mbar_init(smem_u32(&sh.pfull[i][b][1]), 128);
                 mbar_init(smem_u32(&sh.pdone[i][b]), 1);
             }
-            mbar_init(smem_u32(&sh.turn[i]), 128);
+            mbar_init(smem_u32(&sh.turn[i]), 1);
             mbar_init(smem_u32(&sh.pos[i]), 128);
             mbar_init(smem_u32(&sh.fin[i]), 1);
         }

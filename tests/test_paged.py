@@ -548,3 +548,119 @@ def test_python_refusals_on_the_gpu():
     with pytest.raises(up.UpError):
         up.append_kv(q, k, k, pos, m.cu, m.cache, torch.ones(4, device="cuda"))
     assert up.get_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softcap", [2.0, 30.0, 50.0, 400.0])
+@pytest.mark.parametrize("d", [64, 256])
+def test_caps_from_tight_to_wide(d, softcap):
+    """The capped logit's short series, long series and general form."""
+    m = Made([(70, 400), (3, 900)], 2, d, 64, "fp16", seed=11)
+    q = m.normal(m.T, 8, d) * 5
+    out, lse = up.attend_paged(q, m.cu, m.cache, softcap=softcap)
+    own = torch.cat([torch.arange(330, 400), torch.arange(897, 900)]).cuda()
+    zero = torch.zeros_like(own)
+    want = oracle(m, q, zero, own + 1, d ** -0.5, softcap=softcap)
+    check(m, out, lse, want)
+    one = Made([(1, 400), (1, 900)], 2, d, 64, "fp16", seed=12)
+    q = one.normal(2, 8, d) * 5
+    out, lse = up.decode_attend(q, one.cache, softcap=softcap)
+    check(one, out, lse, oracle(one, q, zero[:2], one.kv_lens.long(), d ** -0.5, softcap=softcap))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 0.02])
+def test_any_scale(scale):
+    m = Made([(140, 500)], 2, 128, 32, "bf16", seed=13)
+    q = m.normal(140, 8, 128)
+    own = torch.arange(360, 500).cuda()
+    out, lse = up.attend_paged(q, m.cu, m.cache, scale=scale)
+    check(m, out, lse, oracle(m, q, torch.zeros_like(own), own + 1, scale))
+    out, lse = up.decode_attend(q[-1:].contiguous(), m.cache, scale=scale)
+    check(m, out, lse, tuple(x[-1:] if torch.is_tensor(x) else x
+                             for x in oracle(m, q, torch.zeros_like(own), own + 1, scale)))
+
+
+@pytest.mark.gpu
+def test_more_sequences_than_a_block_has_threads():
+    g = torch.Generator().manual_seed(3)
+    n = torch.randint(0, 4, (1500,), generator=g).tolist()
+    lens = [(a, a + b) for a, b in zip(n, torch.randint(0, 40, (1500,), generator=g).tolist())]
+    m = Made(lens, 2, 64, 16, "bf16", seed=14)
+    q = m.normal(m.T, 4, 64) * 2
+    out, lse = up.attend_paged(q, m.cu, m.cache)
+    own = torch.cat([torch.arange(kv - n, kv) for n, kv in lens]).cuda()
+    check(m, out, lse, oracle(m, q, torch.zeros_like(own), own + 1, 0.125))
+    q = m.normal(1500, 4, 64) * 2
+    out, lse = up.decode_attend(q, m.cache)
+    assert up.get_device_error() == 0
+    m.lens = [(1, kv) for _, kv in lens]
+    check(m, out, lse, oracle(m, q, torch.zeros(1500, dtype=torch.long, device="cuda"), m.kv_lens.long(), 0.125))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk,d", [(32, 8, 128), (16, 2, 256), (24, 3, 64)])
+def test_units_cut_by_shares(Hq, Hk, d):
+    """Enough work for every SM: whole units, units cut in two and units without a token."""
+    lens = [(700, 3000), (1, 20), (0, 64), (33, 2100), (1200, 1200)]
+    m = Made(lens, Hk, d, 128, "bf16", seed=15)
+    q = m.normal(m.T, Hq, d) * 2
+    vis = masks("ragged", lens, 7)
+    vis[300:420] = 0  # units that see nothing
+    own = torch.cat([torch.arange(kv - n, kv) for n, kv in lens]).cuda()
+    for visible in (None, vis):
+        out, lse = up.attend_paged(q, m.cu, m.cache, visible=visible)
+        lo, hi = (torch.zeros_like(own), own + 1) if visible is None else vis.long().unbind(1)
+        check(m, out, lse, oracle(m, q, lo, hi, d ** -0.5))
+    assert up.get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_no_log_sum_asked_for():
+    m = Made([(5, 300), (90, 90)], 2, 64, 32, "bf16", seed=16)
+    q = m.normal(m.T, 8, 64)
+    want, _ = up.attend_paged(q, m.cu, m.cache)
+    L, out = up.lib(), torch.zeros_like(q)
+    ws = torch.empty(up.attend_paged_workspace(m.T, 2, 8, 2, 64), dtype=torch.uint8, device="cuda")
+    lg = ctypes.byref(_CLogits(0.125, 0.0, None, None))
+    stream = torch.cuda.current_stream().cuda_stream
+    assert L.up_attend_paged(q.data_ptr(), m.cu.data_ptr(), m.T, 8, m.cache._ref, lg, None, out.data_ptr(),
+                             None, ws.data_ptr(), ws.numel(), stream) == 0
+    assert torch.equal(out, want)
+    want, _ = up.decode_attend(q[:2].contiguous(), m.cache)
+    assert L.up_decode_attend(q.data_ptr(), 8, m.cache._ref, lg, None, out.data_ptr(), None, ws.data_ptr(),
+                              ws.numel(), stream) == 0
+    assert torch.equal(out[:2], want)
+
+
+@pytest.mark.gpu
+def test_expired_wait_stops_attention_cleanly():
+    """A wait bound of a few cycles: the kernel gives up, reports the timeout and leaves
+    the context usable."""
+    m = Made([(600, 2000)], 8, 128, 64, "bf16", seed=17)
+    q = m.normal(600, 32, 128)
+    want = [x.clone() for x in up.attend_paged(q, m.cu, m.cache)]
+    up.set_wait_limit(64)
+    try:
+        up.attend_paged(q, m.cu, m.cache)
+        assert up.get_device_error() & 0x4
+    finally:
+        up.set_wait_limit(0)
+    for x, y in zip(want, up.attend_paged(q, m.cu, m.cache)):
+        assert torch.equal(x, y)
+    assert up.get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_example_runs_the_operators_together():
+    """Prefill with dropped tokens and captured decode steps; twice the same tokens."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "sparse_prefill_decode.py")
+    spec = importlib.util.spec_from_file_location("sparse_prefill_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    a = ex.main(["--prompt", "700", "333", "--steps", "6"])
+    b = ex.main(["--prompt", "700", "333", "--steps", "6"])
+    assert a == b and len(a) == 2 and all(len(t) == 6 for t in a)
