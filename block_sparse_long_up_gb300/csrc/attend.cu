@@ -47,6 +47,10 @@ constexpr int kMinTiles = 4;      // shares are not cut finer than this: more pa
                                   // 23.6, 22.4 and 26.5 us with 1, 2, 4 and 8)
 constexpr float kSlack = 8.f;     // log2: how far the maximum may grow before a rescale
 constexpr int kPanel = 128 * 128; // 128 rows x 64 elements
+// Tiles' worth of time that a unit costs beside its tiles: without it a share of short
+// units takes far longer than one of long ones (three ragged sequences, 16/2 heads of
+// 256: 380 us with 0, 305 with 2, 287 with 3, 292 with 5)
+constexpr int kUnitCost = 3;
 
 template <int D>
 struct Cfg {
@@ -77,10 +81,10 @@ struct Unit {
     int hi0;            // causal end of the first token's slots
     int kv;             // cached tokens of the sequence
     int pad;
-    int64_t prefix;     // tiles of the units before this one
+    int64_t prefix;     // width of the units before this one
 };
 struct Plan {
-    int64_t W;  // tiles of one KV head
+    int64_t W;  // width of one KV head's units
     int units;
     int pad;
 };
@@ -134,6 +138,10 @@ __device__ __forceinline__ int2 sees(const AttendArgs &a, const Unit &u, int tl)
     if (!a.visible) return make_int2(0, u.hi0 + tl);
     return cut_range(reinterpret_cast<const int2 *>(a.visible)[u.tok0 + tl], u.kv);
 }
+
+// A unit's width in the work laid end to end: its key tiles, and in front of them what
+// beginning and ending it costs (queries, first logits, output).
+__host__ __device__ __forceinline__ int width_of(const Unit &u) { return u.tiles ? u.tiles + kUnitCost : 0; }
 
 constexpr int kPlanThreads = 1024;
 
@@ -252,14 +260,14 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
     for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
         const int64_t i = u0 + tid;
         int64_t total;
-        const int64_t at = block_scan(i < units ? p.units[i].tiles : 0, &total, sh);
+        const int64_t at = block_scan(i < units ? width_of(p.units[i]) : 0, &total, sh);
         if (i < units) p.units[i].prefix = W + at;
         W += total;
     }
     if (tid == 0) *p.plan = Plan{W, (int)units, 0};
 }
 
-// The unit holding tile x (0 <= x < W) of a KV head.
+// The unit at x (0 <= x < W) of a KV head's work.
 __device__ __forceinline__ int find_unit(const Unit *units, int n, int64_t x) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
@@ -275,7 +283,7 @@ struct Pieces {
     Shares sh;
     int64_t W1, at, end;
     int j, ui, n;        // KV head, unit index, units
-    int64_t base;        // tiles of the KV heads before j
+    int64_t base;        // width of the KV heads before j
     Unit u, behind;
     int after = -1;      // the index of `behind`
     int ta, tb;          // tiles [ta, tb) of the unit
@@ -297,27 +305,36 @@ struct Pieces {
         u = pp.units[ui];
     }
     __device__ bool next() {
-        if (at >= end) return false;
-        while (at - base >= u.prefix + u.tiles) {  // units without tiles, or the last one done
-            if (++ui == n) {
-                ui = 0;
-                ++j;
-                base += W1;
+        while (at < end) {
+            while (at - base >= u.prefix + width_of(u)) {  // units without tiles, or the last one done
+                if (++ui == n) {
+                    ui = 0;
+                    ++j;
+                    base += W1;
+                }
+                u = ui == after ? behind : p.units[ui];
             }
-            u = ui == after ? behind : p.units[ui];
+            const int64_t first = base + u.prefix + kUnitCost;  // of the unit's tiles
+            ta = (int)max(at - first, (int64_t)0);
+            tb = (int)min((int64_t)u.tiles, end - first);
+            at = min(end, first + u.tiles);
+            if (ta >= tb) continue;  // the share ends before the unit's first tile
+            ++index;
+            // the next unit's description, on its way while this one is worked on
+            after = ui + 1 < n ? ui + 1 : 0;
+            behind = p.units[after];
+            return true;
         }
-        ta = (int)(at - base - u.prefix);
-        tb = (int)min((int64_t)u.tiles, end - base - u.prefix);
-        at += tb - ta;
-        ++index;
-        // the next unit's description, on its way while this one is worked on
-        after = ui + 1 < n ? ui + 1 : 0;
-        behind = p.units[after];
-        return true;
+        return false;
     }
     __device__ int steps() const { return tb - ta; }
     __device__ int tiles_used() const { return u.ntok > p.tpt ? 2 : 1; }  // row tiles with tokens
-    __device__ int key0(int t) const { return (u.kt0 + ta + t) * kRows; }
+    // First slot of step t.  A distance bias makes the logits grow towards the query, so
+    // with one the steps go from the last key tile to the first: the maximum is then
+    // found at once, instead of growing past the slack at every step.
+    __device__ int key0(int t) const {
+        return (u.kt0 + (p.a.slopes ? u.tiles - 1 - ta - t : ta + t)) * kRows;
+    }
 };
 
 // ---------------------------------------------------------------- shared state
@@ -1131,7 +1148,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params 
     if (!cut.parted) return;
     const Unit u = p.units[cut.unit];
     const int j = cut.j;
-    const int64_t ub = (int64_t)j * pl.W + u.prefix, ue = ub + u.tiles;
+    const int64_t ub = (int64_t)j * pl.W + u.prefix, ue = ub + width_of(u);
     const int n = share_of(sh, ue - 1) - c0 + 1;
     // a block's first piece is in its slot 0, a later one (this unit's first) in slot 1
     const int slot0 = 2 * c0 + (share_begin(sh, c0) < ub);
