@@ -3,8 +3,9 @@
 Each .cu file is compiled in parallel into _build/, then linked with
 ``nvcc -shared``.  A rebuild happens only when a source or header is newer than
 the library.  ``build(checked=True)`` makes the checked variant instead
-(_build_checked/libup_checked.so, compiled with -DUP_CHECK_BOUNDS: every kernel
-tests its index ranges and reports a miss through UP_DEVERR_BOUNDS).
+(_build_checked/libup_checked.so, compiled with -DUP_CHECK_BOUNDS: the kernels of
+the scoring, selection and compaction path test their index ranges and report a
+miss through UP_DEVERR_BOUNDS).
 """
 from __future__ import annotations
 

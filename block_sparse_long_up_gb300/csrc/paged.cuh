@@ -40,7 +40,8 @@ __device__ __forceinline__ int page_of(const PagedKv &c, int s, int slot) {
 // set) when the length cannot be one.
 __device__ __forceinline__ int kv_len_of(const PagedKv &c, int s, int fresh) {
     const int kv = c.kv_lens[s];
-    if (kv < fresh || kv < 0 || kv > (int64_t)c.max_pages * c.page_size) {
+    // (the last 2^16 lengths are left out so that rounding up to tiles stays in 32 bits)
+    if (kv < fresh || kv < 0 || kv > INT32_MAX - 65536 || kv > (int64_t)c.max_pages * c.page_size) {
         atomicOr(c.err, kErrKvLens);
         return -1;
     }

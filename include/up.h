@@ -20,8 +20,8 @@
  *   - Sequences are continuously batched (varlen): `cu_seqlens` is int32
  *     [num_seqs + 1], cu_seqlens[0] = 0, non-decreasing, and
  *     cu_seqlens[num_seqs] = total_tokens.  L_s = cu_seqlens[s+1] - cu_seqlens[s].
- *   - Tensors are token-major, row-major and contiguous; "bf16" buffers hold
- *     IEEE bfloat16 values.
+ *   - Tensors are token-major, row-major and contiguous unless a call says
+ *     otherwise; "bf16" buffers hold IEEE bfloat16 values.
  *   - nb_s = ceil(L_s / G) blocks per sequence; cu_blocks is int32
  *     [num_seqs + 1], the exclusive prefix sum of nb_s.
  *   - Host-checkable arguments are validated before any launch; a rejected
@@ -62,7 +62,8 @@ typedef enum {
 #define UP_DEVERR_TIMEOUT 0x4u         /* a bounded wait inside a kernel gave up */
 #define UP_DEVERR_BAD_PAGE 0x8u        /* a page index outside [0, num_pages) (read as zeros) */
 #define UP_DEVERR_BAD_CU_BLOCKS 0x10u  /* compaction: cu_blocks[num_seqs] < 0 or > total_tokens/G + num_seqs */
-#define UP_DEVERR_BOUNDS 0x20u         /* checked builds only (compiled with -DUP_CHECK_BOUNDS): an index
+#define UP_DEVERR_BOUNDS 0x20u         /* checked builds only (compiled with -DUP_CHECK_BOUNDS; the scoring,
+                                          selection and compaction kernels): an index
                                           range outside its buffer; the access was skipped */
 #define UP_DEVERR_BAD_KV_LENS 0x40u    /* kv_lens[s] negative, below the sequence's new tokens, or above
                                           max_pages * page_size (the sequence is left out) */
@@ -333,7 +334,7 @@ up_status up_compact_noalloc(const void *x, const int32_t *pos, int hidden,
  *                values and positions read as zeros.
  *   kv_lens      int32 [num_seqs]: cached tokens of each sequence, the tokens of
  *                the current call included.  A length outside [new tokens,
- *                max_pages * page_size] sets UP_DEVERR_BAD_KV_LENS: the sequence
+ *                max_pages * page_size], or of 2^31 - 2^16 and more, sets UP_DEVERR_BAD_KV_LENS: the sequence
  *                is not appended to, and its attention output rows are those of
  *                an empty mask.
  *   page_size    a positive multiple of 16 (128 where up_score_blocks_paged reads
@@ -421,11 +422,11 @@ typedef struct {
  *   q        dtype [total_tokens, Hq, d], the new tokens of every sequence, packed
  *            by cu_seqlens (int32 [num_seqs+1]); Hq % Hk == 0, Hq/Hk <= 16; query
  *            head h reads KV head h / (Hq/Hk).
- *   visible  int32 [total_tokens, 2] or NULL: query t sees slots visible[t][0] <= i
+ *   visible  int32 [total_tokens, 2] (8-byte aligned) or NULL: query t sees slots visible[t][0] <= i
  *            < visible[t][1], cut to [0, kv_lens[s]): windows, packed documents and
  *            bidirectional prefixes are such ranges.  NULL: causal, slots up to the
  *            token's own.
- *   out      dtype [total_tokens, Hq, d].
+ *   out      dtype [total_tokens, Hq, d]; may not overlap q.
  *   lse      fp32 [total_tokens, Hq] or NULL: natural log of the softmax's sum.
  *   workspace  up_attend_paged_workspace(...) bytes, 256-byte aligned; its contents
  *            on entry do not matter.
