@@ -452,8 +452,8 @@ def measure_ex2_rate(stream=None) -> float:
 
 
 def set_wait_limit(cycles: int = 0):
-    """Bound, in SM clock cycles, of every spin-wait inside the scoring kernel
-    for scoring calls issued after this one (0: the default, about two
+    """Bound, in SM clock cycles, of every spin-wait inside the scoring and attention
+    kernels for calls issued after this one (0: the default, about two
     seconds).  For tests of the failure path: an expired wait stops the
     kernel cleanly and sets the timeout bit that get_device_error() reports."""
     _check("up_set_wait_limit", lib().up_set_wait_limit(int(cycles)))

@@ -52,7 +52,8 @@ up::PagedKv device_view(const up_paged_kv *c, unsigned int *err) {
 }
 
 up_status check_logits(const up_logits *l, const up_paged_kv *c) {
-    if (!l || !isfinite(l->scale) || !isfinite(l->softcap) || l->softcap < 0.f)
+    if (!l || !isfinite(l->scale) || !isfinite(l->softcap) || l->softcap < 0.f ||
+        (l->softcap > 0.f && l->softcap < 1e-6f))
         return UP_ERR_INVALID_ARG;
     if (l->slopes && (!l->q_pos || !c->pos_pages)) return UP_ERR_INVALID_ARG;
     return UP_OK;

@@ -2,7 +2,8 @@
 //
 // Every new token's query, key and value rows are read once and written once:
 // 2 * (Hq + 2*Hk) * d * 2 bytes a token, which is all there is to do beside
-// rot/2 sines and cosines a token; so memory bounds a prompt and latency a step.
+// rot/2 sines and cosines a token; so memory bounds a prompt and latency a step (32768
+// tokens of 32 + 16 rows of 128: 129 us at 6.2 TB/s; one token: 3.7 us).
 //
 // A block takes a tile of consecutive tokens.  Their angles come first, one
 // thread per (token, frequency), into shared memory: computed once per token and

@@ -13,7 +13,9 @@
 // plan kernel lists the units with their key tiles; all key tiles of all units and
 // KV heads are laid end to end and block c of the grid (one per SM) takes the c-th
 // equal share, so causal, windowed, ragged and few-row batches load every SM alike
-// without the host knowing a length.  A unit cut by a share's end leaves its
+// without the host knowing a length.  2048 tokens over 65536 of 32/8 heads of 128 take
+// 1.44-1.48 ms = 1.46-1.50 PFLOP/s, 0.75-0.77 of the measured burst rate: a chain of
+// products into one accumulator issues one every ~92 cycles instead of 64.  A unit cut by a share's end leaves its
 // running maximum, sum and unnormalised output in the workspace for the join kernel
 // (fixed order: results are reproducible); a whole unit is written by its block.
 //
@@ -80,8 +82,27 @@ struct Unit {
     int kt0, tiles;     // first key tile and how many
     int hi0;            // causal end of the first token's slots
     int kv;             // cached tokens of the sequence
-    int pad;
+    // Slots outside [first, end) no row of the unit sees, and those outside [seen0, seen1)
+    // no new token of the sequence.  All four lie in the unit's first and last key
+    // tile; a byte each: first, end - 1, seen0, seen1 - 1 in its tile (a unit is read
+    // ahead by every role, so its size counts in registers).
+    uint32_t edges;
     int64_t prefix;     // width of the units before this one
+
+    __device__ __forceinline__ int last_tile() const { return (kt0 + tiles - 1) * kRows; }
+    __device__ __forceinline__ int first() const { return kt0 * kRows + (int)(edges & 255u); }
+    __device__ __forceinline__ int end() const { return last_tile() + (int)(edges >> 8 & 255u) + 1; }
+    __device__ __forceinline__ int seen0() const { return kt0 * kRows + (int)(edges >> 16 & 255u); }
+    __device__ __forceinline__ int seen1() const { return last_tile() + (int)(edges >> 24) + 1; }
+    __device__ __forceinline__ void set_seen(int lo, int hi) {
+        const uint32_t a = (uint32_t)max(lo - kt0 * kRows, 0), b = (uint32_t)(min(hi - last_tile(), kRows) - 1);
+        edges = (edges & 0xffffu) | a << 16 | b << 24;
+    }
+    __device__ __forceinline__ void set_range(int lo, int hi) {
+        kt0 = lo / kRows;
+        tiles = (hi + kRows - 1) / kRows - kt0;
+        edges = (uint32_t)(lo - kt0 * kRows) | (uint32_t)(hi - last_tile() - 1) << 8;
+    }
 };
 struct Plan {
     int64_t W;  // width of one KV head's units
@@ -95,7 +116,7 @@ struct Cut {
 };
 
 struct Layout {
-    size_t seq_off, units, cuts, parts, total;
+    size_t seq_off, seen, units, cuts, parts, total;
     int64_t max_units;
 };
 Layout layout_of(int64_t T, int num_seqs, int Hq, int Hk, int d) {
@@ -105,6 +126,7 @@ Layout layout_of(int64_t T, int num_seqs, int Hq, int Hk, int d) {
     size_t off = 256;
     auto take = [&](size_t n) { const size_t at = off; off = (off + n + 255) & ~size_t(255); return at; };
     L.seq_off = take(sizeof(int32_t) * (size_t)(num_seqs + 1));
+    L.seen = take(sizeof(int2) * (size_t)(num_seqs + 1));
     L.units = take(sizeof(Unit) * (size_t)(L.max_units > 0 ? L.max_units : 1));
     L.cuts = take(sizeof(Cut) * kMaxSms);
     L.parts = take((size_t)2 * kMaxSms * tiles * kRows * (size_t)(d + 4) * sizeof(float));
@@ -116,6 +138,7 @@ struct Params {
     AttendArgs a;
     Plan *plan;
     int32_t *seq_off;
+    int2 *seen;  // a sequence's [seen0, seen1)
     Unit *units;
     Cut *cuts;
     float *parts;
@@ -194,7 +217,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         }
         int64_t total;
         const int64_t at = units + block_scan(n, &total, sh);
-        if (s < B) p.seq_off[s] = (int)(at < p.max_units ? at : p.max_units);
+        if (s < B) {
+            p.seq_off[s] = (int)(at < p.max_units ? at : p.max_units);
+            p.seen[s] = make_int2(INT32_MAX, 0);
+        }
         units += total;
     }
     __syncthreads();
@@ -218,7 +244,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         u.ntok = min(tpu, c1 - u.tok0);
         u.kv = kv_len_of(a.kv, lo, c1 - c0);
         u.hi0 = u.kv - (c1 - u.tok0) + 1;
-        if (u.kv >= 0 && !a.visible) u.tiles = (u.hi0 + u.ntok - 1 + kRows - 1) / kRows;
+        if (u.kv >= 0 && !a.visible) {
+            u.set_range(0, u.hi0 + u.ntok - 1);
+            u.set_seen(0, u.kv);
+        }
         p.units[i] = u;
     }
     if (a.visible) {
@@ -249,8 +278,9 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
             for (int k = 0; k < kSame; ++k) {
                 const int lo = __reduce_min_sync(0xffffffffu, first[k]), hi = __reduce_max_sync(0xffffffffu, end[k]);
                 if (lane == k && i0 + k < units && lo < hi) {
-                    p.units[i0 + k].kt0 = lo / kRows;
-                    p.units[i0 + k].tiles = (hi + kRows - 1) / kRows - lo / kRows;
+                    p.units[i0 + k].set_range(lo, hi);
+                    atomicMin(&p.seen[u[k].s].x, lo);
+                    atomicMax(&p.seen[u[k].s].y, hi);
                 }
             }
         }
@@ -261,7 +291,13 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         const int64_t i = u0 + tid;
         int64_t total;
         const int64_t at = block_scan(i < units ? width_of(p.units[i]) : 0, &total, sh);
-        if (i < units) p.units[i].prefix = W + at;
+        if (i < units) {
+            p.units[i].prefix = W + at;
+            if (a.visible && p.units[i].tiles) {
+                const int2 r = __ldcg(p.seen + p.units[i].s);  // where the atomics left it
+                p.units[i].set_seen(r.x, r.y);
+            }
+        }
         W += total;
     }
     if (tid == 0) *p.plan = Plan{W, (int)units, 0};
@@ -417,8 +453,8 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // ---------------------------------------------------------------- roles
 
 // One key or value tile into ring stages it, it+1, ... (kParts of them), by the whole
-// warp: lane l loads the l-th box of 128 / box, from page pg (-1, past the cached
-// tokens or a bad page: a box outside the pool, which reads as zeros).
+// warp: lane l loads the l-th box of 128 / box, from page pg (-1, nothing that a row of
+// the unit sees or a bad page: a box outside the pool, which reads as zeros).
 template <int D>
 __device__ bool load_tile(const CUtensorMap *map, const Params &p, Shared &sh, uint32_t ring, uint32_t &it,
                           const Pieces &w, int key0, int pg) {
@@ -458,7 +494,7 @@ __device__ void role_kv(const CUtensorMap *km, const CUtensorMap *vm, const Para
         // the page of this lane's box, looked up two steps ahead
         auto page = [&](int t) {
             const int key = w.key0(t) + r;
-            return t < n && r < kRows && key < w.u.kv ? page_of(p.a.kv, w.u.s, key) : -1;
+            return t < n && r < kRows && key < w.u.end() && key + p.box > w.u.first() ? page_of(p.a.kv, w.u.s, key) : -1;
         };
         int p0 = page(0), p1 = page(1), p2 = page(2);
         // the order in which the products need them: one tile runs a step ahead with its keys
@@ -504,16 +540,21 @@ __device__ void role_q(const CUtensorMap *qm, const Params &p, Shared &sh, uint3
     if (*(volatile int *)&sh.abort && n) drain(smem_u32(&sh.qfull), (n - 1) & 1);
 }
 
-// Zeros the rows of a value tile in shared memory from slot kv on (what the last page
-// holds there may be anything, and its zero weights would multiply it).
+// Zeros the rows of a value tile in shared memory outside [from, to): slots that no new
+// token sees (they may hold anything, and zero weights would multiply it).  Slots that
+// only this unit's rows do not see hold finite values, by the call's contract: clearing
+// those too cost 3-10 % on ragged prompts.
 template <int D>
-__device__ __forceinline__ void clear_tail(uint32_t stage, int rows_from) {
+__device__ __forceinline__ void clear_unseen(uint32_t stage, int from, int to) {
     using C = Cfg<D>;
     const int lane = threadIdx.x & 31;
-    for (int pn = 0; pn < C::kStagePanels; ++pn)
-        for (int i = rows_from * 8 + lane; i < kRows * 8; i += 32)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stage + pn * kPanel + i * 16), "r"(0)
-                         : "memory");
+    auto zero = [&](uint32_t at) {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+    };
+    for (int pn = 0; pn < C::kStagePanels; ++pn) {
+        for (int i = lane; i < min(from, kRows) * 8; i += 32) zero(stage + pn * kPanel + i * 16);
+        for (int i = max(to, 0) * 8 + lane; i < kRows * 8; i += 32) zero(stage + pn * kPanel + i * 16);
+    }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
 }
@@ -584,13 +625,13 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
         __syncwarp();
         return true;
     };
-    auto ready_v = [&](uint32_t i, int t) {  // the value tile of step t, its tail cleared
+    auto ready_v = [&](uint32_t i, int t) {  // the value tile of step t, what nobody sees cleared
         for (int part = 0; part < C::kParts; ++part)
             if (!wait_stage(i + part)) return false;
-        const int from = w.u.kv - w.key0(t);
-        if (from < kRows)
+        const int from = w.u.seen0() - w.key0(t), to = w.u.seen1() - w.key0(t);
+        if (from > 0 || to < kRows)
             for (int part = 0; part < C::kParts; ++part)
-                clear_tail<D>(ring + ((i + part) % C::kStages) * C::kStageBytes, max(from, 0));
+                clear_unseen<D>(ring + ((i + part) % C::kStages) * C::kStageBytes, from, to);
         return true;
     };
     int before = 0;  // row tiles of the piece before
@@ -745,27 +786,27 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             }
         }
         float m = -INFINITY, l = 0.f;
-        int kp = 0, kp0 = 0;  // positions of this thread's key of the next step and of the step's first
+        int kp = 0, kp0 = 0;  // positions of this thread's key of the next step and of its first seen one
         auto position = [&](int key) {
-            const int pg = key < w.u.kv ? page_of(a.kv, w.u.s, key) : -1;
+            const int pg = key >= w.u.first() && key < w.u.end() ? page_of(a.kv, w.u.s, key) : -1;
             return pg < 0 ? 0 : a.kv.pos[(int64_t)pg * a.kv.page_size + key % a.kv.page_size];
         };
         auto fetch_pos = [&](int t) {
             if constexpr (kMore) {
                 if (a.slopes && t < n) {
                     if (!kSplit || e == 0) kp = position(w.key0(t) + tid);
-                    kp0 = position(w.key0(t));
+                    kp0 = position(max(w.key0(t), w.u.first()));
                 }
             }
         };
         fetch_pos(0);
         for (int t = 0; t < n; ++t) {
             const int buf = use.buf(t, et, used), k0 = w.key0(t);
-            float at = 0.f;  // this row's position relative to the step's first key
+            float at = 0.f;  // this row's position relative to the step's first seen key
             const float *sp = s_pos + (2 * et + (pos_steps & 1)) * 128;
             if constexpr (kMore) {
                 if (a.slopes) {
-                    // positions relative to the step's first one: exact in fp32, and so are
+                    // positions relative to the step's first seen one: exact in fp32, and so are
                     // their distances, up to 2^24.  Two buffers: a thread writes one again
                     // only when all have come past the step between.
                     at = (float)(qp - kp0);
@@ -1094,7 +1135,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t tmem = sh.tmem;
     pdl_wait();
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        // 128 * 88 + 256 * 208 and 128 * 112 + 256 * 192 are at most 384 * 168
+        if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
             role_kv<D>(&km, &vm, p, sh, ring);
         } else if (warp == 2) {
@@ -1104,8 +1147,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         __syncwarp();
     } else {
-        // 128 * 88 + 256 * 208 <= 384 * 168
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         role_softmax<kFp16, D, kMore>(p, sh, s_out, s_pos, s_xch, tmem, (warp - 4) >> 2);
     }
     tc_fence_before();
@@ -1243,6 +1286,7 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     char *ws = static_cast<char *>(a.workspace);
     p.plan = reinterpret_cast<Plan *>(ws);
     p.seq_off = reinterpret_cast<int32_t *>(ws + L.seq_off);
+    p.seen = reinterpret_cast<int2 *>(ws + L.seen);
     p.units = reinterpret_cast<Unit *>(ws + L.units);
     p.cuts = reinterpret_cast<Cut *>(ws + L.cuts);
     p.parts = reinterpret_cast<float *>(ws + L.parts);

@@ -78,7 +78,8 @@ class PagedKV:
     [num_seqs] (cached tokens, those of the current call included) and, where
     positions matter, pos_pages int32 [num_pages, page_size].  Holds the tensors;
     their contents may change between calls (an engine adds to kv_lens and to
-    block_table in place)."""
+    block_table in place), the attributes may not: other tensors are another
+    PagedKV."""
 
     __slots__ = ("k_pages", "v_pages", "block_table", "kv_lens", "pos_pages", "num_seqs", "Hk",
                  "d", "page_size", "dtype", "device", "_c", "_ref")
@@ -101,15 +102,26 @@ class PagedKV:
         _need(kv_lens, "kv_lens", torch.int32, dev, (b,))
         if pos_pages is not None:
             _need(pos_pages, "pos_pages", torch.int32, dev, (n, ps))
-        self.k_pages, self.v_pages, self.pos_pages = k_pages, v_pages, pos_pages
-        self.block_table, self.kv_lens = block_table, kv_lens
-        self.num_seqs, self.Hk, self.d, self.page_size = b, hk, d, ps
-        self.dtype, self.device = dt, dev
-        self._c = _CKv(k_pages.data_ptr(), v_pages.data_ptr(),
-                       None if pos_pages is None else pos_pages.data_ptr(),
-                       block_table.data_ptr(), kv_lens.data_ptr(), n, b, mp, ps, hk, d,
-                       DTYPES[dt])
-        self._ref = ctypes.byref(self._c)
+        c = _CKv(k_pages.data_ptr(), v_pages.data_ptr(),
+                 None if pos_pages is None else pos_pages.data_ptr(), block_table.data_ptr(),
+                 kv_lens.data_ptr(), n, b, mp, ps, hk, d, DTYPES[dt])
+        put = object.__setattr__
+        put(self, "k_pages", k_pages)
+        put(self, "v_pages", v_pages)
+        put(self, "pos_pages", pos_pages)
+        put(self, "block_table", block_table)
+        put(self, "kv_lens", kv_lens)
+        put(self, "num_seqs", b)
+        put(self, "Hk", hk)
+        put(self, "d", d)
+        put(self, "page_size", ps)
+        put(self, "dtype", dt)
+        put(self, "device", dev)
+        put(self, "_c", c)
+        put(self, "_ref", ctypes.byref(c))
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a PagedKV's tensors do not change: make another one")
 
 
 def _on(stream):

@@ -400,13 +400,15 @@ up_status up_append_kv(const void *q, int64_t q_stride, const void *k, int64_t k
 /*
  * How attention turns a query-key product into a logit, and what a query sees.
  *   scale     logits are scale * (q . k) ...
- *   softcap   ... then softcap * tanh(logit / softcap) when softcap > 0 ...
+ *   softcap   ... then softcap * tanh(logit / softcap) when softcap > 0 (1e-6 and
+ *             more) ...
  *   slopes    fp32 [Hq] or NULL: ... then minus slopes[h] * |q_pos - pos_pages|
  *             (needs q_pos and the cache's pos_pages) ...
  *   q_pos     int32 [queries] or NULL.
  * Softmax is over the visible slots only; a query that sees none gives zeros and
- * a log-sum of -infinity.  What is stored in slots from kv_lens[s] on, and in
- * pages that no visible slot names, has no effect, infinities and NaN included.
+ * a log-sum of -infinity.  What is stored in slots that no query of the call sees has
+ * no effect, infinities and NaN included, and pages without a visible slot need no
+ * valid entry in the block table.
  */
 typedef struct {
     float scale;
@@ -431,9 +433,10 @@ typedef struct {
  *   workspace  up_attend_paged_workspace(...) bytes, 256-byte aligned; its contents
  *            on entry do not matter.
  * A cached value that some query of the call may not see but another one may
- * has to be finite (its zero weight multiplies it).  Results are deterministic.
+ * has to be finite (its zero weight multiplies it).  Results are deterministic on
+ * a given GPU model (the parts' boundaries depend on its number of SMs).
  * Errors: as above; UP_ERR_INVALID_ARG for slopes without q_pos or pos_pages, a
- * softcap below 0 or a non-finite scale or softcap.
+ * softcap below 0 or between 0 and 1e-6, or a non-finite scale or softcap.
  */
 size_t up_attend_paged_workspace(int64_t total_tokens, int num_seqs, int Hq, int Hk, int d);
 
@@ -486,14 +489,14 @@ up_status up_measure_ex2_rate(double *ex2_per_second, up_stream_t stream);
 
 /*
  * Instrumentation for tests of the failure path: every spin-wait inside the
- * tensor-core scoring kernel (a role waiting for shared-memory data, a free
- * TMEM buffer or another CTA's results) gives up after `cycles` SM clock
+ * tensor-core scoring and attention kernels (a role waiting for shared-memory data,
+ * a free TMEM buffer or another CTA's results) gives up after `cycles` SM clock
  * cycles; the kernel then stops every role of the CTA, lets its copies and
  * MMAs in flight complete, frees its tensor memory, returns and sets
  * UP_DEVERR_TIMEOUT (the call's outputs are then unspecified).  0 restores
  * the default bound (4e9 cycles, about two seconds); a bound above the
  * default returns UP_ERR_INVALID_ARG.  Process-wide; it applies to scoring
- * calls issued after it.  Not part of the method; no page counterpart.
+ * and attention calls issued after it.  Not part of the method; no page counterpart.
  */
 up_status up_set_wait_limit(uint64_t cycles);
 

@@ -80,7 +80,8 @@ def test_attend_refusals(L):
         for bad in (dict(q=None), dict(out=None), dict(q=264), dict(out=264), dict(lse=258),
                     dict(Hq=0), dict(Hq=7), dict(Hq=-8), dict(lg=(math.inf, 0.0, None, None)),
                     dict(lg=(math.nan, 0.0, None, None)), dict(lg=(0.1, -1.0, None, None)),
-                    dict(lg=(0.1, math.inf, None, None)), dict(lg=(0.1, 0.0, 256, None)),
+                    dict(lg=(0.1, math.inf, None, None)), dict(lg=(0.1, 1e-7, None, None)),
+                    dict(lg=(0.1, 0.0, 256, None)),
                     dict(lg=(0.1, 0.0, 256, 256), cache=_cache(pos=None))):
             assert call(L, **bad) == 1, bad
         assert call(L, Hq=64) == 2  # 32 query heads on a KV head
@@ -664,3 +665,50 @@ def test_example_runs_the_operators_together():
     a = ex.main(["--prompt", "700", "333", "--steps", "6"])
     b = ex.main(["--prompt", "700", "333", "--steps", "6"])
     assert a == b and len(a) == 2 and all(len(t) == 6 for t in a)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 48)])
+def test_what_nobody_sees_may_be_anything(d, page, bias):
+    """A window's old pages may be gone from the table and hold NaN, and so may the slots
+    around the ranges that queries see."""
+    lens = [(40, 700), (90, 1500)]
+    m = Made(lens, 2, d, page, "bf16", seed=18)
+    q = m.normal(m.T, 8, d) * 2
+    own = torch.cat([torch.arange(kv - n, kv) for n, kv in lens]).cuda()
+    lo, hi = own - 333, own - 5
+    vis = torch.stack([lo, hi], 1).to(torch.int32)
+    kw = {}
+    if bias:
+        kw = dict(slopes=torch.linspace(0.01, 0.001, 8, device="cuda"),
+                  q_pos=torch.cat([m.tokens(s, m.pp)[kv - n:] for s, (n, kv) in enumerate(lens)]).contiguous())
+    want = oracle(m, q, lo.clamp(min=0), hi, d ** -0.5, **kw)
+    t0 = 0
+    for s, (n, kv) in enumerate(lens):
+        first, end = int(lo[t0]), int(hi[t0 + n - 1])
+        i = torch.cat([torch.arange(first), torch.arange(end, kv)]).cuda()
+        at = m.table[s].long()[i // page]
+        m.kp[at, :, i % page] = math.nan
+        m.vp[at, :, i % page] = math.nan
+        m.table[s, :first // page] = -1
+        t0 += n
+    out, lse = up.attend_paged(q, m.cu, m.cache, visible=vis, **kw)
+    assert up.get_device_error() == 0
+    check(m, out, lse, want)
+    start = torch.tensor([700 - 300, 1500 - 300], dtype=torch.int32, device="cuda")
+    m2 = Made([(1, 700), (1, 1500)], 2, d, page, "bf16", seed=18)
+    q = m2.normal(2, 8, d)
+    want = oracle(m2, q, start.long(), m2.kv_lens.long(), d ** -0.5)
+    for s in range(2):
+        m2.table[s, :int(start[s]) // page] = 1 << 30
+    out, lse = up.decode_attend(q, m2.cache, kv_start=start)
+    assert up.get_device_error() == 0
+    check(m2, out, lse, want)
+
+
+@pytest.mark.gpu
+def test_a_cache_does_not_change_its_tensors():
+    m = Made([(1, 20)], 2, 64, 16, "bf16")
+    with pytest.raises(AttributeError):
+        m.cache.kv_lens = m.kv_lens + 1
