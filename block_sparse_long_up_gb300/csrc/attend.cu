@@ -492,9 +492,10 @@ __device__ void role_kv(const CUtensorMap *km, const CUtensorMap *vm, const Para
     while (ok && w.next()) {
         const int n = w.steps();
         // the page of this lane's box, looked up two steps ahead
+        const int from = w.u.first() - p.box, end = w.u.end();
         auto page = [&](int t) {
             const int key = w.key0(t) + r;
-            return t < n && r < kRows && key < w.u.end() && key + p.box > w.u.first() ? page_of(p.a.kv, w.u.s, key) : -1;
+            return t < n && r < kRows && key < end && key > from ? page_of(p.a.kv, w.u.s, key) : -1;
         };
         int p0 = page(0), p1 = page(1), p2 = page(2);
         // the order in which the products need them: one tile runs a step ahead with its keys
@@ -625,18 +626,24 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
         __syncwarp();
         return true;
     };
+    int edge0 = -1, edge1 = -1;  // first slots of this piece's tiles with something to clear
     auto ready_v = [&](uint32_t i, int t) {  // the value tile of step t, what nobody sees cleared
         for (int part = 0; part < C::kParts; ++part)
             if (!wait_stage(i + part)) return false;
-        const int from = w.u.seen0() - w.key0(t), to = w.u.seen1() - w.key0(t);
-        if (from > 0 || to < kRows)
+        // only the unit's first and last key tile can hold such slots
+        const int key0 = w.key0(t);
+        if (key0 == edge0 || key0 == edge1) {
+            const int from = w.u.seen0() - key0, to = w.u.seen1() - key0;
             for (int part = 0; part < C::kParts; ++part)
                 clear_unseen<D>(ring + ((i + part) % C::kStages) * C::kStageBytes, from, to);
+        }
         return true;
     };
     int before = 0;  // row tiles of the piece before
     while (w.next()) {
         const int n = w.steps(), used = C::kTiles == 1 ? 1 : w.tiles_used();
+        edge0 = (w.u.edges >> 16 & 255u) ? w.u.kt0 * kRows : -1;
+        edge1 = (w.u.edges >> 24) != kRows - 1 ? w.u.last_tile() : -1;
         if (!mbar_wait_warp(smem_u32(&sh.qfull), nq & 1, ab, lim)) goto out;
         // Between two pieces of two tiles each issuer's own order keeps its S buffer
         // safe, between two of one tile the buffers' turns do; where the kind
@@ -787,15 +794,16 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
         }
         float m = -INFINITY, l = 0.f;
         int kp = 0, kp0 = 0;  // positions of this thread's key of the next step and of its first seen one
+        const int first = w.u.first(), end = w.u.end();
         auto position = [&](int key) {
-            const int pg = key >= w.u.first() && key < w.u.end() ? page_of(a.kv, w.u.s, key) : -1;
+            const int pg = key >= first && key < end ? page_of(a.kv, w.u.s, key) : -1;
             return pg < 0 ? 0 : a.kv.pos[(int64_t)pg * a.kv.page_size + key % a.kv.page_size];
         };
         auto fetch_pos = [&](int t) {
             if constexpr (kMore) {
                 if (a.slopes && t < n) {
                     if (!kSplit || e == 0) kp = position(w.key0(t) + tid);
-                    kp0 = position(max(w.key0(t), w.u.first()));
+                    kp0 = position(max(w.key0(t), first));
                 }
             }
         };
