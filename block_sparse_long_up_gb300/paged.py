@@ -8,6 +8,7 @@ decode attention over it (the paged-cache section of include/up.h).
 """
 from __future__ import annotations
 
+import collections
 import contextlib
 import ctypes
 import functools
@@ -72,7 +73,11 @@ def _need(t, name, dtype, device, shape=None):
         _refuse(t, name, dtype, device, shape)
 
 
-class PagedKV:
+_Fields = collections.namedtuple("_Fields", "k_pages v_pages block_table kv_lens pos_pages num_seqs "
+                                 "Hk d page_size dtype device struct ref")
+
+
+class PagedKV(_Fields):
     """A paged KV-head-major cache: k_pages and v_pages [num_pages, Hk, page_size, d]
     (bf16 or fp16), block_table int32 [num_seqs, max_pages], kv_lens int32
     [num_seqs] (cached tokens, those of the current call included) and, where
@@ -81,10 +86,9 @@ class PagedKV:
     block_table in place), the attributes may not: other tensors are another
     PagedKV."""
 
-    __slots__ = ("k_pages", "v_pages", "block_table", "kv_lens", "pos_pages", "num_seqs", "Hk",
-                 "d", "page_size", "dtype", "device", "_c", "_ref")
+    __slots__ = ()
 
-    def __init__(self, k_pages, v_pages, block_table, kv_lens, pos_pages=None):
+    def __new__(cls, k_pages, v_pages, block_table, kv_lens, pos_pages=None):
         if not isinstance(k_pages, torch.Tensor):
             raise TypeError("k_pages must be a torch.Tensor")
         dt, dev = k_pages.dtype, k_pages.device
@@ -105,23 +109,12 @@ class PagedKV:
         c = _CKv(k_pages.data_ptr(), v_pages.data_ptr(),
                  None if pos_pages is None else pos_pages.data_ptr(), block_table.data_ptr(),
                  kv_lens.data_ptr(), n, b, mp, ps, hk, d, DTYPES[dt])
-        put = object.__setattr__
-        put(self, "k_pages", k_pages)
-        put(self, "v_pages", v_pages)
-        put(self, "pos_pages", pos_pages)
-        put(self, "block_table", block_table)
-        put(self, "kv_lens", kv_lens)
-        put(self, "num_seqs", b)
-        put(self, "Hk", hk)
-        put(self, "d", d)
-        put(self, "page_size", ps)
-        put(self, "dtype", dt)
-        put(self, "device", dev)
-        put(self, "_c", c)
-        put(self, "_ref", ctypes.byref(c))
+        return tuple.__new__(cls, (k_pages, v_pages, block_table, kv_lens, pos_pages, b, hk, d, ps, dt,
+                                   dev, c, ctypes.byref(c)))
 
-    def __setattr__(self, name, value):
-        raise AttributeError("a PagedKV's tensors do not change: make another one")
+    def __repr__(self):
+        return (f"PagedKV({self.k_pages.shape[0]} pages of {self.page_size} slots, {self.Hk} heads of "
+                f"{self.d}, {self.dtype}, {self.num_seqs} sequences)")
 
 
 def _on(stream):
@@ -205,7 +198,7 @@ def append_kv(q, k, v, pos, cu_seqlens, cache, inv_freq, axes=None, interleaved=
             None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
             pos.data_ptr(), A, None if axes is None else axes.data_ptr(),
             None if inv_freq is None else inv_freq.data_ptr(), rot,
-            ROPE_INTERLEAVED if interleaved else 0, cu_seqlens.data_ptr(), T, Hq, cache._ref,
+            ROPE_INTERLEAVED if interleaved else 0, cu_seqlens.data_ptr(), T, Hq, cache.ref,
             None if q is None else q_out.data_ptr(), _raw(stream, dev))
     if st:
         raise _error("up_append_kv", st)
@@ -282,7 +275,7 @@ def attend_paged(q, cu_seqlens, cache, scale=None, softcap=0.0, slopes=None, q_p
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         else:
             size = workspace.numel() * workspace.element_size()
-        st = _L().up_attend_paged(q.data_ptr(), cu_seqlens.data_ptr(), T, Hq, cache._ref, lg,
+        st = _L().up_attend_paged(q.data_ptr(), cu_seqlens.data_ptr(), T, Hq, cache.ref, lg,
                              None if visible is None else visible.data_ptr(),
                              out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
                              _raw(stream, dev))
@@ -318,7 +311,7 @@ def decode_attend(q, cache, scale=None, softcap=0.0, slopes=None, q_pos=None, kv
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         else:
             size = workspace.numel() * workspace.element_size()
-        st = _L().up_decode_attend(q.data_ptr(), Hq, cache._ref, lg,
+        st = _L().up_decode_attend(q.data_ptr(), Hq, cache.ref, lg,
                              None if kv_start is None else kv_start.data_ptr(),
                              out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
                              _raw(stream, dev))

@@ -625,11 +625,11 @@ def test_no_log_sum_asked_for():
     ws = torch.empty(up.attend_paged_workspace(m.T, 2, 8, 2, 64), dtype=torch.uint8, device="cuda")
     lg = ctypes.byref(_CLogits(0.125, 0.0, None, None))
     stream = torch.cuda.current_stream().cuda_stream
-    assert L.up_attend_paged(q.data_ptr(), m.cu.data_ptr(), m.T, 8, m.cache._ref, lg, None, out.data_ptr(),
+    assert L.up_attend_paged(q.data_ptr(), m.cu.data_ptr(), m.T, 8, m.cache.ref, lg, None, out.data_ptr(),
                              None, ws.data_ptr(), ws.numel(), stream) == 0
     assert torch.equal(out, want)
     want, _ = up.decode_attend(q[:2].contiguous(), m.cache)
-    assert L.up_decode_attend(q.data_ptr(), 8, m.cache._ref, lg, None, out.data_ptr(), None, ws.data_ptr(),
+    assert L.up_decode_attend(q.data_ptr(), 8, m.cache.ref, lg, None, out.data_ptr(), None, ws.data_ptr(),
                               ws.numel(), stream) == 0
     assert torch.equal(out[:2], want)
 
