@@ -14,7 +14,7 @@
 // KV heads are laid end to end and block c of the grid (one per SM) takes the c-th
 // equal share, so causal, windowed, ragged and few-row batches load every SM alike
 // without the host knowing a length.  2048 tokens over 65536 of 32/8 heads of 128 take
-// 1.44-1.48 ms = 1.46-1.50 PFLOP/s, 0.75-0.77 of the measured burst rate: a chain of
+// 1.44-1.54 ms = 1.4-1.5 PFLOP/s, 0.73-0.77 of the measured burst rate: a chain of
 // products into one accumulator issues one every ~92 cycles instead of 64.  A unit cut by a share's end leaves its
 // running maximum, sum and unnormalised output in the workspace for the join kernel
 // (fixed order: results are reproducible); a whole unit is written by its block.
