@@ -22,7 +22,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxTokens = 32;   // tokens of a tile
 constexpr int kMaxHalf = 128;    // rot / 2
 constexpr int kAngles = 2048;    // angles of a tile
-constexpr int kUnits = 3072;     // units of a tile: 12 a thread
+constexpr int kUnits = 12 * kThreads;  // units of a tile
 constexpr int kInFlight = 4;     // units a thread loads before it stores any
 
 // inv_freq in turns a position, as a multiple of 2^-64 turns; its product with a
