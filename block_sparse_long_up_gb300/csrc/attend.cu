@@ -756,7 +756,8 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
     // the two threads of a row meet (the pair of warps does): false after an abort
     auto meet = [&]() {
         const uint32_t bar = smem_u32(&sh.xch[quarter]);
-        mbar_arrive(bar);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
         const bool ok = mbar_wait(bar, swaps & 1, &sh.abort, a.wait_limit);
         __syncwarp();
         ++swaps;
@@ -910,12 +911,14 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             }
             if constexpr (!kMore) mt *= sc;
             if constexpr (kSplit) {
-                // both threads of the row need one reference: the larger of their maxima,
-                // rounded to 16 bits (any value near the maximum does)
-                __nv_bfloat16 *x = reinterpret_cast<__nv_bfloat16 *>(s_xch) + (swaps & 1) * 256;
-                x[e * 128 + tid] = __float2bfloat16_rn(mt);
+                // Both threads of the row need one reference: the larger of their maxima, in all its
+                // bits (a maximum rounded to 16 bits is off by a part of itself, and weights
+                // by 2^that: beyond both types for the far keys of a distance bias).
+                float *x = reinterpret_cast<float *>(s_xch);
+                x[e * 128 + tid] = mt;
                 if (!meet()) return;
-                mt = fmaxf(__bfloat162float(x[tid]), __bfloat162float(x[128 + tid]));
+                mt = fmaxf(x[tid], x[128 + tid]);
+                if (!meet()) return;  // read before the place is written again
             }
             const bool grew = mt > m + kSlack;
             if (__any_sync(0xffffffffu, grew)) {
@@ -1113,7 +1116,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         mbar_init(smem_u32(&sh.qfull), 1);
         mbar_init(smem_u32(&sh.qempty), 2);
         mbar_init(smem_u32(&sh.pieces), 2);
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.xch[i]), 64);
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.xch[i]), 2);
         for (int i = 0; i < 2; ++i) {
             for (int b = 0; b < 2; ++b) {
                 mbar_init(smem_u32(&sh.sfull[i][b]), 1);

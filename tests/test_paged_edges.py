@@ -1,0 +1,75 @@
+"""The paged-cache operators at the edges of their ranges: logits of thousands, light weights,
+ranges with gaps, tight caps, what must not reach a result, and a cache's identity."""
+import math
+
+import pytest
+import torch
+
+import block_sparse_long_up_gb300 as up
+from test_paged import Made, oracle
+
+
+def check_at(m, got, lse, want, content=32.0, floor=0.0):
+    """The result against 64 bits where logits are far from zero.  Each weight and the
+    result are rounded to the cache's type (half a step each).  A logit of a key whose weight
+    counts (2^-40 of the row's largest and more) lies within 28 of the largest one, which
+    lies within the log of the keys' number of the log-sum; before its bias it is
+    `content` at most.  The tensor cores add d / 16 times with 23 bits kept, the rest is a few
+    roundings of 2^-24: 2^-18 of the logit's size in all, in the exponent.  `floor`: what
+    the type's smallest steps leave of weights that are far below the largest."""
+    out, mag, ref, _ = want
+    assert torch.isfinite(got).all()
+    empty = ref == -math.inf
+    assert torch.equal(lse == -math.inf, empty)
+    near = torch.where(empty, torch.zeros_like(ref), ref).abs() + 28 + math.log(max(kv for _, kv in m.lens) + 1) + content
+    half = torch.finfo(m.dt).eps / 2
+    tol = half * (mag + out.abs()) + (2.0 ** -12 + 2.0 ** -18 * near[..., None]) * mag + floor + torch.finfo(m.dt).tiny
+    err = (got.double() - out).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    e = ((lse.double() - ref).abs() / (2.0 ** -18 * (near + 16)))[~empty]
+    assert e.numel() == 0 or float(e.max()) <= 1.0, float(e.max())
+
+
+# ------------------------------------------------------------------ logits far from zero
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("steepest", [0.125, 0.5, 0.7])
+@pytest.mark.parametrize("n,kv", [(40, 16384), (512, 16384), (3, 131072)])
+@pytest.mark.parametrize("d,dtype", [(256, "fp16"), (256, "bf16"), (128, "fp16")])
+def test_steep_biases_over_long_caches(d, dtype, n, kv, steepest):
+    """Parts of a cut unit hold only keys whose biased logits are tens of thousands below the row's."""
+    m = Made([(n, kv)], 2, d, 64, dtype, seed=n)
+    q = m.normal(n, 16, d) * 2
+    kw = dict(slopes=torch.linspace(steepest, steepest / 8, 16, device="cuda"),
+              q_pos=m.tokens(0, m.pp)[kv - n:].contiguous())
+    own = torch.arange(kv - n, kv, device="cuda")
+    out, lse = up.attend_paged(q, m.cu, m.cache, **kw)
+    check_at(m, out, lse, oracle(m, q, torch.zeros_like(own), own + 1, d ** -0.5, **kw))
+    # rows that see only far keys
+    vis = torch.stack([own * 0 + 5, own * 0 + 205], 1).to(torch.int32)
+    out, lse = up.attend_paged(q, m.cu, m.cache, visible=vis, **kw)
+    check_at(m, out, lse, oracle(m, q, vis[:, 0].long(), vis[:, 1].long(), d ** -0.5, **kw))
+    one = dict(kw, q_pos=kw["q_pos"][-1:].contiguous())
+    m.lens = [(1, kv)]
+    out, lse = up.decode_attend(q[-1:].contiguous(), m.cache, **one)
+    check_at(m, out, lse, oracle(m, q[-1:], own[-1:] * 0, own[-1:] + 1, d ** -0.5, **one))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_logits_of_thousands(d, dtype):
+    """Logits of 6000 and -6000 with differences of a few, without a bias."""
+    m = Made([(30, 700), (200, 1400)], 2, d, 64, dtype, seed=21)
+    for s in range(2):
+        i = torch.arange(m.lens[s][1], device="cuda")
+        at, row = m.table[s].long()[i // 64], i % 64
+        m.kp[at, :, row] = (15 + 0.1 * m.kp[at, :, row].float()).to(m.dt)
+    size = torch.linspace(-25, 25, 16, device="cuda") * (256 / d) ** 0.5
+    q = size.to(m.dt)[None, :, None].expand(m.T, 16, d).contiguous()
+    own = torch.cat([torch.arange(kv - n, kv) for n, kv in m.lens]).cuda()
+    out, lse = up.attend_paged(q, m.cu, m.cache)
+    check_at(m, out, lse, oracle(m, q, torch.zeros_like(own), own + 1, d ** -0.5))
+    m.lens = [(1, 700), (1, 1400)]
+    out, lse = up.decode_attend(q[:2].contiguous(), m.cache)
+    check_at(m, out, lse, oracle(m, q[:2], own[:2] * 0, m.kv_lens.long(), d ** -0.5))
