@@ -82,8 +82,8 @@ struct Unit {
     int kt0, tiles;     // first key tile and how many
     int hi0;            // causal end of the first token's slots
     int kv;             // cached tokens of the sequence
-    // Slots outside [first, end) no row of the unit sees, and those outside [seen0, seen1)
-    // no new token of the sequence.  All four lie in the unit's first and last key
+    // The slots that rows of the unit see are [first, end), without gaps.  Slots outside
+    // [seen0, seen1) may hold anything.  All four lie in the unit's first and last key
     // tile; a byte each: first, end - 1, seen0, seen1 - 1 in its tile (a unit is read
     // ahead by every role, so its size counts in registers).
     uint32_t edges;
@@ -116,7 +116,7 @@ struct Cut {
 };
 
 struct Layout {
-    size_t seq_off, seen, units, cuts, parts, total;
+    size_t seq_off, seen, units, whole, cuts, parts, total;
     int64_t max_units;
 };
 Layout layout_of(int64_t T, int num_seqs, int Hq, int Hk, int d) {
@@ -126,8 +126,9 @@ Layout layout_of(int64_t T, int num_seqs, int Hq, int Hk, int d) {
     size_t off = 256;
     auto take = [&](size_t n) { const size_t at = off; off = (off + n + 255) & ~size_t(255); return at; };
     L.seq_off = take(sizeof(int32_t) * (size_t)(num_seqs + 1));
-    L.seen = take(sizeof(int2) * (size_t)(num_seqs + 1));
-    L.units = take(sizeof(Unit) * (size_t)(L.max_units > 0 ? L.max_units : 1));
+    L.seen = take(sizeof(int4) * (size_t)(num_seqs + 1));
+    L.units = take(sizeof(Unit) * (size_t)(T > 0 ? T : 1));  // split at every token at worst
+    L.whole = take(sizeof(Unit) * (size_t)(L.max_units > 0 ? L.max_units : 1));
     L.cuts = take(sizeof(Cut) * kMaxSms);
     L.parts = take((size_t)2 * kMaxSms * tiles * kRows * (size_t)(d + 4) * sizeof(float));
     L.total = off;
@@ -138,8 +139,9 @@ struct Params {
     AttendArgs a;
     Plan *plan;
     int32_t *seq_off;
-    int2 *seen;  // a sequence's [seen0, seen1)
+    int4 *seen;    // the slots that a sequence's tokens see lie in [x, y); z: with gaps
     Unit *units;
+    Unit *whole;   // the units before some were split
     Cut *cuts;
     float *parts;
     int64_t max_units;
@@ -195,14 +197,114 @@ __device__ int64_t block_scan(int64_t v, int64_t *total, int64_t *sh) {
     return before;
 }
 
+// The range of the last token with one before this lane's: among the round's (one a lane)
+// or, where there is none, `last`, which is then moved behind the round.  Empty ranges have y = 0.
+__device__ __forceinline__ int2 range_before(int2 r, int2 &last) {
+    const int lane = threadIdx.x & 31;
+    const unsigned some = __ballot_sync(0xffffffffu, r.y > 0), below = some & ((1u << lane) - 1u);
+    const int from = below ? 31 - __clz(below) : 0, to = some ? 31 - __clz(some) : 0;
+    int2 b = make_int2(__shfl_sync(0xffffffffu, r.x, from), __shfl_sync(0xffffffffu, r.y, from));
+    if (!below) b = last;
+    const int2 end = make_int2(__shfl_sync(0xffffffffu, r.x, to), __shfl_sync(0xffffffffu, r.y, to));
+    if (some) last = end;
+    return b;
+}
+// Neither empty, and slots between them that are in neither.
+__device__ __forceinline__ bool apart(int2 a, int2 b) {
+    return a.y > 0 && b.y > 0 && max(a.x, b.x) > min(a.y, b.y);
+}
+
+// Splits the units where a token's range lies apart from the one before it and finds the
+// sequences with gaps; returns the units' number (T at most: a unit has a token).  Out of line,
+// so that the plans that do not need it stay short (128 tokens over 4K: 24 us inline, 23).
+__device__ __noinline__ int64_t split_units(const Params &p, int64_t units, int tpu, int64_t *sh) {
+    const AttendArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto range_of = [&](const Unit &u, int tl) {
+        return tl < u.ntok && u.kv >= 0 ? sees(a, u, tl) : make_int2(INT32_MAX, 0);
+    };
+    for (int64_t i = tid; i < units; i += kPlanThreads) p.whole[i] = p.units[i];
+    __syncthreads();
+    for (int64_t i = warp; i < units; i += kPlanThreads / 32) {
+        const Unit u = p.whole[i];
+        int n = 1;
+        int2 last = make_int2(INT32_MAX, 0);
+        for (int t0 = 0; t0 < u.ntok; t0 += 32) {
+            const int2 r = range_of(u, t0 + lane), b = range_before(r, last);
+            n += __popc(__ballot_sync(0xffffffffu, apart(r, b)));
+        }
+        if (lane == 0) p.whole[i].prefix = n;
+    }
+    __syncthreads();
+    int64_t all = 0;
+    for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
+        const int64_t i = u0 + tid;
+        int64_t total;
+        const int64_t at = block_scan(i < units ? p.whole[i].prefix : 0, &total, sh);
+        if (i < units) p.whole[i].prefix = all + at;
+        all += total;
+    }
+    __syncthreads();
+    for (int64_t i = warp; i < units; i += kPlanThreads / 32) {
+        Unit u = p.whole[i];
+        int64_t at = u.prefix;
+        const int tok0 = u.tok0, end = u.tok0 + u.ntok;
+        int2 last = make_int2(INT32_MAX, 0);
+        for (int t0 = 0; t0 < end - tok0; t0 += 32) {
+            u.tok0 = tok0, u.ntok = end - tok0;
+            const int2 r = range_of(u, t0 + lane), b = range_before(r, last);
+            const bool starts = t0 + lane == 0 || apart(r, b);
+            const unsigned m = __ballot_sync(0xffffffffu, starts);
+            if (starts) {
+                u.tok0 = tok0 + t0 + lane;
+                u.ntok = end - u.tok0;  // up to the next one's first token, see below
+                p.units[at + __popc(m & ((1u << lane) - 1u))] = u;
+            }
+            at += __popc(m);
+        }
+    }
+    __syncthreads();
+    for (int64_t i = warp; i < all; i += kPlanThreads / 32) {
+        Unit u = p.units[i];
+        if (i + 1 < all) u.ntok = min(u.ntok, max(p.units[i + 1].tok0 - u.tok0, 0));
+        int lo = INT32_MAX, hi = 0;
+        for (int t0 = 0; t0 < u.ntok; t0 += 32) {
+            const int2 r = range_of(u, t0 + lane);
+            lo = min(lo, r.x);
+            hi = max(hi, r.y);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        u.tiles = 0;
+        if (lo < hi) u.set_range(lo, hi);
+        if (lane == 0) {
+            p.units[i].ntok = u.ntok;
+            p.units[i].kt0 = u.kt0;
+            p.units[i].tiles = u.tiles;
+            p.units[i].edges = u.edges;
+        }
+    }
+    __syncthreads();
+    // gaps between a sequence's units
+    for (int64_t i = tid; i < all; i += kPlanThreads) {
+        const Unit u = p.units[i];
+        if (!u.tiles) continue;
+        int64_t b = i - 1;
+        while (b >= 0 && p.units[b].s == u.s && !p.units[b].tiles) --b;
+        if (b < 0 || p.units[b].s != u.s) continue;
+        if (max(u.first(), p.units[b].first()) > min(u.end(), p.units[b].end())) atomicOr(&p.seen[u.s].z, 1);
+    }
+    return all;
+}
+
 // Lists the units (one block): sequences' unit counts and their scan, then every
 // unit's key tiles and their scan.
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params p, int tpu) {
     __shared__ int64_t sh[32];
-    __shared__ int bad;
+    __shared__ int bad, torn;
     const AttendArgs &a = p.a;
     const int B = a.kv.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) bad = 0;
+    if (tid == 0) bad = torn = 0;
     pdl_wait();
     pdl_trigger();  // what came before is complete: the main kernel's set-up may overlap
     __syncthreads();
@@ -219,7 +321,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         const int64_t at = units + block_scan(n, &total, sh);
         if (s < B) {
             p.seq_off[s] = (int)(at < p.max_units ? at : p.max_units);
-            p.seen[s] = make_int2(INT32_MAX, 0);
+            p.seen[s] = make_int4(INT32_MAX, 0, 0, 0);
         }
         units += total;
     }
@@ -244,6 +346,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         u.ntok = min(tpu, c1 - u.tok0);
         u.kv = kv_len_of(a.kv, lo, c1 - c0);
         u.hi0 = u.kv - (c1 - u.tok0) + 1;
+        u.prefix = u.tok0 > c0;  // until the scan: a token of the sequence comes before
         if (u.kv >= 0 && !a.visible) {
             u.set_range(0, u.hi0 + u.ntok - 1);
             u.set_seen(0, u.kv);
@@ -252,11 +355,14 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
     }
     if (a.visible) {
         __syncthreads();
-        // a warp looks at its units' ranges, lane by token, kSame units at once
+        // A warp looks at its units' ranges, lane by token, kSame units at once.  Where every range
+        // overlaps or touches that of the token before it (one empty token between is enough
+        // not to know), what the sequence sees is one range without gaps.
         constexpr int kSame = 4;
         for (int64_t i0 = warp * kSame; i0 < units; i0 += kPlanThreads / 32 * kSame) {
             int first[kSame], end[kSame];
             Unit u[kSame];
+            bool gaps = false;
 #pragma unroll
             for (int k = 0; k < kSame; ++k) {
                 u[k] = p.units[min(i0 + k, units - 1)];
@@ -264,16 +370,21 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
                 end[k] = 0;
             }
             for (int t = lane; t < tpu; t += 32) {
-                int2 r[kSame];
+                int2 r[kSame], b[kSame];
 #pragma unroll
-                for (int k = 0; k < kSame; ++k)
-                    r[k] = u[k].kv >= 0 && t < u[k].ntok ? sees(a, u[k], t) : make_int2(INT32_MAX, 0);
+                for (int k = 0; k < kSame; ++k) {
+                    const bool some = u[k].kv >= 0 && t < u[k].ntok;
+                    r[k] = some ? sees(a, u[k], t) : make_int2(INT32_MAX, 0);
+                    b[k] = some && (t || u[k].prefix) ? sees(a, u[k], t - 1) : r[k];
+                }
 #pragma unroll
                 for (int k = 0; k < kSame; ++k) {
                     first[k] = min(first[k], r[k].x);
                     end[k] = max(end[k], r[k].y);
+                    gaps |= r[k].y > 0 && max(b[k].x, r[k].x) > min(b[k].y, r[k].y);
                 }
             }
+            if (gaps) torn = 1;
 #pragma unroll
             for (int k = 0; k < kSame; ++k) {
                 const int lo = __reduce_min_sync(0xffffffffu, first[k]), hi = __reduce_max_sync(0xffffffffu, end[k]);
@@ -284,6 +395,8 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
                 }
             }
         }
+        __syncthreads();
+        if (torn) units = split_units(p, units, tpu, sh);  // seldom, so it may take longer
     }
     __syncthreads();
     int64_t W = 0;
@@ -294,8 +407,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         if (i < units) {
             p.units[i].prefix = W + at;
             if (a.visible && p.units[i].tiles) {
-                const int2 r = __ldcg(p.seen + p.units[i].s);  // where the atomics left it
-                p.units[i].set_seen(r.x, r.y);
+                // Where the atomics left it.  In a sequence with gaps only what a unit's own rows
+                // see is known to be seen.
+                const int4 r = __ldcg(p.seen + p.units[i].s);
+                p.units[i].set_seen(r.z ? p.units[i].first() : r.x, r.z ? p.units[i].end() : r.y);
             }
         }
         W += total;
@@ -544,7 +659,8 @@ __device__ void role_q(const CUtensorMap *qm, const Params &p, Shared &sh, uint3
 // Zeros the rows of a value tile in shared memory outside [from, to): slots that no new
 // token sees (they may hold anything, and zero weights would multiply it).  Slots that
 // only this unit's rows do not see hold finite values, by the call's contract: clearing
-// those too cost 3-10 % on ragged prompts.
+// those too cost 3-10 % on ragged prompts, so it is done only where the sequence's ranges
+// leave gaps.
 template <int D>
 __device__ __forceinline__ void clear_unseen(uint32_t stage, int from, int to) {
     using C = Cfg<D>;
@@ -1297,8 +1413,9 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     char *ws = static_cast<char *>(a.workspace);
     p.plan = reinterpret_cast<Plan *>(ws);
     p.seq_off = reinterpret_cast<int32_t *>(ws + L.seq_off);
-    p.seen = reinterpret_cast<int2 *>(ws + L.seen);
+    p.seen = reinterpret_cast<int4 *>(ws + L.seen);
     p.units = reinterpret_cast<Unit *>(ws + L.units);
+    p.whole = reinterpret_cast<Unit *>(ws + L.whole);
     p.cuts = reinterpret_cast<Cut *>(ws + L.cuts);
     p.parts = reinterpret_cast<float *>(ws + L.parts);
     p.max_units = L.max_units;

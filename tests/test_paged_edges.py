@@ -73,3 +73,54 @@ def test_logits_of_thousands(d, dtype):
     m.lens = [(1, 700), (1, 1400)]
     out, lse = up.decode_attend(q[:2].contiguous(), m.cache)
     check_at(m, out, lse, oracle(m, q[:2], own[:2] * 0, m.kv_lens.long(), d ** -0.5))
+
+
+# ------------------------------------------------------------------ ranges with gaps
+
+def gapped(kind, n, kv, seed):
+    """First visible slot and end for n tokens: together they leave gaps."""
+    t = torch.arange(n)
+    if kind == "pair":        # neighbours see far-apart ranges
+        lo = torch.where(t % 2 == 0, 0, kv // 2)
+        hi = lo + 10
+    elif kind == "halves":    # a gap between the first tokens and the last ones, most of them in units of their own
+        lo = torch.where(t < n // 2, 3, 100)
+        hi = torch.where(t < n // 2, 13, 110)
+    elif kind == "islands":   # three islands across many key tiles, a token without a range between
+        lo = torch.tensor([17, kv // 3, kv - 90])[t // 5 % 3] + t % 4
+        hi = torch.where(t % 5 == 4, 0, lo + 40)
+    else:                     # short ranges anywhere
+        g = torch.Generator().manual_seed(seed)
+        lo = torch.randint(-20, kv, (n,), generator=g)
+        hi = lo + torch.randint(0, 30, (n,), generator=g)
+    return lo, hi
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["pair", "halves", "islands", "any"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("Hq,Hk,d,page", [(8, 2, 64, 16), (8, 2, 128, 64), (16, 2, 256, 48), (2, 2, 128, 256), (12, 4, 64, 384)])
+def test_gaps_between_ranges_may_hold_anything(Hq, Hk, d, page, bias, kind):
+    """Slots that no token sees hold NaN, pages of such slots are gone from the table."""
+    lens = [(40, 700), (1, 5), (300, 1500)]
+    m = Made(lens, Hk, d, page, "bf16", seed=23)
+    q = m.normal(m.T, Hq, d) * 2
+    lo, hi = (torch.cat(x).cuda() for x in zip(*(gapped(kind, n, kv, 3) for n, kv in lens)))
+    kw = {}
+    if bias:
+        kw = dict(slopes=torch.linspace(0.01, 0.001, Hq, device="cuda"),
+                  q_pos=torch.cat([m.tokens(s, m.pp)[kv - n:] for s, (n, kv) in enumerate(lens)]).contiguous())
+    want = oracle(m, q, lo, hi, d ** -0.5, **kw)
+    t0 = 0
+    for s, (n, kv) in enumerate(lens):
+        i = torch.arange(-(-kv // page) * page, device="cuda")
+        seen = ((i >= lo[t0:t0 + n, None]) & (i < hi[t0:t0 + n, None].clamp(max=kv))).any(0)
+        at, row = m.table[s].long()[i // page], i % page
+        m.kp[at[~seen], :, row[~seen]] = math.nan
+        m.vp[at[~seen], :, row[~seen]] = math.nan
+        m.table[s, :-(-kv // page)].masked_fill_(~seen.view(-1, page).any(1), -1)
+        t0 += n
+    vis = torch.stack([lo, hi], 1).to(torch.int32)
+    out, lse = up.attend_paged(q, m.cu, m.cache, visible=vis, **kw)
+    assert up.get_device_error() == 0
+    check_at(m, out, lse, want)
