@@ -968,7 +968,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                             up = max3(up, v[c][i], v[c][i + 1]);
                             dn = min3(dn, v[c][i], v[c][i + 1]);
                         }
-                        const float most = fmaxf(up, -dn) * fabsf(cap.in);
+                        const float most = fmaxf(up, -dn) * cap.reach;
                         if (__all_sync(0xffffffffu, most < 0.2f)) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) cap.small<4>(v[c][i], v[c][i + 1]);

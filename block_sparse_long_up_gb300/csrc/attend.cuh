@@ -47,14 +47,17 @@ __device__ __forceinline__ int share_of(const Shares &h, int64_t x) {
 // A capped logit, softcap * tanh(scale * x / softcap), in log2 units.  Where the
 // argument of tanh is small (most logits of most models) its Taylor series: 4 terms up
 // to 0.2 and 8 up to 0.5 leave less than 2^-23 of the result; elsewhere
-// (1 - t) / (1 + t) with t = e^(-2|y|), off by about 2^-23 of softcap.
+// (1 - t) / (1 + t) with t = e^(-2|y|), off by about 2^-23 of softcap.  The series' coefficients
+// hold powers of scale / softcap up to the 14th; where these pass fp32 (a softcap below about
+// 1/900 of the scale) the general form serves small arguments too.
 struct Cap {
     float in, out;   // scale / softcap, softcap * log2(e)
+    float reach;     // |in|, or infinite where there is no series: product * reach bounds its argument
     uint64_t c[8];   // the series in powers of x, for two logits at once
     __device__ __forceinline__ void set(float scale, float softcap) {
         constexpr float k[8] = {1.f, -1.f / 3.f, 2.f / 15.f, -17.f / 315.f, 62.f / 2835.f, -1382.f / 155925.f,
                                 21844.f / 6081075.f, -929569.f / 638512875.f};
-        in = scale / softcap;
+        in = fmaxf(fminf(scale / softcap, 3.0e38f), -3.0e38f);
         out = softcap * kLog2e;
         float f = scale * kLog2e;
 #pragma unroll
@@ -62,6 +65,9 @@ struct Cap {
             c[i] = sm100::pack2(k[i] * f, k[i] * f);
             f *= in * in;
         }
+        float last, same;
+        sm100::unpack2(c[7], last, same);
+        reach = fabsf(last) <= 3.0e38f ? fabsf(in) : INFINITY;
     }
     template <int kTerms>
     __device__ __forceinline__ void small(float &x, float &y) const {

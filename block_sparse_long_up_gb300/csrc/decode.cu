@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int i = 0; i < 2 * kR; ++i) most = fmaxf(most, fabsf(x[n][i]));
-                    const bool small = __all_sync(0xffffffffu, most * fabsf(cap.in) < 0.5f);
+                    const bool small = __all_sync(0xffffffffu, most * cap.reach < 0.5f);
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll

@@ -124,3 +124,25 @@ def test_gaps_between_ranges_may_hold_anything(Hq, Hk, d, page, bias, kind):
     out, lse = up.attend_paged(q, m.cu, m.cache, visible=vis, **kw)
     assert up.get_device_error() == 0
     check_at(m, out, lse, want)
+
+
+# ------------------------------------------------------------------ tight caps
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softcap", [1e-6, 1e-4, 1e-3, 1.0, 1e30])
+@pytest.mark.parametrize("scale", [0.088, 1.0, -0.088, 1e5])
+@pytest.mark.parametrize("d", [64, 256])
+def test_caps_far_below_the_scale(d, scale, softcap):
+    """Queries of zero, queries whose logits are a part of the cap, and ordinary ones."""
+    lens = [(130, 400), (3, 900)]
+    m = Made(lens, 2, d, 64, "bf16", seed=24)
+    size = torch.tensor([0.0, 0.3 * min(softcap, 1.0) / abs(scale) * d ** -0.5, min(1.0, 10 / abs(scale))], device="cuda")
+    q = (m.normal(m.T, 8, d).float() * size[torch.arange(m.T, device="cuda") // 40 % 3, None, None]).to(m.dt)
+    own = torch.cat([torch.arange(kv - n, kv) for n, kv in lens]).cuda()
+    out, lse = up.attend_paged(q, m.cu, m.cache, scale=scale, softcap=softcap)
+    check_at(m, out, lse, oracle(m, q, own * 0, own + 1, scale, softcap=softcap), content=800.0)
+    m.lens = [(1, 400), (1, 900)]
+    for t in (0, 45, 90):
+        x = q[t:t + 2].contiguous()
+        out, lse = up.decode_attend(x, m.cache, scale=scale, softcap=softcap)
+        check_at(m, out, lse, oracle(m, x, own[:2] * 0, m.kv_lens.long(), scale, softcap=softcap), content=800.0)
