@@ -212,6 +212,11 @@ def _plain_logits(scale, softcap):
 
 
 def _logits(cache, T, Hq, scale, softcap, slopes, q_pos):
+    # plain numbers: a tensor would be remembered by its identity, with its first value
+    if type(scale) is not float:
+        scale = ctypes.c_float(scale).value
+    if type(softcap) is not float:
+        softcap = ctypes.c_float(softcap).value
     if slopes is None:
         return _plain_logits(scale, softcap)
     _need(slopes, "slopes", torch.float32, cache.device, (Hq,))

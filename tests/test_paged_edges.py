@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import block_sparse_long_up_gb300 as up
+from block_sparse_long_up_gb300 import paged
 from test_paged import Made, oracle
 
 
@@ -146,3 +147,16 @@ def test_caps_far_below_the_scale(d, scale, softcap):
         x = q[t:t + 2].contiguous()
         out, lse = up.decode_attend(x, m.cache, scale=scale, softcap=softcap)
         check_at(m, out, lse, oracle(m, x, own[:2] * 0, m.kv_lens.long(), scale, softcap=softcap), content=800.0)
+
+
+def test_a_scale_is_read_at_every_call():
+    """A 0-dim tensor may be the scale or the cap, and may change between calls."""
+    for k in range(2):
+        x = torch.tensor([0.5, 30.0])
+        given = [x[0], x[1]]
+        for a, b in ((0.5, 30.0), (0.25, 20.0)):
+            x[0], x[1] = a, b
+            lg = paged._logits(None, 1, 1, *given, None, None)._obj
+            assert (lg.scale, lg.softcap) == (a, b)
+    with pytest.raises(TypeError):
+        paged._logits(None, 1, 1, "0.5", 0.0, None, None)
