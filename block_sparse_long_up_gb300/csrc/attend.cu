@@ -31,9 +31,8 @@
 //   warps 4-11  two softmax warpgroups, one per tile (at head_dim 256 one per 64 keys of
 //               the only tile).  Thread = row.  It holds the row's logits in registers,
 //               writes the weights over them in TMEM, and rescales its output row
-//               there only when the maximum has grown by more than 2^8 (weights then
-//               stay below 2^8, far inside both types and fp32), which after the first
-//               tiles is rare.
+//               there only when the maximum has grown by more than 2^8 (see kSlack), which
+//               after the first tiles is rare.
 #include "attend.cuh"
 #include "tma_host.cuh"
 
@@ -47,7 +46,6 @@ constexpr int kRows = 128;        // rows of a tile, keys of a step
 constexpr int kMinTiles = 4;      // shares are not cut finer than this: more parts cost
                                   // more to join than a step (128 tokens over 4K: 29.8,
                                   // 23.6, 22.4 and 26.5 us with 1, 2, 4 and 8)
-constexpr float kSlack = 8.f;     // log2: how far the maximum may grow before a rescale
 constexpr int kPanel = 128 * 128; // 128 rows x 64 elements
 // Tiles' worth of time that a unit costs beside its tiles: without it a share of short
 // units takes far longer than one of long ones (three ragged sequences, 16/2 heads of
@@ -1036,10 +1034,10 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                 mt = fmaxf(x[tid], x[128 + tid]);
                 if (!meet()) return;  // read before the place is written again
             }
-            const bool grew = mt > m + kSlack;
+            const bool grew = mt > m + (kSlack + kLift<kFp16>);
             if (__any_sync(0xffffffffu, grew)) {
-                const float f = grew ? exp2f(m - mt) : 1.f;
-                if (grew) m = mt;
+                const float f = grew ? exp2f(m - (mt - kLift<kFp16>)) : 1.f;
+                if (grew) m = mt - kLift<kFp16>;
                 l *= f;
                 if (t > 0) {
                     const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t - 1, et, used)]), use.par(t - 1, used),

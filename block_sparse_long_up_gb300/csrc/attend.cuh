@@ -83,6 +83,16 @@ struct Cap {
     }
 };
 
+// The running reference of a row's weights: a maximum less kLift, replaced when the maximum has grown by
+// more than kSlack (both log2), so that outputs are seldom rescaled.  Weights stay
+// below 2^(kSlack + kLift).  Fp16 ends at 2^16 and loses bits below 2^-14: lifted by 2^7,
+// weights keep them down to 2^-21 of the maximum's and lose 2^-32 of it at most below
+// (unlifted, a first token that draws all the weight left 2^-24 of itself as the smallest
+// weight of the others, which the sum counted in full).
+constexpr float kSlack = 8.f;
+template <bool kFp16>
+constexpr float kLift = kFp16 ? 7.f : 0.f;
+
 template <bool kFp16>
 __device__ __forceinline__ void store_row4(void *out, int64_t at, float4 v) {
     uint2 w;

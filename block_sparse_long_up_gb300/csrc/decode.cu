@@ -37,7 +37,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 16;               // slots of a warp's step
 constexpr int kTile = kGroup * kWarps;   // slots of a block's step
 constexpr int kMaxPerSm = 3;
-constexpr float kSlack = 8.f;            // log2: how far the maximum may grow before a rescale
 constexpr int kMinTiles = 2;             // shares are not cut finer than this
 
 template <int D>
@@ -351,11 +350,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
                 float mx = fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                // the reference follows the maximum only when that has grown by more than 2^8
-                // (weights then stay below 2^8), so the outputs are seldom rescaled
-                const bool grew = mx > m[r] + kSlack;
-                c[r] = grew ? exp2f(m[r] - mx) : 1.f;
-                m[r] = grew ? mx : m[r];
+                const bool grew = mx > m[r] + (kSlack + kLift<kFp16>);
+                c[r] = grew ? exp2f(m[r] - (mx - kLift<kFp16>)) : 1.f;
+                m[r] = grew ? mx - kLift<kFp16> : m[r];
                 ref[r] = m[r] == -INFINITY ? 0.f : m[r];
                 moved |= grew;
             }

@@ -160,3 +160,28 @@ def test_a_scale_is_read_at_every_call():
             assert (lg.scale, lg.softcap) == (a, b)
     with pytest.raises(TypeError):
         paged._logits(None, 1, 1, "0.5", 0.0, None, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", [64, 512, 2000])
+@pytest.mark.parametrize("below", [12.0, 14.5, 17.0])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_light_weights_of_fp16_count(d, below, kv):
+    """One key carries nearly all the weight and its value is zero, so the output is the others',
+    each with a weight of e^-12 to e^-17.  A weight keeps a half step of fp16 down to 2^-21 of
+    the reference; below, 2^-32 of it each."""
+    m = Made([(3, kv)], 2, d, 64, "fp16", seed=22)
+    i = torch.arange(kv, device="cuda")
+    at, row = m.table[0].long()[i // 64], i % 64
+    m.kp[at, :, row] = 0
+    m.kp[at[0], :, 0] = below * d ** -0.5
+    m.vp[at, :, row] = (1024 * (m.vp[at, :, row].float().abs().clamp(max=1) + 0.5)).to(m.dt)
+    m.vp[at[0], :, 0] = 0
+    q = torch.ones(3, 8, d, dtype=m.dt, device="cuda")
+    own = torch.arange(kv - 3, kv, device="cuda")
+    out, lse = up.attend_paged(q, m.cu, m.cache)
+    floor = kv * 2.0 ** -32 * 1536
+    check_at(m, out, lse, oracle(m, q, own * 0, own + 1, d ** -0.5), floor=floor)
+    m.lens = [(1, kv)]
+    out, lse = up.decode_attend(q[:1].contiguous(), m.cache)
+    check_at(m, out, lse, oracle(m, q[:1], own[:1] * 0, m.kv_lens.long(), d ** -0.5), floor=floor)
