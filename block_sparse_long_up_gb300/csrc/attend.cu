@@ -958,6 +958,18 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             for (int c = 0; c < kCh; ++c) tmem_wait_ld_dep(v[c]);
             if constexpr (kMore) {
                 if (a.softcap > 0.f) {
+                    // Only logits that count choose the form, so that the others' cannot change
+                    // a bit: unseen ones are zeros for it, and rows nobody reads have no say.
+                    if (!__all_sync(0xffffffffu, vis.x <= k0 && vis.y >= k0 + kRows)) {
+#pragma unroll
+                        for (int c = 0; c < kCh; ++c) {
+                            const int from = max(vis.x, k0) - k0 - 32 * (ch0 + c);
+                            const int to = min(vis.y, k0 + kRows) - k0 - 32 * (ch0 + c);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < from || i >= to) v[c][i] = 0.f;
+                        }
+                    }
 #pragma unroll
                     for (int c = 0; c < kCh; ++c) {
                         float up = fmaxf(v[c][0], v[c][1]), dn = fminf(v[c][0], v[c][1]);
@@ -966,7 +978,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                             up = max3(up, v[c][i], v[c][i + 1]);
                             dn = min3(dn, v[c][i], v[c][i + 1]);
                         }
-                        const float most = fmaxf(up, -dn) * cap.reach;
+                        const float most = valid ? fmaxf(up, -dn) * cap.reach : 0.f;
                         if (__all_sync(0xffffffffu, most < 0.2f)) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) cap.small<4>(v[c][i], v[c][i + 1]);

@@ -185,3 +185,59 @@ def test_light_weights_of_fp16_count(d, below, kv):
     m.lens = [(1, kv)]
     out, lse = up.decode_attend(q[:1].contiguous(), m.cache)
     check_at(m, out, lse, oracle(m, q[:1], own[:1] * 0, m.kv_lens.long(), d ** -0.5), floor=floor)
+
+
+# ------------------------------------------------------------------ what must not reach a result
+
+CAP = dict(softcap=30.0)
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk,d", [(12, 4, 64), (14, 2, 128), (5, 1, 256)])
+def test_rows_without_a_token_change_no_bit(Hq, Hk, d):
+    """Where the group does not divide 128 a tile ends in rows that hold whatever was there before."""
+    m = Made([(100, 600)], Hk, d, 64, "bf16", seed=25)
+    q = m.normal(m.T, Hq, d) * 0.5
+    before = m.normal(256, 8 * Hk, d)
+    cu = torch.tensor([0, 256], dtype=torch.int32, device="cuda")
+    results = []
+    for size in (0.0, 60.0, 0.0, 60.0):
+        up.attend_paged((before * size), cu, m.cache, visible=torch.tensor([[0, 600]] * 256, dtype=torch.int32, device="cuda"), **CAP)
+        results.append(up.attend_paged(q, m.cu, m.cache, **CAP))
+    assert all(same(results[0], r) for r in results[1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk,d", [(8, 2, 64), (32, 8, 128), (16, 2, 256)])
+def test_other_sequences_change_no_bit(Hq, Hk, d):
+    """A sequence's results do not depend on the queries of the one behind it."""
+    m = Made([(37, 300), (50, 400)], Hk, d, 64, "bf16", seed=26)
+    q = m.normal(m.T, Hq, d) * 0.5
+    loud = q.clone()
+    loud[37:] *= 60
+    a, b = (up.attend_paged(x, m.cu, m.cache, **CAP) for x in (q, loud))
+    assert same([x[:37] for x in a], [x[:37] for x in b])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk,d", [(8, 2, 64), (32, 8, 128), (16, 2, 256)])
+def test_unseen_slots_change_no_bit(Hq, Hk, d):
+    """What is stored in a slot that no query sees, whatever its logit would be."""
+    m = Made([(60, 700)], Hk, d, 64, "bf16", seed=27, poison=False)
+    q = m.normal(m.T, Hq, d) * 0.5
+    vis = torch.tensor([[150, 670]] * 60, dtype=torch.int32, device="cuda")
+    start = torch.tensor([150], dtype=torch.int32, device="cuda")
+    results = []
+    for size in (0.0, 60.0, math.inf):
+        for s in list(range(150)) + list(range(670, 704)):
+            pg = int(m.table[0, s // 64])
+            m.kp[pg, :, s % 64], m.vp[pg, :, s % 64] = size, size
+        m.kv_lens[0] = 700
+        a = up.attend_paged(q, m.cu, m.cache, visible=vis, **CAP)
+        m.kv_lens[0] = 670
+        results.append(a + up.decode_attend(q[:1].contiguous(), m.cache, kv_start=start, **CAP))
+    assert same(results[0], results[1]) and same(results[0], results[2])
