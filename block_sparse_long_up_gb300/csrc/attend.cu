@@ -105,7 +105,7 @@ struct Unit {
 struct Plan {
     int64_t W;  // width of one KV head's units
     int units;
-    int pad;
+    int bad;    // cu_seqlens is malformed: no unit, every row is that of an empty mask
 };
 
 // What a block's share leaves unfinished at its end: a unit that begins in it.
@@ -324,10 +324,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         units += total;
     }
     __syncthreads();
-    if (bad || units > p.max_units) {  // a malformed cu_seqlens: nothing is computed
+    if (bad || units > p.max_units) {
         if (tid == 0) {
             atomicOr(a.kv.err, kErrCuSeqlens);
-            *p.plan = Plan{0, 0, 0};
+            *p.plan = Plan{0, 0, 1};
         }
         return;
     }
@@ -1302,7 +1302,8 @@ constexpr int kJoinThreads = 256, kJoinRows = 32;
 // Block (c, y): the unit that the end of share c cuts, if c is the first to cut it,
 // rows [32y, 32y + 32): a lane takes a row, a warp every eighth four of its columns, the
 // parts in the order of their slots.  All
-// blocks together also write the rows of the units without a visible slot.
+// blocks together also write the rows of the units without a visible slot, or of all tokens
+// when the batch is malformed.
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params p) {
     using C = Cfg<D>;
@@ -1311,10 +1312,13 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params 
     pdl_wait();
     const Plan pl = *p.plan;
     const int nb = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
-    for (int i = me; i < pl.units; i += nb) {
-        const Unit u = p.units[i];
-        if (u.tiles) continue;
-        const int64_t r0 = (int64_t)u.tok0 * a.Hq, nr = (int64_t)u.ntok * a.Hq;
+    for (int i = me; i < (pl.bad ? a.T : pl.units); i += nb) {
+        int64_t r0 = (int64_t)i * a.Hq, nr = a.Hq;
+        if (!pl.bad) {
+            const Unit u = p.units[i];
+            if (u.tiles) continue;
+            r0 = (int64_t)u.tok0 * a.Hq, nr = (int64_t)u.ntok * a.Hq;
+        }
         for (int64_t k = tid; k < nr * D / 8; k += kJoinThreads)
             reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + r0 * D)[k] = make_uint4(0, 0, 0, 0);
         if (a.lse)

@@ -385,7 +385,9 @@ typedef struct {
  *   rot_dim    0, or a multiple of 16 up to d.
  *   q_out      dtype [total_tokens, Hq, d] contiguous; may be q itself when
  *              q_stride = Hq * d.
- * The tokens' pages must not be shared between sequences.  Errors:
+ * The tokens' pages must not be shared between sequences.  Where cu_seqlens is
+ * malformed (UP_DEVERR_BAD_CU_SEQLENS), a token that lies in no range of it, or in one that
+ * ends past total_tokens, is rotated but not appended.  Errors:
  * UP_ERR_INVALID_ARG for null pointers, sizes, strides or alignments outside the
  * above; UP_ERR_UNSUPPORTED for a d or dtype outside the cache's list.
  */
@@ -432,6 +434,8 @@ typedef struct {
  *   lse      fp32 [total_tokens, Hq] or NULL: natural log of the softmax's sum.
  *   workspace  up_attend_paged_workspace(...) bytes, 256-byte aligned; its contents
  *            on entry do not matter.
+ * A malformed cu_seqlens (UP_DEVERR_BAD_CU_SEQLENS) gives every token the output of an
+ * empty mask.
  * A cached value that some query of the call may not see but another one may
  * has to be finite (its zero weight multiplies it).  Results are deterministic on
  * a given GPU model (the parts' boundaries depend on its number of SMs).

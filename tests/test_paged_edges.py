@@ -241,3 +241,31 @@ def test_unseen_slots_change_no_bit(Hq, Hk, d):
         m.kv_lens[0] = 670
         results.append(a + up.decode_attend(q[:1].contiguous(), m.cache, kv_start=start, **CAP))
     assert same(results[0], results[1]) and same(results[0], results[2])
+
+
+# ------------------------------------------------------------------ malformed batches
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu,covered", [([0, 4, 6], range(6)), ([3, 5, 8], range(3, 8)), ([0, 9, 8], ()),
+                                        ([-4, 4, 8], range(4, 8)), ([0, 0, 0], ()), ([0, 4, 1 << 30], range(4))])
+@pytest.mark.parametrize("d", [64, 256])
+def test_malformed_cu_seqlens(d, cu, covered):
+    """Attention gives the rows of an empty mask; the append writes the tokens that lie in a
+    range of the batch and nothing else.  Both report it."""
+    m = Made([(4, 200), (4, 100)], 2, d, 32, "bf16", seed=29, poison=False)
+    q, k, v = m.normal(8, 8, d), m.normal(8, 2, d), m.normal(8, 2, d)
+    bad = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, math.nan), torch.full((8, 8), math.nan, device="cuda")
+    up.attend_paged(q, bad, m.cache, out=out, lse=lse)
+    assert up.get_device_error() == 0x1
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    want = [x.clone() for x in (m.kp, m.vp, m.pp)]
+    pos = torch.arange(100, 108, dtype=torch.int32, device="cuda")
+    for t in covered:
+        s = 0 if cu[0] <= t < cu[1] else 1
+        slot = m.lens[s][1] - (cu[s + 1] - t)
+        pg = int(m.table[s, slot // 32])
+        want[0][pg, :, slot % 32], want[1][pg, :, slot % 32], want[2][pg, slot % 32] = k[t], v[t], pos[t]
+    up.append_kv(None, k, v, pos, bad, m.cache, None)
+    assert up.get_device_error() == 0x1
+    assert all(torch.equal(x, y) for x, y in zip(want, (m.kp, m.vp, m.pp)))
