@@ -213,9 +213,8 @@ __device__ __forceinline__ bool apart(int2 a, int2 b) {
 }
 
 // Splits the units where a token's range lies apart from the one before it and finds the
-// sequences with gaps; returns the units' number (T at most: a unit has a token).  Out of line,
-// so that the plans that do not need it stay short (128 tokens over 4K: 24 us inline, 23).
-__device__ __noinline__ int64_t split_units(const Params &p, int64_t units, int tpu, int64_t *sh) {
+// sequences with gaps; returns the units' number (T at most: a unit has a token).
+__device__ __forceinline__ int64_t split_units(const Params &p, int64_t units, int tpu, int64_t *sh) {
     const AttendArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto range_of = [&](const Unit &u, int tl) {
@@ -296,7 +295,9 @@ __device__ __noinline__ int64_t split_units(const Params &p, int64_t units, int 
 }
 
 // Lists the units (one block): sequences' unit counts and their scan, then every
-// unit's key tiles and their scan.
+// unit's key tiles and their scan.  Calls without `visible` have a shorter kernel of their own
+// (128 tokens over 4K: 23 us instead of 24).
+template <bool kVisible>
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params p, int tpu) {
     __shared__ int64_t sh[32];
     __shared__ int bad, torn;
@@ -345,13 +346,13 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         u.kv = kv_len_of(a.kv, lo, c1 - c0);
         u.hi0 = u.kv - (c1 - u.tok0) + 1;
         u.prefix = u.tok0 > c0;  // until the scan: a token of the sequence comes before
-        if (u.kv >= 0 && !a.visible) {
+        if (u.kv >= 0 && !kVisible) {
             u.set_range(0, u.hi0 + u.ntok - 1);
             u.set_seen(0, u.kv);
         }
         p.units[i] = u;
     }
-    if (a.visible) {
+    if constexpr (kVisible) {
         __syncthreads();
         // A warp looks at its units' ranges, lane by token, kSame units at once.  Where every range
         // overlaps or touches that of the token before it (one empty token between is enough
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
         const int64_t at = block_scan(i < units ? width_of(p.units[i]) : 0, &total, sh);
         if (i < units) {
             p.units[i].prefix = W + at;
-            if (a.visible && p.units[i].tiles) {
+            if (kVisible && p.units[i].tiles) {
                 // Where the atomics left it.  In a sequence with gaps only what a unit's own rows
                 // see is known to be seen.
                 const int4 r = __ldcg(p.seen + p.units[i].s);
@@ -870,8 +871,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
     // the two threads of a row meet (the pair of warps does): false after an abort
     auto meet = [&]() {
         const uint32_t bar = smem_u32(&sh.xch[quarter]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
+        mbar_arrive(bar);
         const bool ok = mbar_wait(bar, swaps & 1, &sh.abort, a.wait_limit);
         __syncwarp();
         ++swaps;
@@ -1242,7 +1242,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         mbar_init(smem_u32(&sh.qfull), 1);
         mbar_init(smem_u32(&sh.qempty), 2);
         mbar_init(smem_u32(&sh.pieces), 2);
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.xch[i]), 2);
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.xch[i]), 64);
         for (int i = 0; i < 2; ++i) {
             for (int b = 0; b < 2; ++b) {
                 mbar_init(smem_u32(&sh.sfull[i][b]), 1);
@@ -1442,7 +1442,7 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     cudaError_t e = more ? allow_smem<attend_kernel<kFp16, D, true>>(C::kSmem)
                          : allow_smem<attend_kernel<kFp16, D, false>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attend_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, C::kTiles * p.tpt);
+    e = launch_pdl(a.visible ? attend_plan_kernel<true> : attend_plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, st, p, C::kTiles * p.tpt);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmem, st, qm, km, vm, p);
     if (e != cudaSuccess) return e;
