@@ -8,7 +8,6 @@ decode attention over it (the paged-cache section of include/up.h).
 """
 from __future__ import annotations
 
-import collections
 import contextlib
 import ctypes
 import functools
@@ -73,22 +72,19 @@ def _need(t, name, dtype, device, shape=None):
         _refuse(t, name, dtype, device, shape)
 
 
-_Fields = collections.namedtuple("_Fields", "k_pages v_pages block_table kv_lens pos_pages num_seqs "
-                                 "Hk d page_size dtype device struct ref")
-
-
-class PagedKV(_Fields):
+class PagedKV:
     """A paged KV-head-major cache: k_pages and v_pages [num_pages, Hk, page_size, d]
     (bf16 or fp16), block_table int32 [num_seqs, max_pages], kv_lens int32
     [num_seqs] (cached tokens, those of the current call included) and, where
     positions matter, pos_pages int32 [num_pages, page_size].  Holds the tensors;
     their contents may change between calls (an engine adds to kv_lens and to
-    block_table in place), the attributes may not: other tensors are another
-    PagedKV."""
+    block_table in place), the attributes and the tensors' storage may not: other
+    tensors are another PagedKV."""
 
-    __slots__ = ()
+    __slots__ = ("k_pages", "v_pages", "block_table", "kv_lens", "pos_pages", "num_seqs", "Hk", "d",
+                 "page_size", "dtype", "device", "struct", "ref")
 
-    def __new__(cls, k_pages, v_pages, block_table, kv_lens, pos_pages=None):
+    def __init__(self, k_pages, v_pages, block_table, kv_lens, pos_pages=None):
         if not isinstance(k_pages, torch.Tensor):
             raise TypeError("k_pages must be a torch.Tensor")
         dt, dev = k_pages.dtype, k_pages.device
@@ -109,12 +105,24 @@ class PagedKV(_Fields):
         c = _CKv(k_pages.data_ptr(), v_pages.data_ptr(),
                  None if pos_pages is None else pos_pages.data_ptr(), block_table.data_ptr(),
                  kv_lens.data_ptr(), n, b, mp, ps, hk, d, DTYPES[dt])
-        return tuple.__new__(cls, (k_pages, v_pages, block_table, kv_lens, pos_pages, b, hk, d, ps, dt,
-                                   dev, c, ctypes.byref(c)))
+        for put, x in zip(_PUT, (k_pages, v_pages, block_table, kv_lens, pos_pages, b, hk, d, ps, dt,
+                                 dev, c, ctypes.byref(c))):
+            put(self, x)
+
+    def _fixed(self, name, value=None):
+        raise AttributeError(f"{name}: a PagedKV's attributes are fixed")
+
+    __setattr__ = __delattr__ = _fixed
+
+    def __reduce__(self):  # copies go through the checks and get a struct of their own
+        return type(self), (self.k_pages, self.v_pages, self.block_table, self.kv_lens, self.pos_pages)
 
     def __repr__(self):
         return (f"PagedKV({self.k_pages.shape[0]} pages of {self.page_size} slots, {self.Hk} heads of "
                 f"{self.d}, {self.dtype}, {self.num_seqs} sequences)")
+
+
+_PUT = tuple(PagedKV.__dict__[name].__set__ for name in PagedKV.__slots__)
 
 
 def _on(stream):

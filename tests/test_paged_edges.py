@@ -1,5 +1,6 @@
 """The paged-cache operators at the edges of their ranges: logits of thousands, light weights,
 ranges with gaps, tight caps, what must not reach a result, and a cache's identity."""
+import copy
 import math
 
 import pytest
@@ -269,3 +270,31 @@ def test_malformed_cu_seqlens(d, cu, covered):
     up.append_kv(None, k, v, pos, bad, m.cache, None)
     assert up.get_device_error() == 0x1
     assert all(torch.equal(x, y) for x, y in zip(want, (m.kp, m.vp, m.pp)))
+
+
+# ------------------------------------------------------------------ a cache's identity
+
+def test_a_cache_is_no_tuple():
+    """No way around the constructor's checks (a replaced field would leave the addresses behind)."""
+    assert not issubclass(up.PagedKV, tuple)
+    for name in ("_replace", "_make"):
+        assert not hasattr(up.PagedKV, name)
+
+
+@pytest.mark.gpu
+def test_copies_of_a_cache_hold_their_own_tensors():
+    m = Made([(1, 20), (1, 70)], 2, 64, 16, "bf16", seed=28)
+    q = m.normal(2, 8, 64)
+    want = up.decode_attend(q, m.cache)
+    shallow, deep = copy.copy(m.cache), copy.deepcopy(m.cache)
+    assert shallow.k_pages is m.kp and deep.k_pages is not m.kp
+    assert torch.equal(deep.kv_lens, m.kv_lens) and torch.equal(deep.pos_pages, m.pp)
+    m.kp.zero_(), m.vp.zero_(), m.kv_lens.zero_()
+    for x, y in zip(want, up.decode_attend(q, deep)):
+        assert torch.equal(x, y)
+    assert bool((up.decode_attend(q, shallow)[0] == 0).all())
+    for name in ("k_pages", "kv_lens", "ref", "anything"):
+        with pytest.raises(AttributeError):
+            setattr(m.cache, name, None)
+        with pytest.raises(AttributeError):
+            delattr(m.cache, name)
