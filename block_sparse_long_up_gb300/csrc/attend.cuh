@@ -9,19 +9,6 @@
 
 namespace up {
 
-namespace sm100 {
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float min3(float a, float b, float c) {
-    float d;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-}  // namespace sm100
-
 constexpr int kMaxSms = 160;  // workspaces are sized for this many
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 

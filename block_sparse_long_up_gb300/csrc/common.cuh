@@ -14,13 +14,15 @@ namespace up {
 // of the stream wrote: that waits until that kernel has finished and its
 // writes are visible (read-after-write and write-after-read alike).  A kernel
 // that calls pdl_trigger() lets the next kernel's CTAs be scheduled while it
-// still runs; one that does not releases them as its CTAs exit.  Only the
-// one-warp plan kernel triggers early, right after its own pdl_wait(): every
+// still runs; one that does not releases them as its CTAs exit.  The scoring
+// call's one-warp plan kernel triggers early, right after its own pdl_wait(): every
 // kernel before it is then complete, so the scoring kernel may read the call's
 // inputs (q_last, k, cu_seqlens) and write its own workspace regions before it
-// waits for the plan itself.  Everywhere else early-scheduled CTAs that only
-// wait measured slower than a release at exit.  Both calls are no-ops for a
-// kernel launched without the attribute.
+// waits for the plan itself.  So do the attention call's plan kernel (the main
+// kernel sets up its barriers and tensor memory meanwhile) and the decode kernel (its
+// join finds its rows' parts from the lengths).  Everywhere else early-scheduled
+// CTAs that only wait measured slower than a release at exit.  Both calls are
+// no-ops for a kernel launched without the attribute.
 __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -41,11 +41,10 @@
 // anyway is queued for an exact CUDA-core fallback in the epilogue.  After its
 // last unit every CTA runs the epilogue: grid barriers, then each row's
 // normaliser and chunk weights, then the block scores (see score_epilogue).
-#include <cudaTypedefs.h>
-
 #include "../../include/up.h"
 #include "common.cuh"
 #include "sm100.cuh"
+#include "tma_host.cuh"
 
 namespace up {
 
@@ -1110,19 +1109,6 @@ score_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant_
     }
     if (threadIdx.x == 0 && sh.abort) atomicOr(p.err, UP_DEVERR_TIMEOUT);
     pdl_wait();  // this grid completes after the plan: later kernels read its table
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
 }
 
 // K viewed as a 2-D row-major matrix [total_tokens, Hk*d] (paged keys:

@@ -1,5 +1,5 @@
 // sm100.cuh -- thin inline-PTX wrappers for the Blackwell (sm_100 family,
-// here sm_103a) features the scoring kernel uses: mbarriers, TMA tile loads,
+// here sm_103a) features the scoring and attention kernels use: mbarriers, TMA tile loads,
 // tensor memory (TMEM) allocation/loads and tcgen05 MMAs.
 #pragma once
 
@@ -265,6 +265,18 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
