@@ -3,7 +3,8 @@
 // Every new token's query, key and value rows are read once and written once:
 // 2 * (Hq + 2*Hk) * d * 2 bytes a token, which is all there is to do beside
 // rot/2 sines and cosines a token; so memory bounds a prompt and latency a step (32768
-// tokens of 32 + 16 rows of 128: 129 us at 6.2 TB/s; one token: 3.7 us).
+// tokens of 32 + 16 rows of 128: 129 us at 6.2 TB/s; one token: 3.9 us in a graph, 20 us
+// a call, the host's).
 //
 // A block takes a tile of consecutive tokens.  Their angles come first, one
 // thread per (token, frequency), into shared memory: computed once per token and
@@ -25,9 +26,10 @@ constexpr int kAngles = 2048;    // angles of a tile
 constexpr int kUnits = 12 * kThreads;  // units of a tile
 constexpr int kInFlight = 4;     // units a thread loads before it stores any
 
-// inv_freq in turns a position, as a multiple of 2^-64 turns; its product with a
-// position wraps at whole turns by itself, so the angle is reduced exactly for every
-// 32-bit position.  (Once a frequency and block: 64-bit floats are slow here.)
+// inv_freq in turns a position, as a multiple of 2^-64 turns (rounded once, to 2^-56 of a
+// turn for up to 1 radian); its product with a position wraps at whole turns by itself, so
+// nothing is lost beside that rounding for every 32-bit position.  (Once a frequency and
+// block: 64-bit floats are slow here.)
 __device__ __forceinline__ unsigned long long turn_step(float inv_freq) {
     double t = (double)inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
     t -= rint(t);

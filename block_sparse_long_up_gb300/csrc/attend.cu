@@ -14,10 +14,17 @@
 // KV heads are laid end to end and block c of the grid (one per SM) takes the c-th
 // equal share, so causal, windowed, ragged and few-row batches load every SM alike
 // without the host knowing a length.  2048 tokens over 65536 of 32/8 heads of 128 take
-// 1.44-1.54 ms = 1.4-1.5 PFLOP/s, 0.73-0.77 of the measured burst rate: a chain of
-// products into one accumulator issues one every ~92 cycles instead of 64.  A unit cut by a share's end leaves its
-// running maximum, sum and unnormalised output in the workspace for the join kernel
-// (fixed order: results are reproducible); a whole unit is written by its block.
+// 1.68-1.71 ms a call among others (1.28 PFLOP/s, 0.66 of the measured burst rate; the
+// power limit holds then) and 1.44-1.54 ms in a graph of ten: products are
+// issued one every ~92 cycles instead of 64 (one chain into each accumulator; whether
+// shared memory's rate has a part in it was not separated).  A unit cut by a share's end
+// leaves its running maximum, sum and unnormalised output in the workspace for the join
+// kernel (fixed order: results are reproducible); a whole unit is written by its block.
+//
+// The weights are rounded once to the cache's type before their product with the
+// values: the tensor cores take no wider operand, and a low part beside them would double that
+// product.  Against 64 bits outputs are off by 2.1-2.3e-3 in the 2-norm in bf16, where one
+// rounding of the result leaves 1.6-1.7e-3; the sum counts the weights unrounded.
 //
 // Roles of a block:
 //   warp 0      keys and values, TMA into a ring (boxes of the largest power of two
@@ -49,7 +56,8 @@ constexpr int kMinTiles = 4;      // shares are not cut finer than this: more pa
 constexpr int kPanel = 128 * 128; // 128 rows x 64 elements
 // Tiles' worth of time that a unit costs beside its tiles: without it a share of short
 // units takes far longer than one of long ones (three ragged sequences, 16/2 heads of
-// 256: 380 us with 0, 305 with 2, 287 with 3, 292 with 5)
+// 256, capped and biased: 380 us with 0, 305 with 2, 287 with 3, 292 with 5; since rows'
+// references are exact and only logits that count choose the cap's form 323 with 3)
 constexpr int kUnitCost = 3;
 
 template <int D>
@@ -1039,7 +1047,9 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             if constexpr (kSplit) {
                 // Both threads of the row need one reference: the larger of their maxima, in all its
                 // bits (a maximum rounded to 16 bits is off by a part of itself, and weights
-                // by 2^that: beyond both types for the far keys of a distance bias).
+                // by 2^that: beyond both types for the far keys of a distance bias).  One
+                // buffer of 32 bits is what shared memory leaves, hence two meetings: 13 us of
+                // the capped case's 311, 1 of 344 for 2048 plain tokens over 16K.
                 float *x = reinterpret_cast<float *>(s_xch);
                 x[e * 128 + tid] = mt;
                 if (!meet()) return;

@@ -3,8 +3,9 @@
 // Every cached key and value is read once, 4*d bytes a slot and KV head, and
 // serves the g query heads of its group: 4*g*d flops for 4*d bytes, so the cache's
 // bandwidth bounds the call (a step of short caches is bounded by latency): 24 sequences
-// of up to 128K, 32/8 heads of 128, take 637 us at 6.9 TB/s, one of 128K 88 us at
-// 6.1 TB/s, one of 4096 with 8/2 heads of 64 8 us.
+// of up to 128K, 32/8 heads of 128, take 642 us at 6.8 TB/s, one of 128K 89 us at
+// 6.0 TB/s; of one of 4096 with 8/2 heads of 64 the kernels take 8 us in a graph, a call
+// 28 us, the host's.
 //
 // The visible slots of every (sequence, KV head) are cut into tiles of 64 and all
 // tiles are laid end to end; block c of the grid takes the c-th equal share of

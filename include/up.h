@@ -369,9 +369,10 @@ typedef struct {
  * dims by the angle pos[axes[i] * total_tokens + t] * inv_freq[i]:
  *     (a, b) -> (a cos - b sin, b cos + a sin)
  * where (a, b) are dims (i, i + rot_dim/2), or (2i, 2i+1) with
- * UP_ROPE_INTERLEAVED; dims from rot_dim on are copied.  The angle is reduced
- * exactly (in 2^-64 turns) before its sine and cosine, so far positions lose
- * nothing.
+ * UP_ROPE_INTERLEAVED; dims from rot_dim on are copied.  The angle is reduced in
+ * 2^-64 turns before its sine and cosine; the frequency in turns is rounded once, to
+ * 2^-56 for up to 1 radian a position, so the farthest position's angle is off by 2^-25
+ * turns.
  *
  *   q, k, v    dtype [total_tokens, Hq | Hk | Hk, d] with token strides q_stride,
  *              k_stride, v_stride in elements (views of a fused projection are
@@ -405,7 +406,8 @@ up_status up_append_kv(const void *q, int64_t q_stride, const void *k, int64_t k
  *   softcap   ... then softcap * tanh(logit / softcap) when softcap > 0 (1e-6 and
  *             more) ...
  *   slopes    fp32 [Hq] or NULL: ... then minus slopes[h] * |q_pos - pos_pages|
- *             (needs q_pos and the cache's pos_pages) ...
+ *             (needs q_pos and the cache's pos_pages; a sequence's positions lie within
+ *             2^31 - 1 of one another) ...
  *   q_pos     int32 [queries] or NULL.
  * Softmax is over the visible slots only; a query that sees none gives zeros and
  * a log-sum of -infinity.  What is stored in slots that no query of the call sees has
