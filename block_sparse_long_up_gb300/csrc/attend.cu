@@ -57,7 +57,7 @@ constexpr int kPanel = 128 * 128; // 128 rows x 64 elements
 // Tiles' worth of time that a unit costs beside its tiles: without it a share of short
 // units takes far longer than one of long ones (three ragged sequences, 16/2 heads of
 // 256, capped and biased: 380 us with 0, 305 with 2, 287 with 3, 292 with 5; since rows'
-// references are exact and only logits that count choose the cap's form 323 with 3)
+// references are exact and only logits that count choose the cap's form 321 with 3)
 constexpr int kUnitCost = 3;
 
 template <int D>
@@ -88,15 +88,17 @@ struct Unit {
     int kt0, tiles;     // first key tile and how many
     int hi0;            // causal end of the first token's slots
     int kv;             // cached tokens of the sequence
-    // The slots that rows of the unit see are [first, end), without gaps.  Slots outside
-    // [seen0, seen1) may hold anything.  All four lie in the unit's first and last key
+    // Slots outside [first, end) no row of the unit sees, and those outside [seen0, seen1)
+    // may hold anything.  All four lie in the unit's first and last key
     // tile; a byte each: first, end - 1, seen0, seen1 - 1 in its tile (a unit is read
-    // ahead by every role, so its size counts in registers).
+    // ahead by every role, so its size counts in registers).  The first byte's high bit: there
+    // may be slots between first and end that no row of the unit sees.
     uint32_t edges;
     int64_t prefix;     // width of the units before this one
 
     __device__ __forceinline__ int last_tile() const { return (kt0 + tiles - 1) * kRows; }
-    __device__ __forceinline__ int first() const { return kt0 * kRows + (int)(edges & 255u); }
+    __device__ __forceinline__ int first() const { return kt0 * kRows + (int)(edges & 127u); }
+    __device__ __forceinline__ bool gaps() const { return edges & 128u; }
     __device__ __forceinline__ int end() const { return last_tile() + (int)(edges >> 8 & 255u) + 1; }
     __device__ __forceinline__ int seen0() const { return kt0 * kRows + (int)(edges >> 16 & 255u); }
     __device__ __forceinline__ int seen1() const { return last_tile() + (int)(edges >> 24) + 1; }
@@ -113,7 +115,8 @@ struct Unit {
 struct Plan {
     int64_t W;  // width of one KV head's units
     int units;
-    int bad;    // cu_seqlens is malformed: no unit, every row is that of an empty mask
+    int16_t bad;   // cu_seqlens is malformed: no unit, every row is that of an empty mask
+    int16_t gaps;  // some sequence has slots between those its tokens see that none of them sees
 };
 
 // What a block's share leaves unfinished at its end: a unit that begins in it.
@@ -122,7 +125,7 @@ struct Cut {
 };
 
 struct Layout {
-    size_t seq_off, seen, units, whole, cuts, parts, total;
+    size_t seq_off, seen, units, cuts, parts, total;
     int64_t max_units;
 };
 Layout layout_of(int64_t T, int num_seqs, int Hq, int Hk, int d) {
@@ -133,8 +136,7 @@ Layout layout_of(int64_t T, int num_seqs, int Hq, int Hk, int d) {
     auto take = [&](size_t n) { const size_t at = off; off = (off + n + 255) & ~size_t(255); return at; };
     L.seq_off = take(sizeof(int32_t) * (size_t)(num_seqs + 1));
     L.seen = take(sizeof(int4) * (size_t)(num_seqs + 1));
-    L.units = take(sizeof(Unit) * (size_t)(T > 0 ? T : 1));  // split at every token at worst
-    L.whole = take(sizeof(Unit) * (size_t)(L.max_units > 0 ? L.max_units : 1));
+    L.units = take(sizeof(Unit) * (size_t)(L.max_units > 0 ? L.max_units : 1));
     L.cuts = take(sizeof(Cut) * kMaxSms);
     L.parts = take((size_t)2 * kMaxSms * tiles * kRows * (size_t)(d + 4) * sizeof(float));
     L.total = off;
@@ -147,7 +149,6 @@ struct Params {
     int32_t *seq_off;
     int4 *seen;    // the slots that a sequence's tokens see lie in [x, y); z: with gaps
     Unit *units;
-    Unit *whole;   // the units before some were split
     Cut *cuts;
     float *parts;
     int64_t max_units;
@@ -220,78 +221,46 @@ __device__ __forceinline__ bool apart(int2 a, int2 b) {
     return a.y > 0 && b.y > 0 && max(a.x, b.x) > min(a.y, b.y);
 }
 
-// Splits the units where a token's range lies apart from the one before it and finds the
-// sequences with gaps; returns the units' number (T at most: a unit has a token).
-__device__ __forceinline__ int64_t split_units(const Params &p, int64_t units, int tpu, int64_t *sh) {
-    const AttendArgs &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto range_of = [&](const Unit &u, int tl) {
-        return tl < u.ntok && u.kv >= 0 ? sees(a, u, tl) : make_int2(INT32_MAX, 0);
-    };
-    for (int64_t i = tid; i < units; i += kPlanThreads) p.whole[i] = p.units[i];
-    __syncthreads();
-    for (int64_t i = warp; i < units; i += kPlanThreads / 32) {
-        const Unit u = p.whole[i];
-        int n = 1;
+// Bits [lo, hi) of a word, as far as it has them.
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi) {
+    lo = max(lo, 0), hi = min(hi, 32);
+    return lo < hi ? (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo) : 0u;
+}
+
+// Which of the 32 slots at key0 some row of the unit sees, a bit each; by the whole warp,
+// which shares the unit's tokens among its lanes.  (A word at a time: the roles that ask have
+// few registers.)
+__device__ __forceinline__ uint32_t seen_word(const AttendArgs &a, const Unit &u, int key0) {
+    uint32_t m = 0;
+#pragma unroll 1
+    for (int tl = threadIdx.x & 31; tl < u.ntok; tl += 32) {
+        const int2 r = sees(a, u, tl);
+        m |= span_bits(r.x - key0, r.y - key0);
+    }
+    return __reduce_or_sync(0xffffffffu, m);
+}
+
+// Marks the units in which some range lies apart from that of the token with one before
+// it, and the sequences that have such a place and whose ranges together do not
+// cover one range either (where a few sweeps do not settle it, it is taken for a gap: that
+// costs time only).
+__device__ __forceinline__ void mark_gaps(const Params &p, int64_t units) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int64_t i = tid >> 5; i < units; i += kPlanThreads / 32) {
+        const Unit u = p.units[i];
+        bool gaps = false;
         int2 last = make_int2(INT32_MAX, 0);
         for (int t0 = 0; t0 < u.ntok; t0 += 32) {
-            const int2 r = range_of(u, t0 + lane), b = range_before(r, last);
-            n += __popc(__ballot_sync(0xffffffffu, apart(r, b)));
+            const int2 r = t0 + lane < u.ntok && u.kv >= 0 ? sees(p.a, u, t0 + lane) : make_int2(INT32_MAX, 0);
+            gaps |= apart(r, range_before(r, last));
         }
-        if (lane == 0) p.whole[i].prefix = n;
-    }
-    __syncthreads();
-    int64_t all = 0;
-    for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
-        const int64_t i = u0 + tid;
-        int64_t total;
-        const int64_t at = block_scan(i < units ? p.whole[i].prefix : 0, &total, sh);
-        if (i < units) p.whole[i].prefix = all + at;
-        all += total;
-    }
-    __syncthreads();
-    for (int64_t i = warp; i < units; i += kPlanThreads / 32) {
-        Unit u = p.whole[i];
-        int64_t at = u.prefix;
-        const int tok0 = u.tok0, end = u.tok0 + u.ntok;
-        int2 last = make_int2(INT32_MAX, 0);
-        for (int t0 = 0; t0 < end - tok0; t0 += 32) {
-            u.tok0 = tok0, u.ntok = end - tok0;
-            const int2 r = range_of(u, t0 + lane), b = range_before(r, last);
-            const bool starts = t0 + lane == 0 || apart(r, b);
-            const unsigned m = __ballot_sync(0xffffffffu, starts);
-            if (starts) {
-                u.tok0 = tok0 + t0 + lane;
-                u.ntok = end - u.tok0;  // up to the next one's first token, see below
-                p.units[at + __popc(m & ((1u << lane) - 1u))] = u;
-            }
-            at += __popc(m);
+        if (__any_sync(0xffffffffu, gaps) && lane == 0) {
+            p.units[i].edges |= 128u;
+            atomicOr(&p.seen[u.s].z, 1);
         }
     }
     __syncthreads();
-    for (int64_t i = warp; i < all; i += kPlanThreads / 32) {
-        Unit u = p.units[i];
-        if (i + 1 < all) u.ntok = min(u.ntok, max(p.units[i + 1].tok0 - u.tok0, 0));
-        int lo = INT32_MAX, hi = 0;
-        for (int t0 = 0; t0 < u.ntok; t0 += 32) {
-            const int2 r = range_of(u, t0 + lane);
-            lo = min(lo, r.x);
-            hi = max(hi, r.y);
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        u.tiles = 0;
-        if (lo < hi) u.set_range(lo, hi);
-        if (lane == 0) {
-            p.units[i].ntok = u.ntok;
-            p.units[i].kt0 = u.kt0;
-            p.units[i].tiles = u.tiles;
-            p.units[i].edges = u.edges;
-        }
-    }
-    __syncthreads();
-    // gaps between a sequence's units
-    for (int64_t i = tid; i < all; i += kPlanThreads) {
+    for (int64_t i = tid; i < units; i += kPlanThreads) {  // between a sequence's units
         const Unit u = p.units[i];
         if (!u.tiles) continue;
         int64_t b = i - 1;
@@ -299,7 +268,30 @@ __device__ __forceinline__ int64_t split_units(const Params &p, int64_t units, i
         if (b < 0 || p.units[b].s != u.s) continue;
         if (max(u.first(), p.units[b].first()) > min(u.end(), p.units[b].end())) atomicOr(&p.seen[u.s].z, 1);
     }
-    return all;
+    __syncthreads();
+    // a warp a sequence: what is covered from the first seen slot on
+    for (int s = tid >> 5; s < p.a.kv.num_seqs; s += kPlanThreads / 32) {
+        const int4 all = __ldcg(p.seen + s);
+        if (!all.z) continue;
+        const int c0 = p.a.cu_seqlens[s], c1 = p.a.cu_seqlens[s + 1], kv = p.a.kv.kv_lens[s];
+        int upto = all.x;
+        for (int sweep = 0; sweep < 8 && upto < all.y; ++sweep) {
+            const int before = upto;
+            for (int t0 = c0; t0 < c1 && upto < all.y; t0 += 128) {
+                int2 r[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int t = t0 + 32 * k + lane;
+                    r[k] = t < c1 ? cut_range(reinterpret_cast<const int2 *>(p.a.visible)[t], kv) : make_int2(INT32_MAX, 0);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) upto = max(upto, __reduce_max_sync(0xffffffffu, r[k].x <= upto ? r[k].y : 0));
+            }
+            if (upto == before) break;
+        }
+        __syncwarp();
+        if (upto >= all.y && lane == 0) p.seen[s].z = 0;
+    }
 }
 
 // Lists the units (one block): sequences' unit counts and their scan, then every
@@ -308,7 +300,7 @@ __device__ __forceinline__ int64_t split_units(const Params &p, int64_t units, i
 template <bool kVisible>
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params p, int tpu) {
     __shared__ int64_t sh[32];
-    __shared__ int bad, torn;
+    __shared__ int bad, torn, gaps;
     const AttendArgs &a = p.a;
     const int B = a.kv.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) bad = torn = 0;
@@ -336,7 +328,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
     if (bad || units > p.max_units) {
         if (tid == 0) {
             atomicOr(a.kv.err, kErrCuSeqlens);
-            *p.plan = Plan{0, 0, 1};
+            *p.plan = Plan{0, 0, 1, 0};
         }
         return;
     }
@@ -403,8 +395,9 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
             }
         }
         __syncthreads();
-        if (torn) units = split_units(p, units, tpu, sh);  // seldom, so it may take longer
+        if (torn) mark_gaps(p, units);  // seldom, so it may take longer
     }
+    if (tid == 0) gaps = 0;
     __syncthreads();
     int64_t W = 0;
     for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
@@ -417,12 +410,14 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const Params 
                 // Where the atomics left it.  In a sequence with gaps only what a unit's own rows
                 // see is known to be seen.
                 const int4 r = __ldcg(p.seen + p.units[i].s);
+                if (r.z) gaps = 1;
                 p.units[i].set_seen(r.z ? p.units[i].first() : r.x, r.z ? p.units[i].end() : r.y);
             }
         }
         W += total;
     }
-    if (tid == 0) *p.plan = Plan{W, (int)units, 0};
+    __syncthreads();
+    if (tid == 0) *p.plan = Plan{W, (int)units, 0, (int16_t)gaps};
 }
 
 // The unit at x (0 <= x < W) of a KV head's work.
@@ -604,7 +599,7 @@ __device__ bool load_tile(const CUtensorMap *map, const Params &p, Shared &sh, u
     return true;
 }
 
-template <int D>
+template <int D, bool kGaps>
 __device__ void role_kv(const CUtensorMap *km, const CUtensorMap *vm, const Params &p, Shared &sh, uint32_t ring) {
     using C = Cfg<D>;
     uint32_t it = 0;
@@ -617,7 +612,17 @@ __device__ void role_kv(const CUtensorMap *km, const CUtensorMap *vm, const Para
         const int from = w.u.first() - p.box, end = w.u.end();
         auto page = [&](int t) {
             const int key = w.key0(t) + r;
-            return t < n && r < kRows && key < end && key > from ? page_of(p.a.kv, w.u.s, key) : -1;
+            bool some = t < n && r < kRows && key < end && key > from;
+            if constexpr (kGaps) {
+                if (w.u.gaps() && t < n) {  // boxes in a gap are not looked up
+                    uint32_t box = 0;
+#pragma unroll 1
+                    for (int k = 0; k < kRows; k += 32)
+                        box |= seen_word(p.a, w.u, w.key0(t) + k) & span_bits(r - k, r + p.box - k);
+                    some = some && box;
+                }
+            }
+            return some ? page_of(p.a.kv, w.u.s, key) : -1;
         };
         int p0 = page(0), p1 = page(1), p2 = page(2);
         // the order in which the products need them: one tile runs a step ahead with its keys
@@ -683,10 +688,23 @@ __device__ __forceinline__ void clear_unseen(uint32_t stage, int from, int to) {
     __syncwarp();
 }
 
+// The same for those of the 32 rows from `from` on whose bit in m is clear.
+template <int D>
+__device__ __forceinline__ void clear_gaps(uint32_t stage, int from, uint32_t m) {
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < 32 * 8 * Cfg<D>::kStagePanels; i += 32)
+        if (!(m >> (i >> 3 & 31) & 1u))
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stage + (i >> 8) * kPanel + from * 128 + (i & 255) * 16),
+                         "r"(0)
+                         : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
 // MMA issuer x (0: warp 1, 1: warp 3).  The whole warp walks the loop and one elected
 // lane issues.  With two row tiles both issuers read every stage and each releases
 // it; with one, the keys' issuer and the values' issuer each release a stage twice.
-template <bool kFp16, int D>
+template <bool kFp16, int D, bool kGaps>
 __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring, uint32_t tmem, int x) {
     using C = Cfg<D>;
     constexpr uint32_t id_s = idesc_f32(kFp16, kRows, kRows, false);
@@ -753,8 +771,20 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
     auto ready_v = [&](uint32_t i, int t) {  // the value tile of step t, what nobody sees cleared
         for (int part = 0; part < C::kParts; ++part)
             if (!wait_stage(i + part)) return false;
-        // only the unit's first and last key tile can hold such slots
         const int key0 = w.key0(t);
+        if constexpr (kGaps) {
+            // all that the unit's own rows do not see
+            if (!w.u.gaps() && key0 != w.u.kt0 * kRows && key0 != w.u.last_tile()) return true;
+#pragma unroll 1
+            for (int k = 0; k < kRows; k += 32) {
+                const uint32_t m = seen_word(p.a, w.u, key0 + k);
+                if (m == 0xffffffffu) continue;
+#pragma unroll 1
+                for (int part = 0; part < C::kParts; ++part)
+                    clear_gaps<D>(ring + ((i + part) % C::kStages) * C::kStageBytes, k, m);
+            }
+            return true;
+        }
         if (key0 == edge0 || key0 == edge1) {
             const int from = w.u.seen0() - key0, to = w.u.seen1() - key0;
             for (int part = 0; part < C::kParts; ++part)
@@ -919,7 +949,8 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
         int kp = 0, kp0 = 0;  // positions of this thread's key of the next step and of its first seen one
         const int first = w.u.first(), end = w.u.end();
         auto position = [&](int key) {
-            const int pg = key >= first && key < end ? page_of(a.kv, w.u.s, key) : -1;
+            // (bad pages are reported where their keys are loaded; one in a gap is none)
+            const int pg = key >= first && key < end ? find_page(a.kv, w.u.s, key) : -1;
             return pg < 0 ? 0 : a.kv.pos[(int64_t)pg * a.kv.page_size + key % a.kv.page_size];
         };
         auto fetch_pos = [&](int t) {
@@ -1226,7 +1257,11 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
     }
 }
 
-template <bool kFp16, int D, bool kMore>
+// kGaps: the kernel of calls whose ranges leave gaps.  Of the two that a call with ranges launches
+// the plan lets one work.  In the ordinary kernel the other's code, even as roles of its
+// own that are not run, cost a capped call 7 % and documents 2 %; a launch that returns costs
+// 4 us of 347.
+template <bool kFp16, int D, bool kMore, bool kGaps>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
                   const __grid_constant__ CUtensorMap vm, const Params p) {
@@ -1242,6 +1277,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     if (base - smem_u32(raw) > C::kPad) {  // cannot be; nothing has been touched yet
         if (threadIdx.x == 0) atomicOr(p.a.kv.err, kErrTimeout);
         return;
+    }
+    if constexpr (kGaps) {
+        pdl_wait();
+        if (!p.plan->gaps) return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -1280,17 +1319,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    pdl_wait();
-    if (warp < 4) {
+    if constexpr (!kGaps) pdl_wait();
+    if (!kGaps && p.plan->gaps) {
+        // the other kernel's call
+    } else if (warp < 4) {
         // 128 * 88 + 256 * 208 and 128 * 112 + 256 * 192 are at most 384 * 168
         if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
-            role_kv<D>(&km, &vm, p, sh, ring);
+            role_kv<D, kGaps>(&km, &vm, p, sh, ring);
         } else if (warp == 2) {
             if (lane == 0) role_q<D>(&qm, p, sh, q);
         } else {
-            role_mma<kFp16, D>(p, sh, q, ring, tmem, warp == 1 ? 0 : 1);
+            role_mma<kFp16, D, kGaps>(p, sh, q, ring, tmem, warp == 1 ? 0 : 1);
         }
         __syncwarp();
     } else {
@@ -1439,7 +1480,6 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     p.seq_off = reinterpret_cast<int32_t *>(ws + L.seq_off);
     p.seen = reinterpret_cast<int4 *>(ws + L.seen);
     p.units = reinterpret_cast<Unit *>(ws + L.units);
-    p.whole = reinterpret_cast<Unit *>(ws + L.whole);
     p.cuts = reinterpret_cast<Cut *>(ws + L.cuts);
     p.parts = reinterpret_cast<float *>(ws + L.parts);
     p.max_units = L.max_units;
@@ -1448,13 +1488,17 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     // a scale that is not positive turns the maximum around: the general path
     // scales before it compares
     const bool more = a.softcap > 0.f || a.slopes || !(a.scale > 0.f);
-    auto kernel = more ? attend_kernel<kFp16, D, true> : attend_kernel<kFp16, D, false>;
-    cudaError_t e = more ? allow_smem<attend_kernel<kFp16, D, true>>(C::kSmem)
-                         : allow_smem<attend_kernel<kFp16, D, false>>(C::kSmem);
+    auto kernel = more ? attend_kernel<kFp16, D, true, false> : attend_kernel<kFp16, D, false, false>;
+    cudaError_t e = more ? allow_smem<attend_kernel<kFp16, D, true, false>>(C::kSmem)
+                         : allow_smem<attend_kernel<kFp16, D, false, false>>(C::kSmem);
+    if (e == cudaSuccess && a.visible) e = allow_smem<attend_kernel<kFp16, D, true, true>>(C::kSmem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(a.visible ? attend_plan_kernel<true> : attend_plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, st, p, C::kTiles * p.tpt);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmem, st, qm, km, vm, p);
+    if (e == cudaSuccess && a.visible)
+        e = launch_pdl(attend_kernel<kFp16, D, true, true>, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmem, st, qm,
+                       km, vm, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(attend_join_kernel<kFp16, D>, dim3((unsigned)p.grid, C::kUnitRows / kJoinRows),
                       dim3(kJoinThreads), 0, st, p);

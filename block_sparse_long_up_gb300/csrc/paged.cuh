@@ -25,14 +25,16 @@ struct PagedKv {
     unsigned int *err;
 };
 
-// Page of slot `slot` of sequence s, or -1 (UP_DEVERR_BAD_PAGE set) when the
-// table names a page outside the pool.  0 <= slot < max_pages * page_size.
-__device__ __forceinline__ int page_of(const PagedKv &c, int s, int slot) {
+// Page of slot `slot` of sequence s, or -1 when the table names a page outside the
+// pool.  0 <= slot < max_pages * page_size.
+__device__ __forceinline__ int find_page(const PagedKv &c, int s, int slot) {
     const int pg = c.block_table[(int64_t)s * c.max_pages + slot / c.page_size];
-    if (pg < 0 || pg >= c.num_pages) {
-        atomicOr(c.err, kErrPage);
-        return -1;
-    }
+    return pg < 0 || pg >= c.num_pages ? -1 : pg;
+}
+// The same, and a page outside the pool sets UP_DEVERR_BAD_PAGE.
+__device__ __forceinline__ int page_of(const PagedKv &c, int s, int slot) {
+    const int pg = find_page(c, s, slot);
+    if (pg < 0) atomicOr(c.err, kErrPage);
     return pg;
 }
 
