@@ -703,7 +703,11 @@ __device__ __forceinline__ void clear_gaps(uint32_t stage, int from, uint32_t m)
 
 // MMA issuer x (0: warp 1, 1: warp 3).  The whole warp walks the loop and one elected
 // lane issues.  With two row tiles both issuers read every stage and each releases
-// it; with one, the keys' issuer and the values' issuer each release a stage twice.
+// it; with one, the keys' issuer and the values' issuer each wait for their own stages and
+// release them twice.  A parity tells a phase from the one before only to whoever knows
+// that one to be over, and a stage's last use may have been the other issuer's: so each
+// waits first for what tells it.  (Without, at head_dim 256 a value stage whose last keys
+// were still on their way passed for full.)
 template <bool kFp16, int D, bool kGaps>
 __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring, uint32_t tmem, int x) {
     using C = Cfg<D>;
@@ -849,15 +853,19 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
                 const int buf = use.buf(t, 0, 1);
                 if (x == 0) {
                     const uint32_t i = at_k(t);
-                    for (int part = 0; part < P; ++part)
-                        if (!wait_stage(i + part)) goto out;
-                    // the buffer's weights of two steps ago have been multiplied
+                    // The buffer's weights of two steps ago have been multiplied; so their values
+                    // had come, which these stages or later ones held.
                     if (use.one + t >= 2 && !mbar_wait_warp(smem_u32(&sh.pdone[0][buf]), use.par(t - 2, 1), ab, lim))
                         goto out;
+                    for (int part = 0; part < P; ++part)
+                        if (!wait_stage(i + part)) goto out;
                     qk(0, buf, i, 0);
                     for (int part = 0; part < P; ++part) release(i + part, 2);
                 } else {
                     const uint32_t i = at_v(t);
+                    // The step's logits: its keys had come, which one of these stages may have held.
+                    // (Where a tile is one stage, the ring's order puts only older keys there.)
+                    if (P > 1 && !mbar_wait_warp(smem_u32(&sh.sfull[0][buf]), use.par(t, 1), ab, lim)) goto out;
                     if (!ready_v(i, t)) goto out;
                     if (!pv(0, buf, i, t == 0, 0, use.par(t, 1))) goto out;
                     for (int part = 0; part < P; ++part) release(i + part, 2);

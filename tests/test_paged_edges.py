@@ -298,3 +298,55 @@ def test_copies_of_a_cache_hold_their_own_tensors():
             setattr(m.cache, name, None)
         with pytest.raises(AttributeError):
             delattr(m.cache, name)
+
+
+# ------------------------------------------------------------------ caches that come from memory
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 3, 20])
+@pytest.mark.parametrize("d,dtype", [(256, "bf16"), (256, "fp16"), (128, "bf16"), (64, "bf16")])
+def test_few_tokens_over_a_long_cache_again_and_again(d, dtype, n):
+    """Keys and values that are read once, from memory, in pages far apart: copies land late and
+    out of order, and the products wait for them."""
+    kv = 131072
+    m = Made([(n, kv)], 2, d, 64, dtype, seed=31)
+    q = m.normal(n, 16, d) * 2
+    own = torch.arange(kv - n, kv, device="cuda")
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    first = up.attend_paged(q, m.cu, m.cache)
+    check_at(m, *first, oracle(m, q, own * 0, own + 1, d ** -0.5))
+    for _ in range(30):
+        flush.zero_()
+        for x, y in zip(first, up.attend_paged(q, m.cu, m.cache)):
+            assert torch.equal(x, y)
+    assert up.get_device_error() == 0
+
+
+def ring_gap(stages, parts, pieces, products, logits):
+    """The ring of attention with one row tile a piece: keys a tile ahead of the values, `parts` stages a
+    tile.  The keys' issuer knows the products up to step - products to be done, the values' issuer
+    the logits up to step - logits, each its own tiles.  The first use of a stage whose use
+    before its waiter does not know to be over, or None."""
+    ring, step = [], {}
+    for p, n in enumerate(pieces):
+        for t in range(n):
+            step[p, t] = len(step)
+        for kind, t in [("k", 0)] + [x for t in range(n) for x in ([("k", t + 1)] if t + 1 < n else []) + [("v", t)]]:
+            ring += [(kind, p, t)] * parts
+    for i in range(stages, len(ring)):
+        (kind, p, t), (was, pp, pt) = ring[i], ring[i - stages]
+        behind = 0 if kind == was else products if kind == "k" else logits
+        if step[pp, pt] > step[p, t] - behind:
+            return ring[i], ring[i - stages]
+    return None
+
+
+@pytest.mark.parametrize("stages,parts", [(8, 1), (4, 1), (5, 2)])  # head_dim 64, 128, 256
+def test_waiters_know_the_phase_before(stages, parts):
+    """A parity tells a phase only to a waiter that knows the one before to be over.  The issuers wait
+    for the products of two steps ago and for the step's logits before their stages."""
+    import itertools
+    lists = [p for k in (1, 2, 3) for p in itertools.product(range(1, 8), repeat=k)]
+    assert all(ring_gap(stages, parts, p, 2, 0) is None for p in lists)
+    # stages waited for first: the order that head_dim 256 must not have
+    assert (parts == 1) == all(ring_gap(stages, parts, p, 3, 1) is None for p in lists)
