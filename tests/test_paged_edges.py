@@ -300,6 +300,47 @@ def test_copies_of_a_cache_hold_their_own_tensors():
             delattr(m.cache, name)
 
 
+# ------------------------------------------------------------------ ranges that hop
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["chunks", "falling", "mixed"])
+@pytest.mark.parametrize("Hq,Hk,d,page", [(8, 2, 64, 48), (32, 8, 128, 128), (16, 2, 256, 16)])
+def test_ranges_that_hop(Hq, Hk, d, page, kind):
+    """Ranges in any order that cover all between them, ranges that cover it from the last to the first,
+    and a batch in which one sequence has gaps and the others have not; whole and cut units."""
+    lens = [(700, 3000), (90, 1500), (333, 333)]
+    m = Made(lens, Hk, d, page, "bf16", seed=30)
+    q = m.normal(m.T, Hq, d) * 2
+    g = torch.Generator().manual_seed(4)
+    lo, hi = [], []
+    for s, (n, kv) in enumerate(lens):
+        size = 30 if kv > 1000 else 7
+        chunks = -(-kv // size)
+        at = torch.arange(n) % chunks if n >= chunks else torch.arange(n) * chunks // n
+        size = size if n >= chunks else -(-kv // n) + size
+        at = at * kv // chunks
+        at = at.flip(0) if kind == "falling" else at[torch.randperm(n, generator=g)]
+        if kind == "mixed" and s == 1:
+            at = torch.where(at > kv // 2, at, at // 4)
+        lo.append(at), hi.append(at + size + 3)
+    lo, hi = torch.cat(lo).cuda(), torch.cat(hi).cuda()
+    want = oracle(m, q, lo, hi, d ** -0.5)
+    t0, gaps = 0, []
+    for s, (n, kv) in enumerate(lens):
+        i = torch.arange(-(-kv // page) * page, device="cuda")
+        seen = ((i >= lo[t0:t0 + n, None]) & (i < hi[t0:t0 + n, None].clamp(max=kv))).any(0)
+        gaps.append(not bool(seen[:kv].all()))
+        at, row = m.table[s].long()[i // page], i % page
+        m.kp[at[~seen], :, row[~seen]] = math.nan
+        m.vp[at[~seen], :, row[~seen]] = math.nan
+        m.table[s, :-(-kv // page)].masked_fill_(~seen.view(-1, page).any(1), -1)
+        t0 += n
+    assert gaps == [False, kind == "mixed", False]
+    out, lse = up.attend_paged(q, m.cu, m.cache, visible=torch.stack([lo, hi], 1).to(torch.int32))
+    assert up.get_device_error() == 0
+    check_at(m, out, lse, want)
+
+
 # ------------------------------------------------------------------ caches that come from memory
 
 @pytest.mark.gpu
