@@ -57,7 +57,7 @@ constexpr int kPanel = 128 * 128; // 128 rows x 64 elements
 // Tiles' worth of time that a unit costs beside its tiles: without it a share of short
 // units takes far longer than one of long ones (three ragged sequences, 16/2 heads of
 // 256, capped and biased: 380 us with 0, 305 with 2, 287 with 3, 292 with 5; since rows'
-// references are exact and only logits that count choose the cap's form 321 with 3)
+// references are exact and only logits that count choose the cap's form 319 with 3)
 constexpr int kUnitCost = 3;
 
 template <int D>
