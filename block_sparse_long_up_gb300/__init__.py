@@ -21,16 +21,16 @@ import os
 import torch
 
 from . import _build
-from .paged import (PagedKV, append_kv, attend_paged, attend_paged_workspace, decode_attend,
-                    decode_attend_workspace)
+from .paged import (PagedKV, append_kv, attend_paged, attend_paged_workspace, attend_tree,
+                    attend_tree_workspace, decode_attend, decode_attend_workspace)
 
 __all__ = ["build", "lib", "UpError", "score_blocks_workspace", "score_blocks",
            "score_blocks_paged", "block_csr", "shard_heads",
            "tp_score_blocks", "select_topp",
            "compact_workspace", "compact", "compact_noalloc", "set_kernel_timing_events",
            "set_wait_limit", "get_device_error", "Sparsifier", "SELECT_MAX_BLOCKS", "PagedKV",
-           "append_kv", "attend_paged", "attend_paged_workspace", "decode_attend",
-           "decode_attend_workspace"]
+           "append_kv", "attend_paged", "attend_paged_workspace", "attend_tree",
+           "attend_tree_workspace", "decode_attend", "decode_attend_workspace"]
 
 SELECT_MAX_BLOCKS = 16384
 _lib = None
@@ -104,6 +104,14 @@ def load_library(path):
     L.up_decode_attend_workspace.restype = SZ
     L.up_decode_attend.argtypes = [P, I, P, P, P, P, P, P, SZ, P]
     L.up_decode_attend.restype = I
+    L.up_attend_sinks.argtypes = [P, P, I64, I, P, P, P, I, P, P, P, SZ, P]
+    L.up_attend_sinks.restype = I
+    L.up_decode_sinks.argtypes = [P, I, P, P, P, I, P, P, P, SZ, P]
+    L.up_decode_sinks.restype = I
+    L.up_attend_tree_workspace.argtypes = [I64, I, I, I, I]
+    L.up_attend_tree_workspace.restype = SZ
+    L.up_attend_tree.argtypes = [P, P, P, I64, I, P, P, P, I, P, P, P, SZ, P]
+    L.up_attend_tree.restype = I
     L.up_set_wait_limit.argtypes = [ctypes.c_uint64]
     L.up_set_wait_limit.restype = I
     return L

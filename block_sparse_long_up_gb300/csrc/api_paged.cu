@@ -59,6 +59,10 @@ up_status check_logits(const up_logits *l, const up_paged_kv *c) {
     return UP_OK;
 }
 
+up_status check_sinks(int sinks) {
+    return sinks < 0 ? UP_ERR_INVALID_ARG : sinks > UP_SINKS_MAX ? UP_ERR_UNSUPPORTED : UP_OK;
+}
+
 up::AttendArgs attend_args(const void *q, int Hq, int64_t T, const up_paged_kv *c,
                            const up_logits *l, void *out, float *lse, void *ws,
                            const up::DeviceInfo &di) {
@@ -141,48 +145,62 @@ size_t up_attend_paged_workspace(int64_t total_tokens, int num_seqs, int Hq, int
     return up::attend_workspace(total_tokens, num_seqs, Hq, Hk, d);
 }
 
+size_t up_attend_tree_workspace(int64_t total_tokens, int num_seqs, int Hq, int Hk, int d) {
+    if (!known_sizes(total_tokens, num_seqs, Hq, Hk, d)) return 0;
+    return up::attend_tree_workspace(total_tokens, num_seqs, Hq, Hk, d);
+}
+
 size_t up_decode_attend_workspace(int num_seqs, int Hq, int Hk, int d) {
     if (!known_sizes(num_seqs, num_seqs, Hq, Hk, d)) return 0;
     return up::decode_workspace(num_seqs, Hq, Hk, d);
 }
 
-up_status up_attend_paged(const void *q, const int32_t *cu_seqlens, int64_t total_tokens, int Hq,
-                          const up_paged_kv *cache, const up_logits *logits,
-                          const int32_t *visible, void *out, float *lse, void *workspace,
-                          size_t workspace_bytes, up_stream_t stream) {
-    const up::CallRange range("up_attend_paged");
+}  // extern "C"
+
+namespace {
+
+// up_attend_paged, up_attend_sinks and (with parents) up_attend_tree.
+up_status attend(const void *q, const int32_t *cu_seqlens, const int32_t *parents, int64_t total_tokens,
+                 int Hq, const up_paged_kv *cache, const up_logits *logits, const int32_t *visible,
+                 const int32_t *kv_start, int sinks, bool tree, void *out, float *lse, void *workspace,
+                 size_t workspace_bytes, up_stream_t stream) {
     up_status st = check_cache(cache, Hq);
     if (st != UP_OK) return st;
     if ((st = check_logits(logits, cache)) != UP_OK) return st;
+    if ((st = check_sinks(sinks)) != UP_OK) return st;
     if (!known_sizes(total_tokens, cache->num_seqs, Hq, cache->Hk, cache->d))
         return UP_ERR_INVALID_ARG;
     if (total_tokens == 0) return UP_OK;
-    if (cache->num_seqs < 1 || !q || !cu_seqlens || !out) return UP_ERR_INVALID_ARG;
+    if (cache->num_seqs < 1 || !q || !cu_seqlens || !out || (tree && !parents)) return UP_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(visible, 8) ||
-        !aligned(cu_seqlens, 4))
+        !aligned(cu_seqlens, 4) || !aligned(parents, 4) || !aligned(kv_start, 4))
         return UP_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) ||
         workspace_bytes <
-            up::attend_workspace(total_tokens, cache->num_seqs, Hq, cache->Hk, cache->d))
+            (tree ? up::attend_tree_workspace : up::attend_workspace)(total_tokens, cache->num_seqs, Hq,
+                                                                      cache->Hk, cache->d))
         return UP_ERR_WORKSPACE;
     up::DeviceInfo di{};
     if ((st = up::device_info(&di)) != UP_OK) return st;
     up::AttendArgs a = attend_args(q, Hq, total_tokens, cache, logits, out, lse, workspace, di);
     a.cu_seqlens = cu_seqlens;
     a.visible = visible;
-    if (up::launch_attend(a, di.sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return UP_ERR_CUDA;
+    a.kv_start = kv_start;
+    a.parents = parents;
+    // without a window nothing lies between the first tokens and the others
+    a.sinks = visible || kv_start ? sinks : 0;
+    const auto launch = a.sinks || tree ? up::launch_attend_set : up::launch_attend;
+    if (launch(a, di.sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return UP_ERR_CUDA;
     return UP_OK;
 }
 
-up_status up_decode_attend(const void *q, int Hq, const up_paged_kv *cache,
-                           const up_logits *logits, const int32_t *kv_start, void *out,
-                           float *lse, void *workspace, size_t workspace_bytes,
-                           up_stream_t stream) {
-    const up::CallRange range("up_decode_attend");
+up_status decode(const void *q, int Hq, const up_paged_kv *cache, const up_logits *logits,
+                 const int32_t *kv_start, int sinks, void *out, float *lse, void *workspace,
+                 size_t workspace_bytes, up_stream_t stream) {
     up_status st = check_cache(cache, Hq);
     if (st != UP_OK) return st;
     if ((st = check_logits(logits, cache)) != UP_OK) return st;
+    if ((st = check_sinks(sinks)) != UP_OK) return st;
     if (!known_sizes(cache->num_seqs, cache->num_seqs, Hq, cache->Hk, cache->d))
         return UP_ERR_INVALID_ARG;
     if (cache->num_seqs == 0) return UP_OK;
@@ -197,9 +215,58 @@ up_status up_decode_attend(const void *q, int Hq, const up_paged_kv *cache,
     up::AttendArgs a =
         attend_args(q, Hq, cache->num_seqs, cache, logits, out, lse, workspace, di);
     a.kv_start = kv_start;
+    a.sinks = kv_start ? sinks : 0;
     if (up::launch_decode(a, di.sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return UP_ERR_CUDA;
     return UP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+up_status up_attend_paged(const void *q, const int32_t *cu_seqlens, int64_t total_tokens, int Hq,
+                          const up_paged_kv *cache, const up_logits *logits,
+                          const int32_t *visible, void *out, float *lse, void *workspace,
+                          size_t workspace_bytes, up_stream_t stream) {
+    const up::CallRange range("up_attend_paged");
+    return attend(q, cu_seqlens, nullptr, total_tokens, Hq, cache, logits, visible, nullptr, 0, false, out, lse,
+                  workspace, workspace_bytes, stream);
+}
+
+up_status up_attend_sinks(const void *q, const int32_t *cu_seqlens, int64_t total_tokens, int Hq,
+                          const up_paged_kv *cache, const up_logits *logits,
+                          const int32_t *visible, int sinks, void *out, float *lse,
+                          void *workspace, size_t workspace_bytes, up_stream_t stream) {
+    const up::CallRange range("up_attend_sinks");
+    return attend(q, cu_seqlens, nullptr, total_tokens, Hq, cache, logits, visible, nullptr, sinks, false, out,
+                  lse, workspace, workspace_bytes, stream);
+}
+
+up_status up_attend_tree(const void *q, const int32_t *cu_seqlens, const int32_t *parents,
+                         int64_t total_tokens, int Hq, const up_paged_kv *cache,
+                         const up_logits *logits, const int32_t *kv_start, int sinks, void *out,
+                         float *lse, void *workspace, size_t workspace_bytes,
+                         up_stream_t stream) {
+    const up::CallRange range("up_attend_tree");
+    return attend(q, cu_seqlens, parents, total_tokens, Hq, cache, logits, nullptr, kv_start, sinks, true, out,
+                  lse, workspace, workspace_bytes, stream);
+}
+
+up_status up_decode_attend(const void *q, int Hq, const up_paged_kv *cache,
+                           const up_logits *logits, const int32_t *kv_start, void *out,
+                           float *lse, void *workspace, size_t workspace_bytes,
+                           up_stream_t stream) {
+    const up::CallRange range("up_decode_attend");
+    return decode(q, Hq, cache, logits, kv_start, 0, out, lse, workspace, workspace_bytes, stream);
+}
+
+up_status up_decode_sinks(const void *q, int Hq, const up_paged_kv *cache,
+                          const up_logits *logits, const int32_t *kv_start, int sinks, void *out,
+                          float *lse, void *workspace, size_t workspace_bytes,
+                          up_stream_t stream) {
+    const up::CallRange range("up_decode_sinks");
+    return decode(q, Hq, cache, logits, kv_start, sinks, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

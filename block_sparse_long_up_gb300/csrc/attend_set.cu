@@ -1,0 +1,189 @@
+// attend_set.cu -- attention of new tokens that see more than one range of slots: a window and
+// the first tokens of the cache that stay visible (sinks), or the cache and a tree of
+// drafted tokens at its end.  The plans, and the launches (see attend_tc.cuh for the kernel).
+//
+// Per row the set is a window [first, end), the slots below `sinks` and, in a tree, one bit for
+// each drafted token: its ancestors and itself.  A unit's key tiles are those of the first
+// slots and those of its rows' windows; between the two nothing is read.  Only tiles at the
+// windows' edges and in the tree take the masked path, where a row's 32 slots are one word.
+#include "attend_tc.cuh"
+
+namespace up {
+
+namespace {
+
+// A unit's tiles: those of the first `send` slots, and those of [first, wend) behind them.
+__device__ __forceinline__ void set_of(Unit &u, int first, int wend, int send, bool gaps) {
+    const int st = (send + kRows - 1) / kRows;
+    const int wt = wend > 0 ? (wend + kRows - 1) / kRows - max(first / kRows, st) : 0;
+    u.kt0 = gaps ? ~first : first;
+    u.edges = (uint32_t)wend;
+    u.tiles = st + max(wt, 0);
+}
+
+// Block 0 lists the units.  With a tree the other blocks write each token's bits: a thread walks
+// its token's line of parents, whose numbers fall at every step.
+template <bool kTree>
+__global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Params p, uint32_t *bits, int tpu) {
+    __shared__ int64_t sh[32];
+    __shared__ int bad;
+    const AttendArgs &a = p.a;
+    const int B = a.kv.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) bad = 0;
+    pdl_wait();
+    pdl_trigger();  // what came before is complete: the main kernel's set-up may overlap
+    __syncthreads();
+    if (kTree && blockIdx.x > 0) {
+        const int t = ((int)blockIdx.x - 1) * kPlanThreads + tid;
+        if (t >= a.T) return;
+        const int s = seq_of_token(a.cu_seqlens, B, t, a.T, a.kv.err);
+        uint32_t m[kTreeWords] = {};
+        if (s >= 0) {
+            const int c0 = a.cu_seqlens[s];
+            int j = t - c0;
+            while (j >= 0 && j < UP_TREE_MAX) {
+#pragma unroll
+                for (int i = 0; i < kTreeWords; ++i) m[i] |= (j >> 5) == i ? 1u << (j & 31) : 0u;
+                const int up = a.parents[c0 + j];
+                if (up >= j) break;  // malformed: the sequence has no unit with tiles
+                j = up;
+            }
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>(bits + (int64_t)t * kTreeWords);
+#pragma unroll
+        for (int i = 0; i < kTreeWords / 4; ++i)
+            dst[i] = make_uint4(m[4 * i], m[4 * i + 1], m[4 * i + 2], m[4 * i + 3]);
+        return;
+    }
+    int64_t units = 0;
+    for (int s0 = 0; s0 < B; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int64_t n = 0;
+        if (s < B) {
+            const int c0 = a.cu_seqlens[s], c1 = a.cu_seqlens[s + 1];
+            if (c0 < 0 || c1 < c0 || c1 > a.T || (s == 0 && c0 != 0) || (s == B - 1 && c1 != a.T)) bad = 1;
+            else n = (c1 - c0 + tpu - 1) / tpu;
+        }
+        int64_t total;
+        const int64_t at = units + block_scan(n, &total, sh);
+        if (s < B) {
+            p.seq_off[s] = (int)(at < p.max_units ? at : p.max_units);
+            p.seen[s] = make_int4(0, 0, 0, 0);
+        }
+        units += total;
+    }
+    __syncthreads();
+    if (bad || units > p.max_units) {
+        if (tid == 0) {
+            atomicOr(a.kv.err, kErrCuSeqlens);
+            *p.plan = Plan{0, 0, 1, 0};
+        }
+        return;
+    }
+    if constexpr (kTree) {
+        // a warp a sequence: every parent comes before its child
+        for (int s = warp; s < B; s += kPlanThreads / 32) {
+            const int c0 = a.cu_seqlens[s], n = a.cu_seqlens[s + 1] - c0;
+            bool wrong = n > UP_TREE_MAX;
+            for (int j = lane; j < n && !wrong; j += 32) wrong = a.parents[c0 + j] < -1 || a.parents[c0 + j] >= j;
+            if (__any_sync(0xffffffffu, wrong) && lane == 0) {
+                p.seen[s].z = 1;
+                atomicOr(a.kv.err, kErrTree);
+            }
+        }
+        __syncthreads();
+    }
+    // a warp a unit, its tokens on the lanes
+    for (int64_t i = warp; i < units; i += kPlanThreads / 32) {
+        int lo = 0, hi = B - 1;  // the last sequence with seq_off <= i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.seq_off[mid] <= i) lo = mid; else hi = mid - 1;
+        }
+        const int c0 = a.cu_seqlens[lo], c1 = a.cu_seqlens[lo + 1];
+        Unit u{};
+        u.s = lo;
+        u.tok0 = c0 + (int)(i - p.seq_off[lo]) * tpu;
+        u.ntok = min(tpu, c1 - u.tok0);
+        u.kv = kv_len_of(a.kv, lo, c1 - c0);
+        if (u.kv >= 0 && !p.seen[lo].z) {
+            int first = INT32_MAX, end = 0, some = 0;
+            bool gaps = false;
+            if constexpr (kTree) {
+                const int past = u.kv - (c1 - c0);
+                if (a.kv_start) {
+                    for (int t = lane; t < u.ntok; t += 32) first = min(first, max(a.kv_start[u.tok0 + t], 0));
+                    first = min(__reduce_min_sync(0xffffffffu, first), past);
+                } else {
+                    first = 0;
+                }
+                u.hi0 = past;
+                set_of(u, first, u.kv, min(a.sinks, past), false);
+            } else {
+                for (int t = lane; t < u.ntok; t += 32) {
+                    const int2 *v = reinterpret_cast<const int2 *>(a.visible) + u.tok0 + t;
+                    const int2 r = cut_range(*v, u.kv), before = t ? cut_range(v[-1], u.kv) : r;
+                    first = min(first, r.x);
+                    end = max(end, r.y);
+                    some = max(some, min(v->y, u.kv));
+                    gaps |= r.y > 0 && max(before.x, r.x) > min(before.y, r.y);
+                }
+                first = __reduce_min_sync(0xffffffffu, first);
+                end = __reduce_max_sync(0xffffffffu, end);
+                u.hi0 = min(a.sinks, max(__reduce_max_sync(0xffffffffu, some), 0));
+                set_of(u, end > 0 ? first : 0, end, u.hi0, __any_sync(0xffffffffu, gaps));
+            }
+        }
+        if (lane == 0) p.units[i] = u;
+    }
+    __syncthreads();
+    int64_t W = 0;
+    for (int64_t u0 = 0; u0 < units; u0 += kPlanThreads) {
+        const int64_t i = u0 + tid;
+        int64_t total;
+        const int64_t at = block_scan(i < units ? width_of(p.units[i]) : 0, &total, sh);
+        if (i < units) p.units[i].prefix = W + at;
+        W += total;
+    }
+    if (tid == 0) *p.plan = Plan{W, (int)units, 0, 0};
+}
+
+template <bool kFp16, int D>
+cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
+    using C = Cfg<D>;
+    Params p{};
+    CUtensorMap qm, km, vm;
+    const size_t used = params_of<D>(a, num_sms, p);
+    uint32_t *bits = a.parents ? reinterpret_cast<uint32_t *>(static_cast<char *>(a.workspace) + used) : nullptr;
+    p.bits = bits;
+    if (!encode_maps(a, p.tpt, p.box, &qm, &km, &vm)) return cudaErrorInvalidValue;
+    const bool more = a.softcap > 0.f || a.slopes || !(a.scale > 0.f);
+    auto kernel = more ? attend_kernel<kFp16, D, true, kSet> : attend_kernel<kFp16, D, false, kSet>;
+    cudaError_t e = more ? allow_smem<attend_kernel<kFp16, D, true, kSet>>(C::kSmem)
+                         : allow_smem<attend_kernel<kFp16, D, false, kSet>>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    const unsigned blocks = a.parents ? 1 + (unsigned)((a.T + kPlanThreads - 1) / kPlanThreads) : 1;
+    e = launch_pdl(a.parents ? attend_set_plan_kernel<true> : attend_set_plan_kernel<false>, dim3(blocks),
+                   dim3(kPlanThreads), 0, st, p, bits, C::kTiles * p.tpt);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kernel, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmem, st, qm, km, vm, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attend_join_kernel<kFp16, D>, dim3((unsigned)p.grid, C::kUnitRows / kJoinRows),
+                      dim3(kJoinThreads), 0, st, p);
+}
+
+}  // namespace
+
+size_t attend_tree_workspace(int64_t T, int num_seqs, int Hq, int Hk, int d) {
+    return layout_of(T, num_seqs, Hq, Hk, d).total + (size_t)T * kTreeWords * sizeof(uint32_t);
+}
+
+cudaError_t launch_attend_set(const AttendArgs &a, int num_sms, cudaStream_t st) {
+    switch (a.kv.d) {
+        case 64: return a.kv.fp16 ? launch_type<true, 64>(a, num_sms, st) : launch_type<false, 64>(a, num_sms, st);
+        case 128: return a.kv.fp16 ? launch_type<true, 128>(a, num_sms, st) : launch_type<false, 128>(a, num_sms, st);
+        default: return a.kv.fp16 ? launch_type<true, 256>(a, num_sms, st) : launch_type<false, 256>(a, num_sms, st);
+    }
+}
+
+}  // namespace up

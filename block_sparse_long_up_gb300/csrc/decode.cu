@@ -61,9 +61,11 @@ struct Cfg {
 constexpr int kUnitCost = 2;
 
 // First slot and end of what sequence s's query sees, and the tiles they take
-// (tiles begin at a multiple of 16 slots, so 16 slots never straddle a page).
+// (tiles begin at a multiple of 16 slots, so 16 slots never straddle a page).  First tokens
+// that stay visible apart from the window, the slots below sinks < lo, take stiles tiles of their
+// own in front.
 struct Span {
-    int lo, hi, first, tiles;
+    int lo, hi, first, tiles, sinks, stiles;
     __device__ __forceinline__ int width() const { return tiles ? tiles + kUnitCost : 0; }
 };
 
@@ -71,9 +73,17 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int s) {
     Span r;
     r.hi = max(kv_len_of(a.kv, s, 0), 0);
     r.lo = a.kv_start ? max(a.kv_start[s], 0) : 0;
-    if (r.lo >= r.hi) r.lo = r.hi = 0;
+    r.sinks = min(a.sinks, r.hi);
+    if (r.lo >= r.hi) {
+        r.hi = r.sinks;
+        r.lo = r.sinks = 0;
+    } else if (r.lo <= r.sinks) {
+        r.lo = a.sinks ? 0 : r.lo;
+        r.sinks = 0;
+    }
     r.first = r.lo & ~(kGroup - 1);
-    r.tiles = (r.hi - r.first + kTile - 1) / kTile;
+    r.stiles = (r.sinks + kTile - 1) / kTile;
+    r.tiles = (r.hi - r.first + kTile - 1) / kTile + r.stiles;
     return r;
 }
 
@@ -173,7 +183,7 @@ __device__ __forceinline__ float *part_of(const AttendArgs &a, int D, int slot) 
     return static_cast<float *>(a.workspace) + (int64_t)slot * a.g * (D + 4);
 }
 
-template <bool kFp16, int D, bool kFew, bool kMore>
+template <bool kFp16, int D, bool kFew, bool kMore, bool kSinks>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const AttendArgs a) {
     using C = Cfg<D>;
     constexpr int kCpr = D / 8;          // 16-byte chunks of a row
@@ -245,15 +255,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
             for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
 
         const int steps = tb - ta;
-        const int key_a = sp.first + ta * kTile + warp * kGroup;  // this warp's first slot
+        // this warp's first slot of a step, and the slots that it may see
+        const int key_a = sp.first + (ta - (kSinks ? sp.stiles : 0)) * kTile + warp * kGroup;
+        const int apart = kSinks ? sp.stiles - ta : 0;  // steps of the first tokens
+        auto key_of = [&](int step) {
+            return kSinks && step < apart ? (ta + step) * kTile + warp * kGroup : key_a + step * kTile;
+        };
+        auto lo_of = [&](int step) { return kSinks && step < apart ? 0 : sp.lo; };
+        auto hi_of = [&](int step) { return kSinks && step < apart ? sp.sinks : sp.hi; };
         auto page_at = [&](int step) -> int {
-            const int key = key_a + step * kTile;
-            return step < steps && key < sp.hi ? page_of(a.kv, s, key) : -1;
+            const int key = key_of(step);
+            return step < steps && key < hi_of(step) ? page_of(a.kv, s, key) : -1;
         };
         int pg = page_at(0);  // page of the next step to load, looked up a step ahead
         auto load = [&](int step) {
             if (step < steps) {
-                const int key = key_a + step * kTile, in_page = key % a.kv.page_size;
+                const int key = key_of(step), in_page = key % a.kv.page_size;
+                const int lo = lo_of(step), hi = hi_of(step);
                 const uint32_t st = ring + (step % C::kStages) * C::kStageBytes;
                 const int64_t rb = pg < 0 ? 0 : ((int64_t)pg * Hk + j) * a.kv.page_size + in_page;
                 const int r0 = lane / kCpr, c = lane % kCpr;
@@ -262,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
 #pragma unroll
                 for (int i = 0; i < kGroup / kRpi; ++i) {
                     const int r = r0 + i * kRpi;
-                    const bool ok = pg >= 0 && key + r >= sp.lo && key + r < sp.hi;
+                    const bool ok = pg >= 0 && key + r >= lo && key + r < hi;
                     const int off = ok ? r * C::kRowBytes + c * 16 : 0;
                     const uint32_t dst = st + r * C::kRowBytes + ((c ^ (r & 7)) << 4);
                     cp16(dst, ks + off, ok);
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int i = 0; i < 2 * kR; ++i) x[n][i] += x2[n][i];
-            const int key = key_a + step * kTile;
+            const int key = key_of(step), from = lo_of(step), to = hi_of(step);
             // logits in log2 units
             if constexpr (kMore) {
                 if (a.softcap > 0.f) {
@@ -335,13 +353,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kPerSm) decode_kernel(const 
                         }
                     }
                 }
-            if (key < sp.lo || key + kGroup > sp.hi) {
+            if (key < from || key + kGroup > to) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int i = 0; i < 2 * kR; ++i) {
                         const int k = key + 8 * n + col + (i & 1);
-                        if (k < sp.lo || k >= sp.hi) x[n][i] = -INFINITY;
+                        if (k < from || k >= to) x[n][i] = -INFINITY;
                     }
             }
             bool moved = false;
@@ -519,13 +537,13 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const AttendA
     if (a.lse && tid == 0) a.lse[orow] = (ref + log2f(L)) * kLn2;
 }
 
-template <bool kFp16, int D, bool kFew, bool kMore>
+template <bool kFp16, int D, bool kFew, bool kMore, bool kSinks>
 cudaError_t launch_variant(const AttendArgs &a, int num_sms, cudaStream_t st) {
     using C = Cfg<D>;
     const int grid = (num_sms < kMaxSms ? num_sms : kMaxSms) * C::kPerSm;
-    cudaError_t e = allow_smem<decode_kernel<kFp16, D, kFew, kMore>>(C::kSmem);
+    cudaError_t e = allow_smem<decode_kernel<kFp16, D, kFew, kMore, kSinks>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(decode_kernel<kFp16, D, kFew, kMore>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, st, a);
+    e = launch_pdl(decode_kernel<kFp16, D, kFew, kMore, kSinks>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, st, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(decode_join_kernel<kFp16, D>, dim3((unsigned)(a.kv.num_seqs * a.Hq)),
                       dim3(kJoinThreads), 0, st, a, grid);
@@ -535,10 +553,12 @@ template <bool kFp16, int D>
 cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     // up to 8 query heads a group: half of the fragment's rows carry no weights
     const bool few = a.g <= 8, more = a.softcap > 0.f || a.slopes;
-    if (few) return more ? launch_variant<kFp16, D, true, true>(a, num_sms, st)
-                         : launch_variant<kFp16, D, true, false>(a, num_sms, st);
-    return more ? launch_variant<kFp16, D, false, true>(a, num_sms, st)
-                : launch_variant<kFp16, D, false, false>(a, num_sms, st);
+    if (a.sinks) return few ? launch_variant<kFp16, D, true, true, true>(a, num_sms, st)
+                            : launch_variant<kFp16, D, false, true, true>(a, num_sms, st);
+    if (few) return more ? launch_variant<kFp16, D, true, true, false>(a, num_sms, st)
+                         : launch_variant<kFp16, D, true, false, false>(a, num_sms, st);
+    return more ? launch_variant<kFp16, D, false, true, false>(a, num_sms, st)
+                : launch_variant<kFp16, D, false, false, false>(a, num_sms, st);
 }
 
 }  // namespace

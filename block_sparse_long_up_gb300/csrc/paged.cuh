@@ -3,6 +3,7 @@
 
 #include <cuda_fp16.h>
 
+#include "../../include/up.h"
 #include "common.cuh"
 
 namespace up {
@@ -12,6 +13,9 @@ constexpr unsigned int kErrCuSeqlens = 0x1u;
 constexpr unsigned int kErrTimeout = 0x4u;
 constexpr unsigned int kErrPage = 0x8u;
 constexpr unsigned int kErrKvLens = 0x40u;
+constexpr unsigned int kErrTree = 0x80u;
+constexpr unsigned int kErrNoPages = 0x100u;
+constexpr unsigned int kErrRefs = 0x200u;
 
 struct PagedKv {
     void *k;
@@ -85,7 +89,8 @@ struct AttendArgs {
     const void *q;
     const int32_t *cu_seqlens;  // null: one token per sequence (decode)
     const int32_t *visible;     // attend: [T][2] or null
-    const int32_t *kv_start;    // decode: [num_seqs] or null
+    const int32_t *kv_start;    // decode: [num_seqs], tree: [T], or null
+    const int32_t *parents;     // tree: [T], else null
     const float *slopes;        // [Hq] or null
     const int32_t *q_pos;       // [T] or null
     void *out;
@@ -93,11 +98,15 @@ struct AttendArgs {
     void *workspace;
     float scale, softcap;
     int T, Hq, g;
+    int sinks;  // slots at the cache's beginning that stay visible
     long long wait_limit;
 };
 size_t attend_workspace(int64_t T, int num_seqs, int Hq, int Hk, int d);
 size_t decode_workspace(int num_seqs, int Hq, int Hk, int d);
+size_t attend_tree_workspace(int64_t T, int num_seqs, int Hq, int Hk, int d);
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
+// with a.sinks and a.visible, or with a.parents
+cudaError_t launch_attend_set(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_decode(const AttendArgs &a, int num_sms, cudaStream_t st);
 
 }  // namespace up

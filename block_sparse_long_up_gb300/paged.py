@@ -1,9 +1,10 @@
-"""Paged KV cache: append with rotary positions, attention of new tokens and
-decode attention over it (the paged-cache section of include/up.h).
+"""Paged KV cache: append with rotary positions, attention of new tokens, of drafted
+trees and decode attention over it (the paged-cache section of include/up.h).
 
     cache = PagedKV(k_pages, v_pages, block_table, kv_lens, pos_pages)
     q = append_kv(q, k, v, pos, cu_seqlens, cache, inv_freq)
     out, lse = attend_paged(q, cu_seqlens, cache)       # a chunk of new tokens
+    out, lse = attend_tree(q, cu_seqlens, parents, cache)  # drafted tokens
     out, lse = decode_attend(q, cache)                  # one new token per sequence
 """
 from __future__ import annotations
@@ -11,6 +12,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import operator
 
 import torch
 
@@ -213,6 +215,11 @@ def append_kv(q, k, v, pos, cu_seqlens, cache, inv_freq, axes=None, interleaved=
     return q_out
 
 
+def _int32(n):
+    """n for a C int; what does not fit is refused like any other number that is too large or small."""
+    return max(-1, min(n, 2 ** 31 - 1))
+
+
 @functools.lru_cache(maxsize=64)
 def _plain_logits(scale, softcap):
     lg = _CLogits(scale, softcap, None, None)  # read by the library during a call, never written
@@ -254,20 +261,28 @@ def attend_paged_workspace(total_tokens, num_seqs, Hq, Hk, d) -> int:
 
 
 @functools.lru_cache(maxsize=256)
+def attend_tree_workspace(total_tokens, num_seqs, Hq, Hk, d) -> int:
+    """Bytes of attend_tree's workspace (0: sizes it does not take)."""
+    return int(_L().up_attend_tree_workspace(total_tokens, num_seqs, Hq, Hk, d))
+
+
+@functools.lru_cache(maxsize=256)
 def decode_attend_workspace(num_seqs, Hq, Hk, d) -> int:
     """Bytes of decode_attend's workspace (0: sizes it does not take)."""
     return int(_L().up_decode_attend_workspace(num_seqs, Hq, Hk, d))
 
 
 def attend_paged(q, cu_seqlens, cache, scale=None, softcap=0.0, slopes=None, q_pos=None,
-                 visible=None, out=None, lse=None, workspace=None, stream=None):
+                 visible=None, out=None, lse=None, workspace=None, stream=None, sinks=0):
     """Attention of the new tokens q [T, Hq, d] (packed by cu_seqlens int32
     [num_seqs + 1]) over the cache, which holds their own keys too; returns (out
     [T, Hq, d], lse fp32 [T, Hq]).  See up_attend_paged.
 
     scale (default d ** -0.5), softcap (0: none); slopes fp32 [Hq] with q_pos int32
     [T]: a bias of -slope * |q_pos - key position|; visible int32 [T, 2]: the slots
-    [first, end) each query sees (default: causal)."""
+    [first, end) each query sees (default: causal); sinks: so many first slots of a sequence
+    stay visible before a query's end (see up_attend_sinks)."""
+    sinks = operator.index(sinks)
     dev = cache.device
     if _rows(q, "q", cache) != q.shape[1] * cache.d:
         raise ValueError("q must be contiguous")
@@ -288,21 +303,69 @@ def attend_paged(q, cu_seqlens, cache, scale=None, softcap=0.0, slopes=None, q_p
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         else:
             size = workspace.numel() * workspace.element_size()
-        st = _L().up_attend_paged(q.data_ptr(), cu_seqlens.data_ptr(), T, Hq, cache.ref, lg,
-                             None if visible is None else visible.data_ptr(),
-                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
-                             _raw(stream, dev))
+        if sinks:
+            st = _L().up_attend_sinks(q.data_ptr(), cu_seqlens.data_ptr(), T, Hq, cache.ref, lg,
+                                      None if visible is None else visible.data_ptr(), _int32(sinks),
+                                      out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
+                                      _raw(stream, dev))
+        else:
+            st = _L().up_attend_paged(q.data_ptr(), cu_seqlens.data_ptr(), T, Hq, cache.ref, lg,
+                                      None if visible is None else visible.data_ptr(),
+                                      out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
+                                      _raw(stream, dev))
     if st:
-        raise _error("up_attend_paged", st)
+        raise _error("up_attend_sinks" if sinks else "up_attend_paged", st)
+    return out, lse
+
+
+def attend_tree(q, cu_seqlens, parents, cache, scale=None, softcap=0.0, slopes=None, q_pos=None,
+                kv_start=None, sinks=0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of drafted tokens q [T, Hq, d] (packed by cu_seqlens int32
+    [num_seqs + 1]) over the cache, whose last slots hold them: each sees the slots before
+    the drafted ones, its ancestors and itself; returns (out [T, Hq, d], lse fp32
+    [T, Hq]).  See up_attend_tree.
+
+    parents int32 [T]: a parent's number among its sequence's drafted tokens, less than the
+    child's, or -1; kv_start int32 [T]: the first slot that each token sees, beside
+    the first `sinks` of its sequence; the other arguments are attend_paged's."""
+    sinks = operator.index(sinks)
+    dev = cache.device
+    if _rows(q, "q", cache) != q.shape[1] * cache.d:
+        raise ValueError("q must be contiguous")
+    T, Hq, d = q.shape
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, (cache.num_seqs + 1,))
+    _need(parents, "parents", torch.int32, dev, (T,))
+    lg = _logits(cache, T, Hq, d ** -0.5 if scale is None else scale, softcap, slopes, q_pos)
+    if kv_start is not None:
+        _need(kv_start, "kv_start", torch.int32, dev, (T,))
+    if out is not None or lse is not None or workspace is not None:
+        _given(out, lse, workspace, cache, q.shape)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=cache.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        if workspace is None:
+            size = attend_tree_workspace(T, cache.num_seqs, Hq, cache.Hk, d)
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        else:
+            size = workspace.numel() * workspace.element_size()
+        st = _L().up_attend_tree(q.data_ptr(), cu_seqlens.data_ptr(), parents.data_ptr(), T, Hq, cache.ref, lg,
+                                 None if kv_start is None else kv_start.data_ptr(), _int32(sinks),
+                                 out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
+                                 _raw(stream, dev))
+    if st:
+        raise _error("up_attend_tree", st)
     return out, lse
 
 
 def decode_attend(q, cache, scale=None, softcap=0.0, slopes=None, q_pos=None, kv_start=None,
-                  out=None, lse=None, workspace=None, stream=None):
+                  out=None, lse=None, workspace=None, stream=None, sinks=0):
     """Attention of one new token per sequence, q [num_seqs, Hq, d], over the cache;
     returns (out, lse fp32 [num_seqs, Hq]).  See up_decode_attend.  kv_start int32
-    [num_seqs]: the first visible slot of each sequence; the other arguments are
-    attend_paged's."""
+    [num_seqs]: the first visible slot of each sequence; sinks: so many first slots stay
+    visible beside those (see up_decode_sinks); the other arguments are attend_paged's."""
+    sinks = operator.index(sinks)
     dev = cache.device
     if _rows(q, "q", cache) != q.shape[1] * cache.d:
         raise ValueError("q must be contiguous")
@@ -324,10 +387,16 @@ def decode_attend(q, cache, scale=None, softcap=0.0, slopes=None, q_pos=None, kv
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         else:
             size = workspace.numel() * workspace.element_size()
-        st = _L().up_decode_attend(q.data_ptr(), Hq, cache.ref, lg,
-                             None if kv_start is None else kv_start.data_ptr(),
-                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
-                             _raw(stream, dev))
+        if sinks:
+            st = _L().up_decode_sinks(q.data_ptr(), Hq, cache.ref, lg,
+                                      None if kv_start is None else kv_start.data_ptr(), _int32(sinks),
+                                      out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
+                                      _raw(stream, dev))
+        else:
+            st = _L().up_decode_attend(q.data_ptr(), Hq, cache.ref, lg,
+                                       None if kv_start is None else kv_start.data_ptr(),
+                                       out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), size,
+                                       _raw(stream, dev))
     if st:
-        raise _error("up_decode_attend", st)
+        raise _error("up_decode_sinks" if sinks else "up_decode_attend", st)
     return out, lse

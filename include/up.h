@@ -68,6 +68,11 @@ typedef enum {
 #define UP_DEVERR_BAD_KV_LENS 0x40u    /* kv_lens[s] negative, below the sequence's new tokens, or above
                                           max_pages * page_size (the sequence is left out) */
 
+#define UP_DEVERR_BAD_TREE 0x80u       /* drafted tokens: a parent that does not come before its child, or more
+                                          than UP_TREE_MAX tokens (the sequence's rows are those of an empty mask) */
+#define UP_DEVERR_NO_PAGES 0x100u      /* the pool has too few free pages for the call */
+#define UP_DEVERR_BAD_REFS 0x200u      /* a page released that nobody holds, or pool counts that cannot be */
+
 /* Largest nb_s that the selection calls rank on chip (1M tokens at G = 64). */
 #define UP_SELECT_MAX_BLOCKS 16384
 
@@ -470,6 +475,62 @@ up_status up_decode_attend(const void *q, int Hq, const up_paged_kv *cache,
                            const up_logits *logits, const int32_t *kv_start, void *out,
                            float *lse, void *workspace, size_t workspace_bytes,
                            up_stream_t stream);
+
+/*
+ * Attention with first tokens that stay visible: up_attend_paged and
+ * up_decode_attend where a query sees, beside its window, the first `sinks` slots of
+ * its sequence -- as many of them as lie before the window's end.
+ *
+ * Query t sees slot i iff i < end and (i >= first or i < sinks), with first and end from
+ * visible[t] (cut to [0, kv_lens[s])), or kv_start[s] and kv_lens[s].  The pages between
+ * the first slots and the window are not read and need no valid entry in the block table.
+ *   sinks    0 .. UP_SINKS_MAX (0: the calls above; so is a NULL visible or kv_start, which
+ *            leaves nothing between the two).
+ * Everything else, the workspaces too, is as for those calls.  UP_ERR_INVALID_ARG for
+ * sinks below 0, UP_ERR_UNSUPPORTED above UP_SINKS_MAX.
+ */
+#define UP_SINKS_MAX 4096
+
+up_status up_attend_sinks(const void *q, const int32_t *cu_seqlens, int64_t total_tokens, int Hq,
+                          const up_paged_kv *cache, const up_logits *logits,
+                          const int32_t *visible, int sinks, void *out, float *lse,
+                          void *workspace, size_t workspace_bytes, up_stream_t stream);
+
+up_status up_decode_sinks(const void *q, int Hq, const up_paged_kv *cache,
+                          const up_logits *logits, const int32_t *kv_start, int sinks, void *out,
+                          float *lse, void *workspace, size_t workspace_bytes,
+                          up_stream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache (speculative decoding: the
+ * cache already holds the drafted tokens' own keys and values, one slot each, in the order of
+ * the call).
+ *
+ * The n_s = cu_seqlens[s+1] - cu_seqlens[s] drafted tokens of sequence s are its last n_s
+ * cached ones.  Each sees the slots before them, from kv_start on and the first
+ * `sinks`, and of the drafted ones itself, its parent, its parent's parent and so on.
+ *
+ *   q         dtype [total_tokens, Hq, d], packed by cu_seqlens, as in up_attend_paged.
+ *   parents   int32 [total_tokens]: the parent's number among the sequence's drafted tokens, less
+ *             than the token's own, or -1 for one that follows the cache.  A sequence with any
+ *             other parent, or of more than UP_TREE_MAX drafted tokens, sets
+ *             UP_DEVERR_BAD_TREE and its rows are those of an empty mask.
+ *   kv_start  int32 [total_tokens] or NULL: the first slot that each token sees of those
+ *             before the drafted ones (a window that moves with a token's depth).
+ *   sinks     as in up_attend_sinks.
+ *   workspace up_attend_tree_workspace(...) bytes, 256-byte aligned; its contents on entry
+ *             do not matter.
+ * Values, determinism and errors are as in up_attend_paged.
+ */
+#define UP_TREE_MAX 256
+
+size_t up_attend_tree_workspace(int64_t total_tokens, int num_seqs, int Hq, int Hk, int d);
+
+up_status up_attend_tree(const void *q, const int32_t *cu_seqlens, const int32_t *parents,
+                         int64_t total_tokens, int Hq, const up_paged_kv *cache,
+                         const up_logits *logits, const int32_t *kv_start, int sinks, void *out,
+                         float *lse, void *workspace, size_t workspace_bytes,
+                         up_stream_t stream);
 
 /*
  * Instrumentation: when both events are non-NULL, every later scoring call
