@@ -21,6 +21,8 @@ import os
 import torch
 
 from . import _build
+from .pages import (PagePool, compact_kv, compact_kv_workspace, copy_pages, fork_pages, release_pages,
+                    reserve_pages)
 from .paged import (PagedKV, append_kv, attend_paged, attend_paged_workspace, attend_tree,
                     attend_tree_workspace, decode_attend, decode_attend_workspace)
 
@@ -30,7 +32,9 @@ __all__ = ["build", "lib", "UpError", "score_blocks_workspace", "score_blocks",
            "compact_workspace", "compact", "compact_noalloc", "set_kernel_timing_events",
            "set_wait_limit", "get_device_error", "Sparsifier", "SELECT_MAX_BLOCKS", "PagedKV",
            "append_kv", "attend_paged", "attend_paged_workspace", "attend_tree",
-           "attend_tree_workspace", "decode_attend", "decode_attend_workspace"]
+           "attend_tree_workspace", "decode_attend", "decode_attend_workspace", "PagePool",
+           "reserve_pages", "release_pages", "fork_pages", "copy_pages", "compact_kv",
+           "compact_kv_workspace"]
 
 SELECT_MAX_BLOCKS = 16384
 _lib = None
@@ -112,6 +116,18 @@ def load_library(path):
     L.up_attend_tree_workspace.restype = SZ
     L.up_attend_tree.argtypes = [P, P, P, I64, I, P, P, P, I, P, P, P, SZ, P]
     L.up_attend_tree.restype = I
+    L.up_compact_kv_workspace.argtypes = [I64, I, I, I]
+    L.up_compact_kv_workspace.restype = SZ
+    L.up_compact_kv.argtypes = [P, P, I64, P, I64, P, I, P, P, SZ, P]
+    L.up_compact_kv.restype = I
+    L.up_reserve_pages.argtypes = [P, P, I, I, I, P, P, P]
+    L.up_reserve_pages.restype = I
+    L.up_release_pages.argtypes = [P, P, I, I, I, P, P, P]
+    L.up_release_pages.restype = I
+    L.up_fork_pages.argtypes = [P, P, P, I, I, I, P, I, P, P, P, P]
+    L.up_fork_pages.restype = I
+    L.up_copy_pages.argtypes = [P, P, I, P]
+    L.up_copy_pages.restype = I
     L.up_set_wait_limit.argtypes = [ctypes.c_uint64]
     L.up_set_wait_limit.restype = I
     return L

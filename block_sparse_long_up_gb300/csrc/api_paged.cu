@@ -4,7 +4,7 @@
 
 #include "../../include/up.h"
 #include "api_util.cuh"
-#include "paged.cuh"
+#include "pages.cuh"
 
 namespace {
 
@@ -58,6 +58,29 @@ up_status check_logits(const up_logits *l, const up_paged_kv *c) {
     if (l->slopes && (!l->q_pos || !c->pos_pages)) return UP_ERR_INVALID_ARG;
     return UP_OK;
 }
+
+// what a pool call takes, before its pointers to rows
+up_status check_table(const up_page_pool *p, int num_seqs, int max_pages, int page_size) {
+    if (!p || !p->refs || !p->free_pages || !p->num_free || p->num_pages < 1 || p->num_pages > INT32_MAX ||
+        !aligned(p->refs, 4) || !aligned(p->free_pages, 4) || !aligned(p->num_free, 4))
+        return UP_ERR_INVALID_ARG;
+    if (num_seqs < 0 || max_pages < 1 || page_size < 16 || page_size % 16 != 0 ||
+        (int64_t)num_seqs * max_pages > INT32_MAX)
+        return UP_ERR_INVALID_ARG;
+    return UP_OK;
+}
+
+up::PagePool pool_view(const up_page_pool *p, unsigned int *err) {
+    return up::PagePool{p->refs, p->free_pages, p->num_free, (int)p->num_pages, err};
+}
+
+bool overlap(const int32_t *a, int64_t na, const int32_t *b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + 4 * (uint64_t)nb && y < x + 4 * (uint64_t)na;
+}
+
+// the tiles of a compaction (64 rows and more each, of every head's keys and values) have 32-bit numbers
+bool few_tiles(int64_t T, int num_seqs, int Hk) { return (T / 64 + num_seqs) * 2 * Hk <= INT32_MAX; }
 
 up_status check_sinks(int sinks) {
     return sinks < 0 ? UP_ERR_INVALID_ARG : sinks > UP_SINKS_MAX ? UP_ERR_UNSUPPORTED : UP_OK;
@@ -267,6 +290,134 @@ up_status up_decode_sinks(const void *q, int Hq, const up_paged_kv *cache,
                           up_stream_t stream) {
     const up::CallRange range("up_decode_sinks");
     return decode(q, Hq, cache, logits, kv_start, sinks, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t up_compact_kv_workspace(int64_t max_tokens, int num_seqs, int Hk, int d) {
+    if (max_tokens < 0 || max_tokens > INT32_MAX || num_seqs < 0 || Hk < 1 ||
+        (d != 64 && d != 128 && d != 256) || !few_tiles(max_tokens, num_seqs, Hk))
+        return 0;
+    return up::kv_compact_workspace(max_tokens, num_seqs, Hk, d);
+}
+
+up_status up_compact_kv(const up_paged_kv *cache, const int32_t *cu_seqlens, int64_t max_tokens,
+                        const uint8_t *keep, int64_t num_flags, const int32_t *cu_blocks, int G,
+                        int32_t *kv_lens_out, void *workspace, size_t workspace_bytes,
+                        up_stream_t stream) {
+    const up::CallRange range("up_compact_kv");
+    up_status st = check_cache(cache, -1);
+    if (st != UP_OK) return st;
+    if (max_tokens < 0 || max_tokens > INT32_MAX || num_flags < 0 || G < 1 || (!cu_blocks && G > 1) ||
+        !few_tiles(max_tokens, cache->num_seqs, cache->Hk))
+        return UP_ERR_INVALID_ARG;
+    if (cache->num_seqs == 0) return UP_OK;
+    if (!cu_seqlens || !kv_lens_out || (max_tokens > 0 && !keep)) return UP_ERR_INVALID_ARG;
+    if (!aligned(cu_seqlens, 4) || !aligned(cu_blocks, 4) || !aligned(kv_lens_out, 4)) return UP_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < up::kv_compact_workspace(max_tokens, cache->num_seqs, cache->Hk, cache->d))
+        return UP_ERR_WORKSPACE;
+    up::DeviceInfo di{};
+    if ((st = up::device_info(&di)) != UP_OK) return st;
+    up::KvCompactArgs a{};
+    a.kv = device_view(cache, di.err);
+    a.cu_seqlens = cu_seqlens;
+    a.cu_blocks = cu_blocks ? cu_blocks : cu_seqlens;
+    a.keep = keep;
+    a.lens_out = kv_lens_out;
+    a.workspace = workspace;
+    a.num_flags = num_flags;
+    a.T = (int)max_tokens;
+    a.G = G;
+    a.wait_limit = di.wait_limit;
+    if (up::launch_kv_compact(a, di.sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return UP_ERR_CUDA;
+    return UP_OK;
+}
+
+up_status up_reserve_pages(const up_page_pool *pool, int32_t *block_table, int num_seqs,
+                           int max_pages, int page_size, const int32_t *have, const int32_t *want,
+                           up_stream_t stream) {
+    const up::CallRange range("up_reserve_pages");
+    up_status st = check_table(pool, num_seqs, max_pages, page_size);
+    if (st != UP_OK) return st;
+    if (num_seqs == 0) return UP_OK;
+    if (!block_table || !have || !want || !aligned(block_table, 4) || !aligned(have, 4) || !aligned(want, 4))
+        return UP_ERR_INVALID_ARG;
+    up::DeviceInfo di{};
+    if ((st = up::device_info(&di)) != UP_OK) return st;
+    const up::PageTable t{block_table, num_seqs, max_pages, page_size};
+    if (up::launch_reserve(pool_view(pool, di.err), t, have, want, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return UP_ERR_CUDA;
+    return UP_OK;
+}
+
+up_status up_release_pages(const up_page_pool *pool, int32_t *block_table, int num_seqs,
+                           int max_pages, int page_size, const int32_t *first, const int32_t *end,
+                           up_stream_t stream) {
+    const up::CallRange range("up_release_pages");
+    up_status st = check_table(pool, num_seqs, max_pages, page_size);
+    if (st != UP_OK) return st;
+    if (num_seqs == 0) return UP_OK;
+    if (!block_table || !end || !aligned(block_table, 4) || !aligned(first, 4) || !aligned(end, 4))
+        return UP_ERR_INVALID_ARG;
+    up::DeviceInfo di{};
+    if ((st = up::device_info(&di)) != UP_OK) return st;
+    const up::PageTable t{block_table, num_seqs, max_pages, page_size};
+    if (up::launch_release(pool_view(pool, di.err), t, first, end, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return UP_ERR_CUDA;
+    return UP_OK;
+}
+
+up_status up_fork_pages(const up_page_pool *pool, const int32_t *block_table,
+                        const int32_t *kv_lens, int num_seqs, int max_pages, int page_size,
+                        const int32_t *parents, int num_children, int32_t *table_out,
+                        int32_t *lens_out, int32_t *copies, up_stream_t stream) {
+    const up::CallRange range("up_fork_pages");
+    up_status st = check_table(pool, num_seqs, max_pages, page_size);
+    if (st != UP_OK) return st;
+    if (num_children < 0 || (int64_t)num_children * max_pages > INT32_MAX || (int64_t)num_children * 3 > INT32_MAX)
+        return UP_ERR_INVALID_ARG;
+    if (num_children == 0) return UP_OK;
+    if (num_seqs < 1 || !block_table || !kv_lens || !parents || !table_out || !lens_out || !copies)
+        return UP_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(parents, 4) || !aligned(table_out, 4) ||
+        !aligned(lens_out, 4) || !aligned(copies, 4))
+        return UP_ERR_INVALID_ARG;
+    // a child's row must not be written over a parent's, nor its length over a parent's or another's parent
+    const int64_t row = (int64_t)max_pages;
+    if (overlap(table_out, num_children * row, block_table, num_seqs * row) ||
+        overlap(lens_out, num_children, kv_lens, num_seqs) || overlap(lens_out, num_children, parents, num_children))
+        return UP_ERR_INVALID_ARG;
+    up::DeviceInfo di{};
+    if ((st = up::device_info(&di)) != UP_OK) return st;
+    up::ForkArgs a{};
+    a.pool = pool_view(pool, di.err);
+    a.from = up::PageTable{const_cast<int32_t *>(block_table), num_seqs, max_pages, page_size};
+    a.kv_lens = kv_lens;
+    a.parents = parents;
+    a.children = num_children;
+    a.table = table_out;
+    a.lens = lens_out;
+    a.copies = copies;
+    if (up::launch_fork(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return UP_ERR_CUDA;
+    return UP_OK;
+}
+
+up_status up_copy_pages(const up_paged_kv *cache, const int32_t *copies, int num_copies,
+                        up_stream_t stream) {
+    const up::CallRange range("up_copy_pages");
+    up_status st = check_cache(cache, -1);
+    if (st != UP_OK) return st;
+    if (num_copies < 0) return UP_ERR_INVALID_ARG;
+    if (num_copies == 0) return UP_OK;
+    if (!copies || !aligned(copies, 4) || !cache->k_pages || !cache->v_pages || cache->num_pages < 1)
+        return UP_ERR_INVALID_ARG;
+    if (up::copy_blocks(device_view(cache, nullptr), num_copies) > INT32_MAX) return UP_ERR_INVALID_ARG;
+    up::DeviceInfo di{};
+    if ((st = up::device_info(&di)) != UP_OK) return st;
+    const up::PagedKv kv = device_view(cache, di.err);
+    if (up::launch_copy_pages(kv, copies, num_copies, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return UP_ERR_CUDA;
+    return UP_OK;
 }
 
 }  // extern "C"

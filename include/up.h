@@ -69,7 +69,8 @@ typedef enum {
                                           max_pages * page_size (the sequence is left out) */
 
 #define UP_DEVERR_BAD_TREE 0x80u       /* drafted tokens: a parent that does not come before its child, or more
-                                          than UP_TREE_MAX tokens (the sequence's rows are those of an empty mask) */
+                                          than UP_TREE_MAX tokens (the sequence's rows are those of an empty
+                                          mask); a fork from a sequence that is none (the child is empty) */
 #define UP_DEVERR_NO_PAGES 0x100u      /* the pool has too few free pages for the call */
 #define UP_DEVERR_BAD_REFS 0x200u      /* a page released that nobody holds, or pool counts that cannot be */
 
@@ -531,6 +532,117 @@ up_status up_attend_tree(const void *q, const int32_t *cu_seqlens, const int32_t
                          const up_logits *logits, const int32_t *kv_start, int sinks, void *out,
                          float *lse, void *workspace, size_t workspace_bytes,
                          up_stream_t stream);
+
+/*
+ * Compaction of the paged cache in place: of the last n_s = cu_seqlens[s+1] - cu_seqlens[s]
+ * cached tokens of every sequence those that are kept move together, in order, right behind
+ * the tokens before them -- the accepted path of a drafted tree, or the blocks of a
+ * prompt that up_select_blocks kept.  Keys, values and positions move; the slots behind the
+ * kept tokens hold what they held or copies.
+ *
+ *   max_tokens  what cu_seqlens[num_seqs] is at most (above: UP_DEVERR_BAD_CU_SEQLENS); it sizes
+ *               the workspace.
+ *   keep        uint8 [num_flags]: token i of the n_s is kept iff keep[cu_blocks[s] + i / G].
+ *   cu_blocks   int32 [num_seqs+1]: where each sequence's ceil(n_s / G) flags begin (more are
+ *               allowed); NULL with G = 1: cu_seqlens.  A sequence whose flags do not fit there,
+ *               or reach past num_flags, sets UP_DEVERR_BAD_CU_BLOCKS.
+ *   G           tokens of a flag, positive.
+ *   kv_lens_out int32 [num_seqs]: the cached tokens that remain, kv_lens[s] - n_s + kept (kv_lens
+ *               itself is allowed).
+ *   workspace   up_compact_kv_workspace(...) bytes, 256-byte aligned; its contents on entry do
+ *               not matter.
+ * Pages that hold kept tokens of the n_s, or the slots that they move to, must not be shared between
+ * sequences (nor with one that up_fork_pages made).  A sequence with an error (UP_DEVERR_BAD_KV_LENS,
+ * UP_DEVERR_BAD_CU_BLOCKS) keeps its cache and length, and so do all under a malformed cu_seqlens
+ * (UP_DEVERR_BAD_CU_SEQLENS); a token whose old or new page is outside the pool does not
+ * move (UP_DEVERR_BAD_PAGE).  The move's waits are bounded like those of the attention
+ * kernels (UP_DEVERR_TIMEOUT: the cache's contents are then unspecified).
+ * Errors: as for the calls above; UP_ERR_INVALID_ARG for a cu_blocks of NULL with G > 1.
+ */
+size_t up_compact_kv_workspace(int64_t max_tokens, int num_seqs, int Hk, int d);
+
+up_status up_compact_kv(const up_paged_kv *cache, const int32_t *cu_seqlens, int64_t max_tokens,
+                        const uint8_t *keep, int64_t num_flags, const int32_t *cu_blocks, int G,
+                        int32_t *kv_lens_out, void *workspace, size_t workspace_bytes,
+                        up_stream_t stream);
+
+/*
+ * The pool of a cache's pages, on the device: sequences grow, fork and shrink without the
+ * host knowing a length.  One pool serves the caches of all layers that share a block table.
+ *   refs        int32 [num_pages]: how many block-table entries hold each page.
+ *   free_pages  int32 [num_pages]: a stack; its first num_free entries are the free pages.
+ *   num_free    int32 [1].
+ * A new pool has no holders, all pages on the stack and block tables of -1.  Calls on one pool
+ * (or one block table) are ordered by the caller: one stream, or events.  Tables and stack
+ * come out the same in every run.  A num_free outside [0, num_pages], or a stack entry that
+ * is no page, sets UP_DEVERR_BAD_REFS.
+ */
+typedef struct {
+    int32_t *refs;
+    int32_t *free_pages;
+    int32_t *num_free;
+    int64_t num_pages;
+} up_page_pool;
+
+/*
+ * Reserve: every entry of row s of block_table that belongs to the tokens have[s] <= t < want[s]
+ * -- the entries i with have[s] <= i * page_size < want[s] -- and is negative gets a free
+ * page, in the order of (s, i), from the top of the stack down.  Entries that hold a page
+ * keep it.  Where the stack ends (UP_DEVERR_NO_PAGES) the entries left stay as they are.  A want
+ * above max_pages * page_size sets UP_DEVERR_BAD_KV_LENS and leaves the sequence out.
+ *   block_table  int32 [num_seqs, max_pages] (num_seqs * max_pages below 2^31).
+ */
+up_status up_reserve_pages(const up_page_pool *pool, int32_t *block_table, int num_seqs,
+                           int max_pages, int page_size, const int32_t *have, const int32_t *want,
+                           up_stream_t stream);
+
+/*
+ * Release: the entries i of row s with first[s] <= i * page_size < end[s] let go of their pages
+ * and become -1 (negative ones are passed over); a page without a holder goes back on the
+ * stack.  Of the pages that go back, the one whose first entry comes first lies on top, so
+ * that reserving the same entries again gives the same pages.  first = NULL: 0.
+ *   - a sequence that ends: first NULL, end its length (or max_pages * page_size);
+ *   - one that is cut back: first the new length, end the old one;
+ *   - pages behind a window with first tokens that stay: first the sinks, end the window's first
+ *     slot less page_size - 1.
+ * An end above max_pages * page_size sets UP_DEVERR_BAD_KV_LENS and leaves the sequence out.  An
+ * entry outside the pool (UP_DEVERR_BAD_PAGE), or of a page that nobody holds (any more:
+ * UP_DEVERR_BAD_REFS), becomes -1 and nothing else happens to it.
+ */
+up_status up_release_pages(const up_page_pool *pool, int32_t *block_table, int num_seqs,
+                           int max_pages, int page_size, const int32_t *first, const int32_t *end,
+                           up_stream_t stream);
+
+/*
+ * Fork: child i (0 <= i < num_children) becomes a copy of sequence parents[i].  Its row of
+ * table_out shares the parent's full pages (one holder more each); a partial last
+ * page gets a free page of its own, whose rows up_copy_pages then copies in every layer's
+ * cache.  Entries of the parent that are negative (released ones behind a window) stay -1, as
+ * do those behind its kv_lens.
+ *   table_out  int32 [num_children, max_pages], not overlapping block_table.
+ *   lens_out   int32 [num_children]: the parent's length.
+ *   copies     int32 [3, num_children]: source page, new page, rows (-1, -1 where there is nothing
+ *              to copy).
+ * A child whose parent is not in [0, num_seqs) (UP_DEVERR_BAD_TREE), has a length that cannot be
+ * (UP_DEVERR_BAD_KV_LENS), or for which no free page is left (UP_DEVERR_NO_PAGES; earlier
+ * children come first) is empty: length 0, no page.
+ */
+up_status up_fork_pages(const up_page_pool *pool, const int32_t *block_table,
+                        const int32_t *kv_lens, int num_seqs, int max_pages, int page_size,
+                        const int32_t *parents, int num_children, int32_t *table_out,
+                        int32_t *lens_out, int32_t *copies, up_stream_t stream);
+
+/*
+ * Copies rows of pages, over all heads, in the keys, the values and (where the cache has them) the
+ * positions: the first copies[2n + i] slots of page copies[i] to page copies[n + i].  A
+ * negative page means nothing to copy.  No destination may be a source, or another copy's
+ * destination.  A page outside the pool, or rows outside [0, page_size], set
+ * UP_DEVERR_BAD_PAGE and copy nothing.  Of the cache the table and the lengths are not used.
+ * Errors: UP_ERR_INVALID_ARG for a cache that the calls above do not take, or for more copies
+ * than one launch has blocks (2 * Hk * ceil(page_size * d / 8192) * n below 2^31).
+ */
+up_status up_copy_pages(const up_paged_kv *cache, const int32_t *copies, int num_copies,
+                        up_stream_t stream);
 
 /*
  * Instrumentation: when both events are non-NULL, every later scoring call
