@@ -26,7 +26,7 @@ __device__ __forceinline__ void set_of(Unit &u, int first, int wend, int send, b
 template <bool kTree>
 __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Params p, uint32_t *bits, int tpu) {
     __shared__ int64_t sh[32];
-    __shared__ int bad;
+    __shared__ int bad, s_off[kPlanThreads];
     const AttendArgs &a = p.a;
     const int B = a.kv.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) bad = 0;
@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
         const int64_t at = units + block_scan(n, &total, sh);
         if (s < B) {
             p.seq_off[s] = (int)(at < p.max_units ? at : p.max_units);
-            p.seen[s] = make_int4(0, 0, 0, 0);
+            if (s0 == 0) s_off[s] = p.seq_off[s];
+            if (kTree) p.seen[s].z = 0;
         }
         units += total;
     }
@@ -93,12 +94,12 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
         }
         __syncthreads();
     }
-    // a warp a unit, its tokens on the lanes
-    for (int64_t i = warp; i < units; i += kPlanThreads / 32) {
+    // the unit numbered i, without its tiles (a tree's without windows: with them)
+    auto unit_at = [&](int64_t i) {
         int lo = 0, hi = B - 1;  // the last sequence with seq_off <= i
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (p.seq_off[mid] <= i) lo = mid; else hi = mid - 1;
+            if ((mid < kPlanThreads ? s_off[mid] : p.seq_off[mid]) <= i) lo = mid; else hi = mid - 1;
         }
         const int c0 = a.cu_seqlens[lo], c1 = a.cu_seqlens[lo + 1];
         Unit u{};
@@ -106,35 +107,77 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
         u.tok0 = c0 + (int)(i - p.seq_off[lo]) * tpu;
         u.ntok = min(tpu, c1 - u.tok0);
         u.kv = kv_len_of(a.kv, lo, c1 - c0);
-        if (u.kv >= 0 && !p.seen[lo].z) {
-            int first = INT32_MAX, end = 0, some = 0;
-            bool gaps = false;
-            if constexpr (kTree) {
-                const int past = u.kv - (c1 - c0);
-                if (a.kv_start) {
-                    for (int t = lane; t < u.ntok; t += 32) first = min(first, max(a.kv_start[u.tok0 + t], 0));
-                    first = min(__reduce_min_sync(0xffffffffu, first), past);
-                } else {
-                    first = 0;
+        if (kTree && p.seen[lo].z) u.kv = -1;
+        if (kTree && u.kv >= 0) {
+            u.hi0 = u.kv - (c1 - c0);
+            set_of(u, 0, u.kv, min(a.sinks, u.hi0), false);
+        }
+        return u;
+    };
+    if (kTree && !a.kv_start) {
+        for (int64_t i = tid; i < units; i += kPlanThreads) p.units[i] = unit_at(i);
+    } else {
+        // A warp takes four units at once, a lane each to begin with, then its lanes at their tokens (one at a
+        // time 250 units took 14 us; XX so).
+        constexpr int kSame = 4;
+        for (int64_t i0 = warp * kSame; i0 < units; i0 += kPlanThreads / 32 * kSame) {
+            Unit u = unit_at(min(i0 + (lane & (kSame - 1)), units - 1));
+            int tok0[kSame], ntok[kSame], kv[kSame], first[kSame], end[kSame], some[kSame];
+            bool gaps[kSame];
+#pragma unroll
+            for (int k = 0; k < kSame; ++k) {
+                tok0[k] = __shfl_sync(0xffffffffu, u.tok0, k);
+                ntok[k] = __shfl_sync(0xffffffffu, u.ntok, k);
+                kv[k] = __shfl_sync(0xffffffffu, u.kv, k);
+                if (kv[k] < 0) ntok[k] = 0;
+                first[k] = INT32_MAX;
+                end[k] = some[k] = 0;
+                gaps[k] = false;
+            }
+            for (int t = lane; t < tpu; t += 32) {
+                int2 v[kSame], b[kSame];
+#pragma unroll
+                for (int k = 0; k < kSame; ++k) {
+                    const int at = tok0[k] + min(t, max(ntok[k] - 1, 0));
+                    if constexpr (kTree) {
+                        v[k].x = a.kv_start[at];
+                    } else {
+                        const int2 *vis = reinterpret_cast<const int2 *>(a.visible) + at;
+                        v[k] = *vis;
+                        b[k] = vis[t && t < ntok[k] ? -1 : 0];
+                    }
                 }
-                u.hi0 = past;
-                set_of(u, first, u.kv, min(a.sinks, past), false);
-            } else {
-                for (int t = lane; t < u.ntok; t += 32) {
-                    const int2 *v = reinterpret_cast<const int2 *>(a.visible) + u.tok0 + t;
-                    const int2 r = cut_range(*v, u.kv), before = t ? cut_range(v[-1], u.kv) : r;
-                    first = min(first, r.x);
-                    end = max(end, r.y);
-                    some = max(some, min(v->y, u.kv));
-                    gaps |= r.y > 0 && max(before.x, r.x) > min(before.y, r.y);
+#pragma unroll
+                for (int k = 0; k < kSame; ++k) {
+                    if (t >= ntok[k]) continue;
+                    if constexpr (kTree) {
+                        first[k] = min(first[k], max(v[k].x, 0));
+                    } else {
+                        const int2 r = cut_range(v[k], kv[k]), before = cut_range(b[k], kv[k]);
+                        first[k] = min(first[k], r.x);
+                        end[k] = max(end[k], r.y);
+                        some[k] = max(some[k], min(v[k].y, kv[k]));
+                        gaps[k] |= r.y > 0 && max(before.x, r.x) > min(before.y, r.y);
+                    }
                 }
-                first = __reduce_min_sync(0xffffffffu, first);
-                end = __reduce_max_sync(0xffffffffu, end);
-                u.hi0 = min(a.sinks, max(__reduce_max_sync(0xffffffffu, some), 0));
-                set_of(u, end > 0 ? first : 0, end, u.hi0, __any_sync(0xffffffffu, gaps));
+            }
+#pragma unroll
+            for (int k = 0; k < kSame; ++k) {
+                const int lo = __reduce_min_sync(0xffffffffu, first[k]);
+                const int hi = __reduce_max_sync(0xffffffffu, end[k]), most = __reduce_max_sync(0xffffffffu, some[k]);
+                const bool torn = __any_sync(0xffffffffu, gaps[k]);
+                if (lane != k || i0 + k >= units) continue;
+                if (u.kv >= 0) {
+                    if constexpr (kTree) {
+                        set_of(u, min(lo, u.hi0), u.kv, min(a.sinks, u.hi0), false);
+                    } else {
+                        u.hi0 = min(a.sinks, most);
+                        set_of(u, hi > 0 ? lo : 0, hi, u.hi0, torn);
+                    }
+                }
+                p.units[i0 + k] = u;
             }
         }
-        if (lane == 0) p.units[i] = u;
     }
     __syncthreads();
     int64_t W = 0;
@@ -168,8 +211,7 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmem, st, qm, km, vm, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attend_join_kernel<kFp16, D>, dim3((unsigned)p.grid, C::kUnitRows / kJoinRows),
-                      dim3(kJoinThreads), 0, st, p);
+    return launch_pdl(attend_join_kernel<kFp16, D>, dim3((unsigned)p.grid * kJoinPerSm), dim3(kJoinThreads), 0, st, p);
 }
 
 }  // namespace

@@ -1270,51 +1270,33 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 // ---------------------------------------------------------------- the join
 
 constexpr int kJoinThreads = 256, kJoinRows = 32;
+constexpr int kJoinPerSm = 4;
 
-// Block (c, y): the unit that the end of share c cuts, if c is the first to cut it,
-// rows [32y, 32y + 32): a lane takes a row, a warp every eighth four of its columns, the
-// parts in the order of their slots.  All
-// blocks together also write the rows of the units without a visible slot, or of all tokens
-// when the batch is malformed.
-template <bool kFp16, int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params p) {
+// Rows [rows0, rows0 + 32) of a cut unit and kC fours of columns a warp from col0 on: a lane takes a row, a
+// warp every eighth four, the parts in the order of their slots.
+template <bool kFp16, int D, int kC>
+__device__ __forceinline__ void join_piece(const Params &p, const Plan &pl, const Shares &sh, int c0, int rows0, int col0) {
     using C = Cfg<D>;
+    constexpr int kCols = 32 * kC;
+    __shared__ __align__(16) uint32_t s_out[kJoinRows][kCols / 2 + 4];
+    __shared__ int s_row[kJoinRows];
     const AttendArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait();
-    const Plan pl = *p.plan;
-    const int nb = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
-    for (int i = me; i < (pl.bad ? a.T : pl.units); i += nb) {
-        int64_t r0 = (int64_t)i * a.Hq, nr = a.Hq;
-        if (!pl.bad) {
-            const Unit u = p.units[i];
-            if (u.tiles) continue;
-            r0 = (int64_t)u.tok0 * a.Hq, nr = (int64_t)u.ntok * a.Hq;
-        }
-        for (int64_t k = tid; k < nr * D / 8; k += kJoinThreads)
-            reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + r0 * D)[k] = make_uint4(0, 0, 0, 0);
-        if (a.lse)
-            for (int64_t k = tid; k < nr; k += kJoinThreads) a.lse[r0 + k] = -INFINITY;
-    }
-    if (pl.W == 0) return;
-    const Shares sh = shares_of(pl.W * a.kv.Hk, p.grid, kMinTiles);
-    const int c0 = blockIdx.x;
-    if (c0 + 1 >= sh.n) return;
     const Cut cut = p.cuts[c0];
-    if (!cut.parted) return;
     const Unit u = p.units[cut.unit];
     const int j = cut.j;
+    const int r = rows0 + lane, e = r / kRows, rr = r % kRows;
+    const int tl = rr / a.g, tok = e * p.tpt + tl;
+    const bool valid = tl < p.tpt && tok < u.ntok;
+    if (!__any_sync(0xffffffffu, valid)) return;  // all warps do
     const int64_t ub = (int64_t)j * pl.W + u.prefix, ue = ub + width_of(u);
     const int n = share_of(sh, ue - 1) - c0 + 1;
     // a block's first piece is in its slot 0, a later one (this unit's first) in slot 1
     const int slot0 = 2 * c0 + (share_begin(sh, c0) < ub);
     auto part = [&](int i) { return p.parts + (int64_t)(i == 0 ? slot0 : 2 * (c0 + i)) * C::kUnitRows * (D + 4); };
-    constexpr int kC = D / 32;  // fours of columns of a warp
-    __shared__ __align__(16) uint32_t s_out[kJoinRows][D / 2 + 4];
-    __shared__ int s_row[kJoinRows];
-    const int r = blockIdx.y * kJoinRows + lane, e = r / kRows, rr = r % kRows;
-    const int tl = rr / a.g, tok = e * p.tpt + tl;
-    const bool valid = tl < p.tpt && tok < u.ntok;
+    auto four = [&](const float *src, int k) {
+        return (reinterpret_cast<const float4 *>(src + 4 * C::kUnitRows) + r)[(col0 / 4 + warp + 8 * k) * C::kUnitRows];
+    };
     float M = -INFINITY, L = 0.f;
     float4 O[kC];
 #pragma unroll
@@ -1328,10 +1310,9 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params 
             const float *src = part(i);
             const float w = exp2f(src[r] - ref);
             L = fmaf(w, src[C::kUnitRows + r], L);
-            const float4 *o = reinterpret_cast<const float4 *>(src + 4 * C::kUnitRows) + r;
 #pragma unroll
             for (int k = 0; k < kC; ++k) {
-                const float4 v = o[(warp + 8 * k) * C::kUnitRows];
+                const float4 v = four(src, k);
                 O[k].x = fmaf(w, v.x, O[k].x); O[k].y = fmaf(w, v.y, O[k].y);
                 O[k].z = fmaf(w, v.z, O[k].z); O[k].w = fmaf(w, v.w, O[k].w);
             }
@@ -1347,14 +1328,67 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params 
     if (warp == 0) {
         const int orow = (u.tok0 + tok) * a.Hq + j * a.g + rr - tl * a.g;
         s_row[lane] = valid ? orow : -1;
-        if (valid && a.lse) a.lse[orow] = ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
+        if (valid && a.lse && col0 == 0) a.lse[orow] = ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2;
     }
     __syncthreads();
-    for (int i = tid; i < kJoinRows * D / 8; i += kJoinThreads) {
-        const int k = i / (D / 8), c = i - k * (D / 8);
+    for (int i = tid; i < kJoinRows * kCols / 8; i += kJoinThreads) {
+        const int k = i / (kCols / 8), c = i % (kCols / 8);
         if (s_row[k] >= 0)
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (int64_t)s_row[k] * D + 8 * c) =
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (int64_t)s_row[k] * D + col0 + 8 * c) =
                 *reinterpret_cast<const uint4 *>(&s_out[k][4 * c]);
+    }
+    __syncthreads();
+}
+
+// Joins the units that a share's end cuts, named by the first share that does, 32 rows at a time, and where
+// there are blocks enough 32 of their columns at a time too.  (A block for each 32 rows of each
+// share, most of them without any, took 8.8 us of a call of 128 tokens over 1K and 19 of 64 drafted ones
+// over 128K, whose 8 units are in 19 parts each; XX and XX so.)  All blocks together also write the rows of the
+// units without a visible slot, or of all tokens when the batch is malformed.
+template <bool kFp16, int D>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params p) {
+    using C = Cfg<D>;
+    constexpr int kRowGroups = C::kUnitRows / kJoinRows;
+    __shared__ int s_cut[kMaxSms], s_count[kMaxSms / 32];
+    const AttendArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    const Plan pl = *p.plan;
+    for (int i = blockIdx.x; i < (pl.bad ? a.T : pl.units); i += gridDim.x) {
+        int64_t r0 = (int64_t)i * a.Hq, nr = a.Hq;
+        if (!pl.bad) {
+            const Unit u = p.units[i];
+            if (u.tiles) continue;
+            r0 = (int64_t)u.tok0 * a.Hq, nr = (int64_t)u.ntok * a.Hq;
+        }
+        for (int64_t k = tid; k < nr * D / 8; k += kJoinThreads)
+            reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + r0 * D)[k] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int64_t k = tid; k < nr; k += kJoinThreads) a.lse[r0 + k] = -INFINITY;
+    }
+    if (pl.W == 0) return;
+    const Shares sh = shares_of(pl.W * a.kv.Hk, p.grid, kMinTiles);
+    // the shares whose ends are the first to cut a unit
+    uint32_t m = 0;
+    if (tid < kMaxSms) {
+        m = __ballot_sync(0xffffffffu, tid + 1 < sh.n && p.cuts[tid].parted);
+        if (lane == 0) s_count[warp] = __popc(m);
+    }
+    __syncthreads();
+    int cuts = 0, before = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxSms / 32; ++k) {
+        if (k == warp) before = cuts;
+        cuts += s_count[k];
+    }
+    if (m >> lane & 1u) s_cut[before + __popc(m & ((1u << lane) - 1u))] = tid;
+    __syncthreads();
+    const bool split = cuts * kRowGroups * (D / 32) <= (int)gridDim.x;
+    const int pieces = kRowGroups * (split ? D / 32 : 1);
+    for (int x = blockIdx.x; x < cuts * pieces; x += gridDim.x) {
+        const int c0 = s_cut[x / pieces], y = x % pieces, rows0 = y % kRowGroups * kJoinRows;
+        if (split) join_piece<kFp16, D, 1>(p, pl, sh, c0, rows0, y / kRowGroups * 32);
+        else join_piece<kFp16, D, D / 32>(p, pl, sh, c0, rows0, 0);
     }
 }
 

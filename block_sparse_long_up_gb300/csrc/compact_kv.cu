@@ -30,15 +30,16 @@ constexpr int kTileBytes = kMoveThreads * kInFlight * 16;
 __host__ __device__ constexpr int tile_rows(int d) { return kTileBytes / (2 * d); }
 
 struct Head {
-    int ticket;   // tiles handed out
+    int ticket;   // tickets handed out
     int abort;
-    int tiles;    // of the call
+    int tickets;  // of the call
     int pad;
 };
-// One sequence: the slot of its first flagged token, the list's place of its first kept one, its kept
-// tokens, those before the first dropped one (they stay), its first tile.
-struct Moved {
-    int base, at, kept, stay, tile0, pad[3];
+// One sequence: the slot of its first flagged token (-1: left out), the list's place of its first
+// kept one, its kept tokens, those before the first dropped one (they stay), its first ticket and
+// the tickets of a tile.
+struct alignas(32) Moved {
+    int base, at, kept, stay, ticket0, groups, pad[2];
 };
 
 struct Layout {
@@ -60,6 +61,7 @@ Layout layout_of(int64_t T, int num_seqs, int Hk, int d) {
 
 struct Params {
     KvCompactArgs a;
+    int r_log2, g_log2;  // of R, and of G (-1: G is no power of two)
     Head *head;
     Moved *seqs;
     int32_t *list;   // the kept tokens' numbers among their sequence's flagged ones
@@ -71,7 +73,54 @@ struct Params {
 // where the edges of sequence s begin: every sequence before it may have a partial one
 __device__ __forceinline__ int64_t edges_of(const Params &p, int s) { return p.a.cu_seqlens[s] / p.R + (int64_t)s; }
 
-__global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads) kv_plan_kernel(const Params p) {
+// The slot before sequence s's flagged tokens, where its flags begin, and whether they can be.
+struct Region {
+    int base, flags, end;  // base: -1 for a sequence that is left out; end: of its tokens
+};
+__device__ __forceinline__ Region region_of(const KvCompactArgs &a, int s, bool tell) {
+    const int c0 = a.cu_seqlens[s], c1 = a.cu_seqlens[s + 1], n = c1 - c0, nb = (n + a.G - 1) / a.G;
+    const int b0 = a.cu_blocks[s], b1 = a.cu_blocks[s + 1], kv = a.kv.kv_lens[s];
+    Region r{kv - n, b0, c1};
+    if (tell) kv_len_of(a.kv, s, n);  // (its error bit)
+    if (kv < n || kv > INT32_MAX - 65536 || kv > (int64_t)a.kv.max_pages * a.kv.page_size) {
+        r.base = -1;
+    } else if (b0 < 0 || b1 < b0 || b1 - b0 < nb || b1 > a.num_flags) {
+        if (tell) atomicOr(a.kv.err, 0x10u);  // UP_DEVERR_BAD_CU_BLOCKS
+        r.base = -1;
+    }
+    return r;
+}
+
+// Tickets of a sequence that moves m rows: tiles of R rows of one chain each; where all rows
+// are fewer, as many chains (a power of two) as fill a tile share a ticket.
+__host__ __device__ __forceinline__ int chains_of(int m, int R) {
+    int c = 1;
+    while (c < 64 && 2 * c * m <= R) c *= 2;
+    return c;
+}
+
+// The last of the numbers 0 .. n - 1 for which f holds, which it does up to it (for 0 at least); by a
+// warp, 32 at a time.
+template <typename F>
+__device__ __forceinline__ int last_of(int n, F &&f) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const unsigned m = __ballot_sync(0xffffffffu, lane * step < n && f(lo + lane * step));
+        const int hit = 31 - __clz(m | 1u);
+        lo += hit * step;
+        n = min(step, n - hit * step);
+    }
+    return lo;
+}
+
+// The scan: 8 blocks, 256 warps, equal runs of the flagged tokens.  A lane looks at up to
+// kAhead tokens at once -- the loads of a step hang on one another, so latency is what it costs (131072
+// tokens: 35 us one at a time).
+constexpr int kAhead = 16;
+
+__global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) kv_plan_kernel(const Params p) {
     __shared__ int s_bad;
     const KvCompactArgs &a = p.a;
     const int B = a.kv.num_seqs, tid = threadIdx.x, lane = tid & 31;
@@ -91,108 +140,117 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads) kv_plan_ke
         for (int s = me; s < B; s += kBlocks * kThreads) a.lens_out[s] = a.kv.kv_lens[s];
         return;  // all blocks do
     }
-    // base: -1 for a sequence that is left out
+    const int T = a.cu_seqlens[B];
     for (int s = me; s < B; s += kBlocks * kThreads) {
-        const int n = a.cu_seqlens[s + 1] - a.cu_seqlens[s], nb = (n + a.G - 1) / a.G;
-        const int kv = kv_len_of(a.kv, s, n);
-        const int b0 = a.cu_blocks[s], b1 = a.cu_blocks[s + 1];
-        int base = kv - n;
-        if (kv < 0) {
-            base = -1;
-        } else if (b0 < 0 || b1 < b0 || b1 - b0 < nb || b1 > a.num_flags) {
-            atomicOr(a.kv.err, 0x10u);  // UP_DEVERR_BAD_CU_BLOCKS
-            base = -1;
-        }
-        p.seqs[s] = Moved{base, 0, 0, n, 0, {0, 0, 0}};
+        const Region r = region_of(a, s, true);
+        p.seqs[s] = Moved{r.base, 0, 0, r.end - a.cu_seqlens[s], 0, 0, {0, 0}};
     }
-    meet();
-    // the tokens in equal runs over the warps
+    const int64_t flags = ((int64_t)T / p.R + B) * 2 * a.kv.Hk;
+    for (int64_t i = me; i < flags; i += kBlocks * kThreads) p.flags[i] = 0;
+    // this warp's run of tokens, in groups of kAhead * 32
     const int w = cluster_warp();
-    const int64_t T = a.cu_seqlens[B];
-    const int from = (int)(T * w / kAllWarps), to = (int)(T * (w + 1) / kAllWarps);
-    int s_first = 0;  // the sequence of token `from`
-    {
-        int lo = 0, hi = B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.cu_seqlens[mid] <= from) lo = mid; else hi = mid - 1;
-        }
-        s_first = lo;
-    }
+    const int from = (int)((int64_t)T * w / kAllWarps), to = (int)((int64_t)T * (w + 1) / kAllWarps);
+    const int s_first = last_of(B, [&](int s) { return a.cu_seqlens[s] <= from; });  // of token `from`
+    // f(token, sequence, its first token and end, whether it is kept, the ballot of that) for the run's tokens
     auto each = [&](auto &&f) {
+        auto block_of = [&](int i) { return p.g_log2 >= 0 ? i >> p.g_log2 : i / a.G; };
         int s = s_first;
-        for (int t0 = from; t0 < to; t0 += 32) {
-            const int t = t0 + lane;
-            bool kept = false, there = t < to;
-            int i = 0;
-            if (there) {
-                while (a.cu_seqlens[s + 1] <= t) ++s;
-                i = t - a.cu_seqlens[s];
-                kept = __ldcg(&p.seqs[s].base) >= 0 && a.keep[a.cu_blocks[s] + i / a.G];
+        Region r = from < to ? region_of(a, s, false) : Region{-1, 0, 0};
+        for (int g0 = from; g0 < to; g0 += 32 * kAhead) {
+            if (g0 + 32 * kAhead <= r.end || (to <= r.end)) {
+                // one sequence's: the loads do not wait for one another
+                const int c0 = a.cu_seqlens[s];
+                uint32_t kept = 0;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int t = g0 + 32 * k + lane;
+                    if (t < to && r.base >= 0 && a.keep[r.flags + block_of(t - c0)]) kept |= 1u << k;
+                }
+#pragma unroll 1
+                for (int k = 0; k < kAhead && g0 + 32 * k < to; ++k)
+                    f(g0 + 32 * k + lane, s, c0, r.end, kept >> k & 1u, __ballot_sync(0xffffffffu, kept >> k & 1u));
+                continue;
             }
-            f(t, s, i, there, kept, __ballot_sync(0xffffffffu, kept));
+#pragma unroll 1
+            for (int t0 = g0; t0 < min(to, g0 + 32 * kAhead); t0 += 32) {
+                const int t = t0 + lane;
+                bool kept = false;
+                if (t < to) {
+                    if (t >= r.end) {
+                        while (a.cu_seqlens[s + 1] <= t) ++s;
+                        r = region_of(a, s, false);
+                    }
+                    kept = r.base >= 0 && a.keep[r.flags + block_of(t - a.cu_seqlens[s])];
+                }
+                f(t, s, a.cu_seqlens[s], r.end, kept, __ballot_sync(0xffffffffu, kept));
+            }
+            // the lanes go on from the last one's sequence
+            s = __reduce_max_sync(0xffffffffu, s);
+            r = region_of(a, s, false);
         }
     };
     int mine = 0;
-    each([&](int, int, int, bool, bool, unsigned m) { mine += __popc(m); });
+    each([&](int, int, int, int, bool, unsigned m) { mine += __popc(m); });
     int total, rank = before_warp(mine, &total);
-    int last_s = -1;
-    each([&](int t, int s, int i, bool there, bool kept, unsigned m) {
-        const int r = rank + __popc(m & ((1u << lane) - 1u));
-        if (there) {
+    int told = -1;  // the sequence whose first dropped token this warp has told of
+    each([&](int t, int s, int c0, int end, bool kept, unsigned m) {
+        // sequences rise over the lanes: of each, the first dropped token (a lane each, and 8192 of them
+        // on one address, took 15 us of 131072 tokens' 27)
+        const unsigned gone = __ballot_sync(0xffffffffu, t < to && !kept), below = gone & ((1u << lane) - 1u);
+        const int before = __shfl_sync(0xffffffffu, s, below ? 31 - __clz(below) : 0);
+        if (t < to && !kept && s != (below ? before : told)) atomicMin(&p.seqs[s].stay, t - c0);
+        if (gone) told = __shfl_sync(0xffffffffu, s, 31 - __clz(gone));
+        if (t < to) {
+            const int r = rank + __popc(m & ((1u << lane) - 1u)), i = t - c0;
             if (i == 0) p.seqs[s].at = r;
-            if (t + 1 == a.cu_seqlens[s + 1]) p.seqs[s].kept = r + kept;  // `at` comes off below
-            if (i % p.R == 0) p.edges[edges_of(p, s) + i / p.R] = r;  // of all; the sequence's share comes off later
+            if (t + 1 == end) p.seqs[s].kept = r + kept;  // `at` comes off below
+            if ((i & (p.R - 1)) == 0) p.edges[(c0 >> p.r_log2) + s + (i >> p.r_log2)] = r;  // (see edges_of) of all; the sequence's share comes off later
             if (kept) p.list[r] = i;
-            else if (s != last_s) atomicMin(&p.seqs[s].stay, i);  // (later ones of the run are larger)
-            if (!kept) last_s = s;
         }
         rank += __popc(m);
     });
+    await_all();
     meet();
-    // kept tokens of every sequence, and the tiles' numbers (block 0; many sequences in rounds)
-    if (blockIdx.x == 0) {
-        __shared__ int s_sum[kWarps];
-        int tiles = 0;
-        for (int s0 = 0; s0 < B; s0 += kThreads) {
-            const int s = s0 + tid;
-            int n = 0, kept = 0;
-            Moved q{};
-            if (s < B) {
-                q = Moved{__ldcg(&p.seqs[s].base), __ldcg(&p.seqs[s].at), 0, __ldcg(&p.seqs[s].stay), 0, {0, 0, 0}};
-                kept = q.base >= 0 ? __ldcg(&p.seqs[s].kept) - q.at : 0;
-                a.lens_out[s] = q.base < 0 ? a.kv.kv_lens[s] : q.base + kept;
-                n = (max(kept - q.stay, 0) + p.R - 1) / p.R;
-            }
-            int inc = n;
-#pragma unroll
-            for (int k = 1; k < 32; k <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, k);
-                if (lane >= k) inc += y;
-            }
-            if (lane == 31) s_sum[tid >> 5] = inc;
-            __syncthreads();
-            int sum = s_sum[lane];
-#pragma unroll
-            for (int k = 1; k < 32; k <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, sum, k);
-                if (lane >= k) sum += y;
-            }
-            const int before = (tid >> 5) ? __shfl_sync(0xffffffffu, sum, (tid >> 5) - 1) : 0;
-            const int all = __shfl_sync(0xffffffffu, sum, 31);
-            if (s < B) {
-                q.kept = kept;
-                q.tile0 = tiles + before + inc - n;
-                p.seqs[s] = q;
-            }
-            tiles += all;
-            __syncthreads();
+    if (blockIdx.x) return;
+    // kept tokens of every sequence, and the tickets' numbers (many sequences in rounds)
+    __shared__ int s_sum[kWarps];
+    int tickets = 0;
+    for (int s0 = 0; s0 < B; s0 += kThreads) {
+        const int s = s0 + tid;
+        int n = 0;
+        Moved q{};
+        if (s < B) {
+            q = Moved{__ldcg(&p.seqs[s].base), __ldcg(&p.seqs[s].at), 0, __ldcg(&p.seqs[s].stay), 0, 0, {0, 0}};
+            q.kept = q.base >= 0 ? __ldcg(&p.seqs[s].kept) - q.at : 0;
+            a.lens_out[s] = q.base < 0 ? a.kv.kv_lens[s] : q.base + q.kept;
+            const int m = max(q.kept - q.stay, 0);
+            q.groups = (2 * a.kv.Hk - 1) / chains_of(max(m, 1), p.R) + 1;
+            n = (m + p.R - 1) / p.R * q.groups;
         }
-        if (tid == 0) p.head->tiles = tiles;
+        int inc = n;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, k);
+            if (lane >= k) inc += y;
+        }
+        if (lane == 31) s_sum[tid >> 5] = inc;
+        __syncthreads();
+        int sum = s_sum[lane];
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, k);
+            if (lane >= k) sum += y;
+        }
+        const int before = (tid >> 5) ? __shfl_sync(0xffffffffu, sum, (tid >> 5) - 1) : 0;
+        const int all = __shfl_sync(0xffffffffu, sum, 31);
+        if (s < B) {
+            q.ticket0 = tickets + before + inc - n;
+            p.seqs[s] = q;
+        }
+        tickets += all;
+        __syncthreads();
     }
-    meet();
-    const int64_t flags = (int64_t)__ldcg(&p.head->tiles) * 2 * a.kv.Hk;
-    for (int64_t i = me; i < flags; i += kBlocks * kThreads) p.flags[i] = 0;
+    if (tid == 0) p.head->tickets = tickets;
 }
 
 __device__ __forceinline__ int load_acquire(const int *at) {
@@ -204,87 +262,156 @@ __device__ __forceinline__ void store_release(int *at, int v) {
     asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(at), "r"(v) : "memory");
 }
 
-__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const Params p) {
-    __shared__ int64_t s_src[tile_rows(64)], s_dst[tile_rows(64)];
-    __shared__ int s_ticket, s_stop;
+// What a ticket stands for: rows [r0, r0 + rows) of a sequence, of the chains (keys and values of the
+// heads in turn) [chain, chain + chains), and the tickets [w0, w1) by `step` whose rows must have been read.
+struct Ticket {
+    int number, rows, chain, chains, base, r0, places, w0, w1, step;
+};
+
+// By one warp; number = -1 where there is none.
+__device__ Ticket describe(const Params &p, int number, int all, int *list_at, int *seq) {
     const KvCompactArgs &a = p.a;
-    const int tid = threadIdx.x, Hk = a.kv.Hk, ps = a.kv.page_size;
-    const int pieces = a.kv.d / 8;  // of a row
+    Ticket k{};
+    k.number = number < all ? number : -1;
+    if (k.number < 0) return k;
+    const int lo = last_of(a.kv.num_seqs, [&](int s) { return __ldg(&p.seqs[s].ticket0) <= number; });
+    Moved q;
+    reinterpret_cast<int4 *>(&q)[0] = __ldg(reinterpret_cast<const int4 *>(p.seqs + lo));
+    reinterpret_cast<int4 *>(&q)[1] = __ldg(reinterpret_cast<const int4 *>(p.seqs + lo) + 1);
+    const int per = q.groups, i = (number - q.ticket0) / per, group = (number - q.ticket0) % per;
+    const int moved = q.kept - q.stay;
+    k.chains = chains_of(moved, p.R);
+    k.chain = group * k.chains;
+    k.chains = min(k.chains, 2 * a.kv.Hk - k.chain);
+    k.base = q.base;
+    k.r0 = q.stay + i * p.R;
+    k.rows = min(p.R, q.kept - k.r0);
+    k.places = a.kv.pos && group == 0;
+    // The tiles that read what this one is about to write over: those of the kept tokens in slots
+    // [r0, r0 + rows), by the ranks at the edges around them.
+    const int64_t e = edges_of(p, lo);
+    const int len = a.cu_seqlens[lo + 1] - a.cu_seqlens[lo], next = (k.r0 + k.rows - 1) / p.R + 1;
+    const int ea = __ldg(p.edges + e + k.r0 / p.R) - q.at;
+    const int eb = next < (len + p.R - 1) / p.R ? __ldg(p.edges + e + next) - q.at : q.kept;
+    const int t0 = max(ea - q.stay, 0) / p.R, t1 = min((max(eb - q.stay, 0) + p.R - 1) / p.R, i);
+    k.w0 = q.ticket0 + t0 * per + group;
+    k.w1 = q.ticket0 + t1 * per + group;
+    k.step = per;
+    *list_at = q.at + k.r0;
+    *seq = lo;
+    return k;
+}
+
+// A block reads a tile's rows into registers, and while they come one warp describes the ticket after
+// next and all look up the next one's rows (each a chain of loads as long as the rows' own: 131072
+// tokens of which a quarter stay take XX us so, 62 with one ticket looked up whole).  It tells that
+// its rows are there, waits for whoever still has to read the slots that they go to, and writes them.
+__global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const Params p) {
+    constexpr int kMaxRows = tile_rows(64);
+    static_assert(kMaxRows <= kMoveThreads, "a thread a row");
+    __shared__ int64_t s_src[3][kMaxRows], s_dst[3][kMaxRows];
+    __shared__ Ticket s_ticket[3];
+    __shared__ int s_list[3], s_seq[3], s_stop;
+    const KvCompactArgs &a = p.a;
+    const int tid = threadIdx.x, Hk = a.kv.Hk, ps = a.kv.page_size, d2 = a.kv.d * 2;
+    const int shift = a.kv.d == 64 ? 3 : a.kv.d == 128 ? 4 : 5;  // 16-byte pieces of a row, log2
     pdl_wait();
-    const int64_t all = (int64_t)p.head->tiles * 2 * Hk;
-    for (;;) {
+    const int all = p.head->tickets;
+    if (all == 0) return;
+    int number = 0;  // thread 0: the next ticket
+    auto next_ticket = [&](int slot) {  // by warp 0
+        int at = 0, seq = 0;
+        const Ticket k = describe(p, __shfl_sync(0xffffffffu, number, 0), all, &at, &seq);
         if (tid == 0) {
-            s_ticket = atomicAdd(&p.head->ticket, 1);
+            s_ticket[slot] = k;
+            s_list[slot] = at;
+            s_seq[slot] = seq;
+            if (k.number >= 0) number = atomicAdd(&p.head->ticket, 1);
+        }
+    };
+    auto look_up = [&](int slot) {
+        if (s_ticket[slot].number >= 0 && tid < s_ticket[slot].rows) {
+            const int base = s_ticket[slot].base;
+            const int src = base + __ldg(p.list + s_list[slot] + tid), dst = base + s_ticket[slot].r0 + tid;
+            const int from = page_of(a.kv, s_seq[slot], src), to = page_of(a.kv, s_seq[slot], dst);
+            s_src[slot][tid] = from < 0 || to < 0 ? -1 : (int64_t)from * Hk * ps + src % ps;
+            s_dst[slot][tid] = (int64_t)to * Hk * ps + dst % ps;
+        }
+    };
+    if (tid < 32) {
+        if (tid == 0) {
+            number = atomicAdd(&p.head->ticket, 1);
             s_stop = 0;
         }
-        __syncthreads();
-        const int64_t ticket = s_ticket;
-        if (ticket >= all) return;
-        const int tile = (int)(ticket / (2 * Hk)), chain = (int)(ticket % (2 * Hk));
-        int lo = 0, hi = a.kv.num_seqs - 1;  // the last sequence whose first tile is <= tile
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.seqs[mid].tile0 <= tile) lo = mid; else hi = mid - 1;
-        }
-        const int s = lo;
-        const Moved q = p.seqs[s];
-        const int i = tile - q.tile0;                      // tile of the sequence
-        const int r0 = q.stay + i * p.R, rows = min(p.R, q.kept - r0);
-        const int j = chain >> 1;
-        for (int r = tid; r < rows; r += kMoveThreads) {
-            const int src = q.base + p.list[q.at + r0 + r], dst = q.base + r0 + r;
-            const int ps_ = page_of(a.kv, s, src), pd = page_of(a.kv, s, dst);
-            s_src[r] = ps_ < 0 || pd < 0 ? -1 : (int64_t)ps_ * Hk * ps + src % ps;
-            s_dst[r] = (int64_t)pd * Hk * ps + dst % ps;
-        }
-        __syncthreads();
-        char *base = static_cast<char *>(chain & 1 ? a.kv.v : a.kv.k) + (int64_t)j * ps * a.kv.d * 2;
+        next_ticket(0);
+        next_ticket(1);
+    }
+    __syncthreads();
+    look_up(0);
+    __syncthreads();
+    for (int b = 0;; b = b == 2 ? 0 : b + 1) {
+        const Ticket k = s_ticket[b];
+        if (k.number < 0) return;
+        const int pieces = k.rows << shift;  // of a chain
         uint4 v[kInFlight];
-        int pos = 0;
+        // piece x of the tile: its row, and where its chain's row 0 of page 0 lies
+        auto row_of = [&](int x) { return (k.chains == 1 ? x : x % pieces) >> shift; };
+        auto base_of = [&](int x) {
+            const int c = k.chains == 1 ? k.chain : k.chain + x / pieces;
+            return static_cast<char *>(c & 1 ? a.kv.v : a.kv.k) + (int64_t)(c >> 1) * ps * d2 + (x & ((1 << shift) - 1)) * 16;
+        };
 #pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-            const int x = tid + k * kMoveThreads, r = x / pieces;
-            if (r < rows && s_src[r] >= 0)
-                v[k] = *reinterpret_cast<const uint4 *>(base + s_src[r] * (a.kv.d * 2) + (x % pieces) * 16);
+        for (int j = 0; j < kInFlight; ++j) {
+            const int x = tid + j * kMoveThreads;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (x < pieces * k.chains) {
+                const int64_t src = s_src[b][row_of(x)];
+                if (src >= 0) v[j] = *reinterpret_cast<const uint4 *>(base_of(x) + src * d2);
+            }
         }
-        // the first chain moves the positions too: row (page * Hk) * ps + slot, less the heads
+        // the first chains' ticket moves the positions too: row (page * Hk) * ps + slot, less the heads
         auto pos_at = [&](int64_t row) { return row / ((int64_t)Hk * ps) * ps + row % ((int64_t)Hk * ps); };
-        const bool places = a.kv.pos && chain == 0 && tid < rows && s_src[tid] >= 0;
-        if (places) pos = a.kv.pos[pos_at(s_src[tid])];
-        // read: nothing that this tile wrote over later can reach these rows any more
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) store_release(p.flags + ticket, 1);
-        // the tiles that read what this one is about to write over
-        const int64_t e = edges_of(p, s);
-        const int n = a.cu_seqlens[s + 1] - a.cu_seqlens[s];
-        const int ea = p.edges[e + r0 / p.R] - q.at;
-        const int eb = (r0 + rows - 1) / p.R + 1 < (n + p.R - 1) / p.R ? p.edges[e + (r0 + rows - 1) / p.R + 1] - q.at : q.kept;
-        const int t0 = max(ea - q.stay, 0) / p.R, t1 = min((max(eb - q.stay, 0) + p.R - 1) / p.R, i);
-        for (int t = t0 + tid; t < t1; t += kMoveThreads) {
-            const int *flag = p.flags + (int64_t)(q.tile0 + t) * 2 * Hk + chain;
+        const bool places = k.places && tid < k.rows && s_src[b][tid] >= 0;
+        int pos = 0;
+        if (places) pos = a.kv.pos[pos_at(s_src[b][tid])];
+        // most of those that this one has to wait for have long read their rows
+        int t = k.w0 + tid * k.step;
+        while (t < k.w1 && load_acquire(p.flags + t)) t += kMoveThreads * k.step;
+        if (tid < 32) next_ticket(b == 0 ? 2 : b - 1);
+        look_up(b == 2 ? 0 : b + 1);
+        // All rows of the block have come: the barrier and the release order the reads before whatever
+        // a waiter writes, and the sum makes every thread hold its values before it arrives.  (A fence
+        // of every thread waits for the stores of the ticket before, too.)
+        uint32_t sum = 0;
+#pragma unroll
+        for (int j = 0; j < kInFlight; ++j) sum ^= v[j].x ^ v[j].y ^ v[j].z ^ v[j].w;
+        const bool some = __syncthreads_or((t < k.w1) | (sum == 0x9e3779b9u) | (pos == INT32_MIN));
+        if (tid == 0) store_release(p.flags + k.number, 1);
+        if (some) {
             const long long began = clock64();
-            while (!load_acquire(flag)) {
-                if (*(volatile int *)&p.head->abort || clock64() - began > a.wait_limit) {
+            while (t < k.w1) {
+                if (load_acquire(p.flags + t)) {
+                    t += kMoveThreads * k.step;
+                } else if (*(volatile int *)&p.head->abort || clock64() - began > a.wait_limit) {
                     *(volatile int *)&p.head->abort = 1;
                     s_stop = 1;
                     break;
                 }
             }
-        }
-        __syncthreads();
-        if (s_stop) {
-            if (tid == 0) atomicOr(a.kv.err, kErrTimeout);
-            return;
+            __syncthreads();
+            if (s_stop) {
+                if (tid == 0) atomicOr(a.kv.err, kErrTimeout);
+                return;
+            }
         }
 #pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-            const int x = tid + k * kMoveThreads, r = x / pieces;
-            if (r < rows && s_src[r] >= 0)
-                *reinterpret_cast<uint4 *>(base + s_dst[r] * (a.kv.d * 2) + (x % pieces) * 16) = v[k];
+        for (int j = 0; j < kInFlight; ++j) {
+            const int x = tid + j * kMoveThreads;
+            if (x < pieces * k.chains && s_src[b][row_of(x)] >= 0)
+                *reinterpret_cast<uint4 *>(base_of(x) + s_dst[b][row_of(x)] * d2) = v[j];
         }
-        if (places) a.kv.pos[pos_at(s_dst[tid])] = pos;
-        __syncthreads();  // s_src, s_dst and the ticket are free
+        if (places) a.kv.pos[pos_at(s_dst[b][tid])] = pos;
+        // (of the three slots the next pass writes the one that no thread reads any more)
     }
 }
 
@@ -296,6 +423,9 @@ cudaError_t launch_kv_compact(const KvCompactArgs &a, int num_sms, cudaStream_t 
     Params p{};
     p.a = a;
     p.R = tile_rows(a.kv.d);
+    while (1 << p.r_log2 < p.R) ++p.r_log2;
+    while (p.g_log2 < 30 && 1 << p.g_log2 < a.G) ++p.g_log2;
+    if (1 << p.g_log2 != a.G) p.g_log2 = -1;
     const Layout L = layout_of(a.T, a.kv.num_seqs, a.kv.Hk, a.kv.d);
     char *ws = static_cast<char *>(a.workspace);
     p.head = reinterpret_cast<Head *>(ws + L.head);

@@ -62,7 +62,7 @@ __device__ __forceinline__ int take(const PagePool &p, int top, int rank) {
 
 // ---------------------------------------------------------------- reserve
 
-__global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
     reserve_kernel(const PagePool pool, const PageTable t, const int32_t *have, const int32_t *want) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
@@ -91,6 +91,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads)
             rank += __popc(m);
         }
     }
+    await_all();
     // (all blocks have read the count: they met in the scan)
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         if (total > top) atomicOr(pool.err, kErrNoPages);
@@ -100,7 +101,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads)
 
 // ---------------------------------------------------------------- release
 
-__global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
     release_kernel(const PagePool pool, const PageTable t, const int32_t *first, const int32_t *end) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
@@ -154,6 +155,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads)
         if (pg >= 0) t.entries[at] = -1;
         rank += __popc(m);
     });
+    await_all();
     if (blockIdx.x == 0 && threadIdx.x == 0 && total) *pool.num_free = min(top + total, pool.num_pages);
 }
 
@@ -185,7 +187,7 @@ __device__ __forceinline__ int entry_of(const ForkArgs &a, int parent, int i) {
     return pg < 0 || pg >= a.pool.num_pages ? -1 : pg;
 }
 
-__global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
+__global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a) {
     const int lane = threadIdx.x & 31, n = a.children;
     pdl_wait();
     const int top = free_of(a.pool);
@@ -222,6 +224,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads) fork_kerne
             a.copies[2 * n + i] = c.rows;
         }
     }
+    await_all();
     meet();
     const Runs runs(n, a.from.max_pages);
     for (int64_t k = runs.from; k < runs.to; ++k) {

@@ -58,9 +58,14 @@ constexpr int kAllWarps = kBlocks * kWarps;
 __device__ __forceinline__ int cluster_warp() { return blockIdx.x * kWarps + (threadIdx.x >> 5); }
 
 // All threads of the cluster meet; what each wrote before is there for all (read through L2: __ldcg).
-__device__ __forceinline__ void meet() {
+__device__ __forceinline__ void arrive() {
     __threadfence();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void await_all() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void meet() {
+    arrive();
+    await_all();
 }
 
 // Shared memory of another block of the cluster.
@@ -73,7 +78,8 @@ __device__ __forceinline__ int read_other(const int *mine, int block) {
 }
 
 // Sum of `mine` (a warp's) over the warps before this one in the cluster; *total over all.  Every thread
-// of the cluster comes here, with its warp's value.
+// of the cluster comes here once, with its warp's value, and calls await_all() later: nobody may leave
+// while another block reads its sum.
 __device__ __forceinline__ int before_warp(int mine, int *total) {
     __shared__ int s_warp[kWarps], s_block;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -95,7 +101,7 @@ __device__ __forceinline__ int before_warp(int mine, int *total) {
         if (b < (int)blockIdx.x) before += v;
         all += v;
     }
-    meet();  // nobody leaves, or writes again, before all have read
+    arrive();
     *total = all;
     return before + own;
 }
