@@ -26,10 +26,10 @@ __device__ __forceinline__ void set_of(Unit &u, int first, int wend, int send, b
 template <bool kTree>
 __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Params p, uint32_t *bits, int tpu) {
     __shared__ int64_t sh[32];
-    __shared__ int bad, s_off[kPlanThreads];
+    __shared__ int bad, s_wrong, s_off[kPlanThreads];
     const AttendArgs &a = p.a;
     const int B = a.kv.num_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) bad = 0;
+    if (tid == 0) bad = s_wrong = 0;
     pdl_wait();
     pdl_trigger();  // what came before is complete: the main kernel's set-up may overlap
     __syncthreads();
@@ -69,7 +69,11 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
         if (s < B) {
             p.seq_off[s] = (int)(at < p.max_units ? at : p.max_units);
             if (s0 == 0) s_off[s] = p.seq_off[s];
-            if (kTree) p.seen[s].z = 0;
+            // (see Pieces::all)
+            const int past = kTree && n ? a.kv.kv_lens[s] - (a.cu_seqlens[s + 1] - a.cu_seqlens[s]) : 0;
+            p.seen[s] = kTree ? make_int4(a.kv_start ? max(past, 0) : 0, past + (a.cu_seqlens[s + 1] - a.cu_seqlens[s]),
+                                          min(a.sinks, max(past, 0)), 0)
+                              : make_int4(INT32_MAX, 0, 0, 0);
         }
         units += total;
     }
@@ -88,7 +92,8 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
             bool wrong = n > UP_TREE_MAX;
             for (int j = lane; j < n && !wrong; j += 32) wrong = a.parents[c0 + j] < -1 || a.parents[c0 + j] >= j;
             if (__any_sync(0xffffffffu, wrong) && lane == 0) {
-                p.seen[s].z = 1;
+                s_wrong = 1;
+                p.seen[s].y = -1;
                 atomicOr(a.kv.err, kErrTree);
             }
         }
@@ -107,7 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
         u.tok0 = c0 + (int)(i - p.seq_off[lo]) * tpu;
         u.ntok = min(tpu, c1 - u.tok0);
         u.kv = kv_len_of(a.kv, lo, c1 - c0);
-        if (kTree && p.seen[lo].z) u.kv = -1;
+        if (kTree && s_wrong && p.seen[lo].y < 0) u.kv = -1;
         if (kTree && u.kv >= 0) {
             u.hi0 = u.kv - (c1 - c0);
             set_of(u, 0, u.kv, min(a.sinks, u.hi0), false);
@@ -122,8 +127,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
         constexpr int kSame = 4;
         for (int64_t i0 = warp * kSame; i0 < units; i0 += kPlanThreads / 32 * kSame) {
             Unit u = unit_at(min(i0 + (lane & (kSame - 1)), units - 1));
+            // (the first token has one before it in its sequence?)
+            const bool goes_on = u.tok0 > a.cu_seqlens[u.s];
             int tok0[kSame], ntok[kSame], kv[kSame], first[kSame], end[kSame], some[kSame];
-            bool gaps[kSame];
+            bool on[kSame], gaps[kSame], torn[kSame];
 #pragma unroll
             for (int k = 0; k < kSame; ++k) {
                 tok0[k] = __shfl_sync(0xffffffffu, u.tok0, k);
@@ -132,7 +139,8 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
                 if (kv[k] < 0) ntok[k] = 0;
                 first[k] = INT32_MAX;
                 end[k] = some[k] = 0;
-                gaps[k] = false;
+                on[k] = __shfl_sync(0xffffffffu, goes_on, k);
+                gaps[k] = torn[k] = false;
             }
             for (int t = lane; t < tpu; t += 32) {
                 int2 v[kSame], b[kSame];
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
                     } else {
                         const int2 *vis = reinterpret_cast<const int2 *>(a.visible) + at;
                         v[k] = *vis;
-                        b[k] = vis[t && t < ntok[k] ? -1 : 0];
+                        b[k] = vis[(t || on[k]) && t < ntok[k] ? -1 : 0];
                     }
                 }
 #pragma unroll
@@ -157,7 +165,9 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
                         first[k] = min(first[k], r.x);
                         end[k] = max(end[k], r.y);
                         some[k] = max(some[k], min(v[k].y, kv[k]));
-                        gaps[k] |= r.y > 0 && max(before.x, r.x) > min(before.y, r.y);
+                        const bool apart = r.y > 0 && max(before.x, r.x) > min(before.y, r.y);
+                        torn[k] |= apart;
+                        gaps[k] |= apart && t;
                     }
                 }
             }
@@ -165,14 +175,21 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
             for (int k = 0; k < kSame; ++k) {
                 const int lo = __reduce_min_sync(0xffffffffu, first[k]);
                 const int hi = __reduce_max_sync(0xffffffffu, end[k]), most = __reduce_max_sync(0xffffffffu, some[k]);
-                const bool torn = __any_sync(0xffffffffu, gaps[k]);
+                const bool gap = __any_sync(0xffffffffu, gaps[k]), tear = __any_sync(0xffffffffu, torn[k]);
                 if (lane != k || i0 + k >= units) continue;
                 if (u.kv >= 0) {
                     if constexpr (kTree) {
                         set_of(u, min(lo, u.hi0), u.kv, min(a.sinks, u.hi0), false);
+                        atomicMin(&p.seen[u.s].x, lo);
                     } else {
                         u.hi0 = min(a.sinks, most);
-                        set_of(u, hi > 0 ? lo : 0, hi, u.hi0, torn);
+                        set_of(u, hi > 0 ? lo : 0, hi, u.hi0, gap);
+                        if (hi > 0) {
+                            atomicMin(&p.seen[u.s].x, lo);
+                            atomicMax(&p.seen[u.s].y, hi);
+                        }
+                        atomicMax(&p.seen[u.s].z, u.hi0);
+                        if (tear) atomicOr(&p.seen[u.s].w, 1);
                     }
                 }
                 p.units[i0 + k] = u;

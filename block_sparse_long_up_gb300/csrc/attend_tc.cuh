@@ -297,8 +297,11 @@ struct Pieces {
     int ta, tb;          // tiles [ta, tb) of the unit
     int64_t index = -1;  // pieces so far, less one
     // kSet: the windows' first slot and their end, the end of the first slots that stay
-    // visible and their tiles; the windows' tiles lie `shift` tiles on
+    // visible and their tiles; the windows' tiles lie `shift` tiles on.  Of the sequence's tokens
+    // together: their windows' first slot and end, the first slots' end, and whether the
+    // windows leave gaps
     int wfirst, wend, send, stiles, shift;
+    int4 all;
 
     __device__ explicit Pieces(const Params &pp) : p(pp) {
         const Plan pl = *pp.plan;
@@ -337,6 +340,7 @@ struct Pieces {
                 send = p.bits ? min(p.a.sinks, u.hi0) : u.hi0;
                 stiles = (send + kRows - 1) / kRows;
                 shift = max(wfirst / kRows - stiles, 0);
+                all = __ldg(p.seen + u.s);
             }
             // the next unit's description, on its way while this one is worked on
             after = ui + 1 < n ? ui + 1 : 0;
@@ -565,7 +569,24 @@ __device__ __forceinline__ void clear_unseen(uint32_t stage, int from, int to) {
     __syncwarp();
 }
 
-// The same for those of the 32 rows from `from` on whose bit in m is clear.
+// Zeros the rows [from, to) and those from `end` on.
+template <int D>
+__device__ __forceinline__ void clear_rows(uint32_t stage, int from, int to, int end) {
+    using C = Cfg<D>;
+    const int lane = threadIdx.x & 31;
+    auto zero = [&](uint32_t at) {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+    };
+#pragma unroll 1
+    for (int pn = 0; pn < C::kStagePanels; ++pn) {
+        for (int i = from * 8 + lane; i < to * 8; i += 32) zero(stage + pn * kPanel + i * 16);
+        for (int i = end * 8 + lane; i < kRows * 8; i += 32) zero(stage + pn * kPanel + i * 16);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
+// Zeros those of the 32 rows from `from` on whose bit in m is clear.
 template <int D>
 __device__ __forceinline__ void clear_gaps(uint32_t stage, int from, uint32_t m) {
 #pragma unroll 1
@@ -577,6 +598,14 @@ __device__ __forceinline__ void clear_gaps(uint32_t stage, int from, uint32_t m)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
 }
+
+// In the kernel of sets a piece of one row tile -- a few tokens over a long cache, where a step's
+// logits, softmax and product follow one another -- is two streams: the softmax warpgroups and the
+// two S buffers take its steps in turn, each with a reference, a sum and an output accumulator of
+// its own (that of the second row tile), joined at the piece's end.  (8 tokens over 128K of 8/2 heads of 64: XX us
+// instead of 45, of 32/8 heads of 128 XX instead of 99.)
+template <Mask kMask, int D>
+constexpr bool twin = kMask == kSet && Cfg<D>::kTiles == 2;
 
 // MMA issuer x (0: warp 1, 1: warp 3).  The whole warp walks the loop and one elected
 // lane issues.  With two row tiles both issuers read every stage and each releases
@@ -653,6 +682,17 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
         for (int part = 0; part < C::kParts; ++part)
             if (!wait_stage(i + part)) return false;
         const int key0 = w.key0(t);
+        if constexpr (kMask == kSet) {
+            if (!w.all.w) {
+                // what no token of the sequence sees: between the first slots and the windows, and behind these
+                const int from = max(w.all.z - key0, 0), to = min(w.all.x - key0, kRows);
+                const int end = max(max(w.all.y, w.all.z) - key0, 0);
+                if (from >= to && end >= kRows) return true;
+                for (int part = 0; part < C::kParts; ++part)
+                    clear_rows<D>(ring + ((i + part) % C::kStages) * C::kStageBytes, from, min(to, end), end);
+                return true;
+            }
+        }
         if constexpr (kMask != kRanges) {
             // all that the unit's own rows do not see
             if (kMask == kSet ? !w.gaps() && w.sees_all(key0)
@@ -746,7 +786,8 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
                     // (Where a tile is one stage, the ring's order puts only older keys there.)
                     if (P > 1 && !mbar_wait_warp(smem_u32(&sh.sfull[0][buf]), use.par(t, 1), ab, lim)) goto out;
                     if (!ready_v(i, t)) goto out;
-                    if (!pv(0, buf, i, t == 0, 0, use.par(t, 1))) goto out;
+                    const bool twins = twin<kMask, D>;
+                    if (!pv(twins ? buf : 0, buf, i, t < (twins ? 2 : 1), 0, use.par(t, 1))) goto out;
                     for (int part = 0; part < P; ++part) release(i + part, 2);
                 }
             }
@@ -780,7 +821,8 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
     using C = Cfg<D>;
     constexpr bool kSplit = C::kTiles == 1;      // the warpgroups share a row tile, 64 columns each
     constexpr int kCh = kSplit ? 2 : 4;          // chunks of 32 columns of a thread
-    const int et = kSplit ? 0 : e;               // row tile
+    constexpr bool kTwin = twin<kMask, D>;
+    const int et = kSplit ? 0 : e;               // row tile (of a piece of two), output accumulator
     const int ch0 = kSplit ? 2 * e : 0;          // first chunk
     const AttendArgs &a = p.a;
     const int tid = threadIdx.x & 127, lane = tid & 31, quarter = (threadIdx.x >> 5) & 3;
@@ -806,11 +848,14 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
     Pieces<kMask> w(p);
     while (w.next()) {
         const int n = w.steps(), used = kSplit ? 1 : w.tiles_used();
-        if (et >= used) {
+        const bool twins = kTwin && used == 1;
+        if (et >= used && !twins) {
             use.add(n, used);
             continue;
         }
-        const int tok = et * p.tpt + tl;  // of the unit
+        const int every = twins ? 2 : 1, t_first = twins ? (int)((e - use.one) & 1u) : 0;  // this warpgroup's steps
+        const int rt = twins ? 0 : et;        // row tile
+        const int tok = rt * p.tpt + tl;  // of the unit
         const bool valid = tl < p.tpt && tok < w.u.ntok;
         int2 vis = make_int2(INT32_MIN, INT32_MAX);  // a row nobody reads needs no mask
         Row row{0, INT32_MAX, 0, INT32_MAX, nullptr};
@@ -855,8 +900,8 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                 }
             }
         };
-        fetch_pos(0);
-        for (int t = 0; t < n; ++t) {
+        fetch_pos(t_first);
+        for (int t = t_first; t < n; t += every) {
             const int buf = use.buf(t, et, used), k0 = w.key0(t);
             float at = 0.f;  // this row's position relative to the step's first seen key
             const float *sp = s_pos + (2 * et + (pos_steps & 1)) * 128;
@@ -874,7 +919,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                     __syncwarp();
                     if (!__all_sync(0xffffffffu, ok)) return;
                     ++pos_steps;
-                    fetch_pos(t + 1);
+                    fetch_pos(t + every);
                 }
             }
             {
@@ -1013,9 +1058,9 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                 const float f = grew ? exp2f(m - (mt - kLift<kFp16>)) : 1.f;
                 if (grew) m = mt - kLift<kFp16>;
                 l *= f;
-                if (t > 0) {
-                    const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t - 1, et, used)]), use.par(t - 1, used),
-                                              &sh.abort, a.wait_limit);
+                if (t >= every) {
+                    const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t - every, et, used)]),
+                                              use.par(t - every, used), &sh.abort, a.wait_limit);
                     __syncwarp();
                     if (!__all_sync(0xffffffffu, ok)) return;
                     tc_fence_after();
@@ -1072,13 +1117,39 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             unpack2(add2(sum[0], sum[1]), x, y);
             l += x + y;
         }
-        {
-            const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(n - 1, et, used)]), use.par(n - 1, used),
+        const int t_last = twins ? n - 1 - ((n - 1 - t_first) & 1) : n - 1;  // before t_first: no step
+        if (t_last >= t_first) {
+            const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t_last, et, used)]), use.par(t_last, used),
                                       &sh.abort, a.wait_limit);
             __syncwarp();
             if (!__all_sync(0xffffffffu, ok)) return;
         }
         tc_fence_after();
+        float f0 = 1.f, f1 = 0.f;  // what the first and the second stream count
+        if constexpr (kTwin) {
+            if (twins) {
+                // the second warpgroup hands its reference and sum over (each warp where it lays out output
+                // rows), then waits until its accumulator has been read
+                float2 *x = reinterpret_cast<float2 *>(s_out + (4 + quarter) * 4096);
+                if (e == 1) {
+                    x[lane] = make_float2(m, l);
+                    tc_fence_before();
+                    if (!meet()) return;
+                    if (!meet()) return;
+                    use.add(n, used);
+                    continue;
+                }
+                tc_fence_before();
+                if (!meet()) return;
+                tc_fence_after();
+                const float2 y = x[lane];
+                const float both = fmaxf(m, y.x), at = both == -INFINITY ? 0.f : both;
+                f0 = exp2f(m - at);
+                f1 = exp2f(y.x - at);
+                m = both;
+                l = fmaf(f0, l, f1 * y.y);
+            }
+        }
         if constexpr (kSplit) {  // the row's sum is both threads'
             float *x = reinterpret_cast<float *>(s_xch);
             x[e * 128 + tid] = l;
@@ -1089,7 +1160,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
         const bool whole = w.ta == 0 && w.tb == w.u.tiles;
         const int64_t orow = (int64_t)(w.u.tok0 + tok) * a.Hq + head;
         float *part = p.parts + (int64_t)(2 * blockIdx.x + (w.index ? 1 : 0)) * C::kUnitRows * (D + 4);
-        const int prow = et * kRows + tid;
+        const int prow = rt * kRows + tid;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (valid && (!kSplit || e == 0)) {
             if (!whole) {
@@ -1109,6 +1180,27 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             tmem_ld32(ocol + c + 32, o[1]);
             tmem_wait_ld_dep(o[0]);
             tmem_wait_ld_dep(o[1]);
+            if constexpr (kTwin) {
+                if (twins) {
+                    // (of a piece of one step one accumulator holds nothing of it)
+                    const bool some0 = t_last >= t_first, some1 = n > 1 || !some0;
+                    if (some1) {
+                        float o1[2][32];
+                        tmem_ld32(ocol + D + c, o1[0]);
+                        tmem_ld32(ocol + D + c + 32, o1[1]);
+                        tmem_wait_ld_dep(o1[0]);
+                        tmem_wait_ld_dep(o1[1]);
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) {
+                            const float first = some0 ? f0 * o[i >> 5][i & 31] : 0.f;
+                            o[i >> 5][i & 31] = fmaf(f1, o1[i >> 5][i & 31], first);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) o[i >> 5][i & 31] *= f0;
+                    }
+                }
+            }
             if (whole) {
                 uint4 pc[8];
 #pragma unroll
@@ -1174,6 +1266,9 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             }
         }
         tc_fence_before();  // the reads end before the next piece's first product is let in
+        if constexpr (kTwin) {
+            if (twins && !meet()) return;
+        }
         use.add(n, used);
     }
 }
@@ -1346,7 +1441,7 @@ __device__ __forceinline__ void join_piece(const Params &p, const Plan &pl, cons
 // over 128K, whose 8 units are in 19 parts each; XX and XX so.)  All blocks together also write the rows of the
 // units without a visible slot, or of all tokens when the batch is malformed.
 template <bool kFp16, int D>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const Params p) {
+__global__ void __launch_bounds__(kJoinThreads, 3) attend_join_kernel(const Params p) {
     using C = Cfg<D>;
     constexpr int kRowGroups = C::kUnitRows / kJoinRows;
     __shared__ int s_cut[kMaxSms], s_count[kMaxSms / 32];

@@ -304,7 +304,7 @@ __device__ Ticket describe(const Params &p, int number, int all, int *list_at, i
 
 // A block reads a tile's rows into registers, and while they come one warp describes the ticket after
 // next and all look up the next one's rows (each a chain of loads as long as the rows' own: 131072
-// tokens of which a quarter stay take XX us so, 62 with one ticket looked up whole).  It tells that
+// tokens of which a quarter stay take 54 us, 3.3 + 3.3 TB/s less what the cache keeps; 62 with one ticket looked up whole).  It tells that
 // its rows are there, waits for whoever still has to read the slots that they go to, and writes them.
 __global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const Params p) {
     constexpr int kMaxRows = tile_rows(64);
@@ -415,6 +415,104 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const Params p
     }
 }
 
+// ---------------------------------------------------------------- few tokens a sequence
+
+// Block (j, s): the keys and values of head j of sequence s, in one launch.  It scans the sequence's flags
+// kRun at a time and moves what they keep itself, a tile of rows read into registers before it is
+// written; so nothing waits for another block.  In a graph, 8 heads of 128: 64 sequences of 64 tokens
+// 6-9 us (by tickets 22-23), 256 of 64 14-21 (23-50), one of 256 4-10 (17); but 16384 tokens 142-519 (23-46)
+// where all are one sequence's, and 4096 38-122 (20-24).  Which it is the host does not know: up to 1024
+// tokens times the root of the number of sequences.
+constexpr int kRun = 256;
+static_assert(kRun == kMoveThreads, "a thread a flag");
+bool few_tokens(int64_t T, int64_t num_seqs) { return T * T <= num_seqs << 20; }
+
+__global__ void __launch_bounds__(kMoveThreads) kv_few_kernel(const Params p) {
+    __shared__ int64_t s_src[kRun], s_dst[kRun];
+    __shared__ int s_warp[kMoveThreads / 32], s_bad;
+    const KvCompactArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int j = blockIdx.x % a.kv.Hk, s = blockIdx.x / a.kv.Hk, Hk = a.kv.Hk, ps = a.kv.page_size, d2 = a.kv.d * 2;
+    const int shift = a.kv.d == 64 ? 3 : a.kv.d == 128 ? 4 : 5;
+    if (tid == 0) s_bad = 0;
+    pdl_wait();
+    __syncthreads();
+    // a malformed cu_seqlens is one for all sequences
+    for (int x = tid; x < a.kv.num_seqs; x += kMoveThreads) {
+        const int c0 = a.cu_seqlens[x], c1 = a.cu_seqlens[x + 1];
+        if (c0 < 0 || c1 < c0 || c1 > a.T || (x == 0 && c0 != 0)) s_bad = 1;
+    }
+    __syncthreads();
+    Region r{-1, 0, 0};
+    if (s_bad) {
+        if (blockIdx.x == 0 && tid == 0) atomicOr(a.kv.err, kErrCuSeqlens);
+    } else {
+        r = region_of(a, s, j == 0 && tid == 0);
+    }
+    if (r.base < 0) {
+        if (j == 0 && tid == 0) a.lens_out[s] = a.kv.kv_lens[s];
+        return;
+    }
+    const int n = r.end - a.cu_seqlens[s];
+    int kept = 0;  // of the runs before
+    for (int i0 = 0; i0 < n; i0 += kRun) {
+        const int i = i0 + tid;
+        const bool keep = i < n && a.keep[r.flags + (p.g_log2 >= 0 ? i >> p.g_log2 : i / a.G)];
+        const unsigned m = __ballot_sync(0xffffffffu, keep);
+        if (lane == 0) s_warp[warp] = __popc(m);
+        __syncthreads();
+        int before = 0, rows = 0;
+#pragma unroll
+        for (int w = 0; w < kMoveThreads / 32; ++w) {
+            if (w == warp) before = rows;
+            rows += s_warp[w];
+        }
+        before += __popc(m & ((1u << lane) - 1u));
+        if (keep) {
+            const int src = r.base + i, dst = r.base + kept + before;
+            // (one that stays where it is, like the others whose pages are none, does not move)
+            const int from = src == dst ? -1 : page_of(a.kv, s, src), to = from < 0 ? -1 : page_of(a.kv, s, dst);
+            s_src[before] = to < 0 ? -1 : ((int64_t)from * Hk + j) * ps + src % ps;
+            s_dst[before] = ((int64_t)to * Hk + j) * ps + dst % ps;
+        }
+        __syncthreads();
+        const int pieces = rows << shift;  // of the keys; the values' follow
+        // kept tokens of this run go to slots of this run and of those before: read in order, they can be
+        // written in order
+        for (int x0 = 0; x0 < 2 * pieces; x0 += kInFlight * kMoveThreads) {
+            uint4 v[kInFlight];
+            auto at = [&](int x, const int64_t *row) {
+                const bool value = x >= pieces;
+                const int y = value ? x - pieces : x;
+                return static_cast<char *>(value ? a.kv.v : a.kv.k) + row[y >> shift] * d2 + (y & ((1 << shift) - 1)) * 16;
+            };
+            auto moves = [&](int x) { return x < 2 * pieces && s_src[(x >= pieces ? x - pieces : x) >> shift] >= 0; };
+#pragma unroll
+            for (int k = 0; k < kInFlight; ++k) {
+                const int x = x0 + tid + k * kMoveThreads;
+                if (moves(x)) v[k] = *reinterpret_cast<const uint4 *>(at(x, s_src));
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kInFlight; ++k) {
+                const int x = x0 + tid + k * kMoveThreads;
+                if (moves(x)) *reinterpret_cast<uint4 *>(at(x, s_dst)) = v[k];
+            }
+            __syncthreads();
+        }
+        if (j == 0 && a.kv.pos) {
+            auto place = [&](int64_t row) { return row / ((int64_t)Hk * ps) * ps + row % ps; };
+            const bool moves = tid < rows && s_src[tid] >= 0;
+            const int pos = moves ? a.kv.pos[place(s_src[tid])] : 0;
+            __syncthreads();
+            if (moves) a.kv.pos[place(s_dst[tid])] = pos;
+        }
+        kept += rows;
+        __syncthreads();
+    }
+    if (j == 0 && tid == 0) a.lens_out[s] = r.base + kept;
+}
+
 }  // namespace
 
 size_t kv_compact_workspace(int64_t T, int num_seqs, int Hk, int d) { return layout_of(T, num_seqs, Hk, d).total; }
@@ -433,6 +531,11 @@ cudaError_t launch_kv_compact(const KvCompactArgs &a, int num_sms, cudaStream_t 
     p.list = reinterpret_cast<int32_t *>(ws + L.list);
     p.edges = reinterpret_cast<int32_t *>(ws + L.edges);
     p.flags = reinterpret_cast<int32_t *>(ws + L.flags);
+    // Few tokens a sequence: one launch, unless it would write lengths that its other blocks still read.
+    const int32_t *lens = a.kv.kv_lens;
+    const bool apart = a.lens_out + a.kv.num_seqs <= lens || lens + a.kv.num_seqs <= a.lens_out;
+    if (apart && few_tokens(a.T, a.kv.num_seqs) && (int64_t)a.kv.num_seqs * a.kv.Hk <= INT32_MAX)
+        return launch_pdl(kv_few_kernel, dim3((unsigned)a.kv.num_seqs * (unsigned)a.kv.Hk), dim3(kMoveThreads), 0, st, p);
     cudaError_t e = launch_pdl(kv_plan_kernel, dim3(kBlocks), dim3(kThreads), 0, st, p);
     if (e != cudaSuccess) return e;
     const int64_t most = ((int64_t)a.T / p.R + a.kv.num_seqs) * 2 * a.kv.Hk;

@@ -381,23 +381,26 @@ def equal(x, y):
 
 COMPACT = [([(1, 1)], 1), ([(5, 300), (0, 40), (7, 7), (1, 2)], 1), ([(64, 4000)] * 9, 1), ([(300, 300), (255, 1000), (257, 700)], 1),
            ([(3000, 3100), (0, 0), (0, 9), (5000, 5000)], 1), ([(4000, 4000), (65, 65), (1, 500)], 64),
-           ([(9000, 9001), (127, 127), (129, 400)], 128), ([(700, 700)], 32), ([(20000, 20000)], 1), ([(1000, 1000)], 5)]
+           ([(0, 5)] * 40 + [(9000, 9100)] + [(3, 3)] * 30, 1), ([(9000, 9001), (127, 127), (129, 400)], 128), ([(700, 700)], 32), ([(20000, 20000)], 1), ([(1000, 1000)], 5)]
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("lens,G", COMPACT, ids=str)
 @pytest.mark.parametrize("share", [0.0, 0.1, 0.5, 0.97, 1.0])
 @pytest.mark.parametrize("d,Hk,dtype", [(64, 2, "bf16"), (128, 8, "fp16"), (256, 1, "bf16")])
-def test_compaction(d, Hk, dtype, share, lens, G):
+@pytest.mark.parametrize("into", ["new", "the cache's"])
+def test_compaction(into, d, Hk, dtype, share, lens, G):
+    """(Lengths written over the cache's own take the launches of many tokens, whatever their number.)"""
     i = COMPACT.index((lens, G))
     m = Made(lens, Hk, d, [16, 128, 48, 64, 256, 384][(i + d // 64) % 6], dtype, seed=i)
     flags = flags_of(lens, G, share, i)
     k, v, p, new = compacted(m, flags, G)
     keep = torch.cat(flags).to(torch.uint8).cuda() * 3  # any value but 0 counts
     cb = ints([0] + [f.numel() for f in flags]).cumsum(0, dtype=torch.int32)
-    out = up.compact_kv(m.cache, m.cu, keep, cu_blocks=None if G == 1 else cb, G=G)
+    out = up.compact_kv(m.cache, m.cu, keep, cu_blocks=None if G == 1 else cb, G=G,
+                        kv_lens_out=None if into == "new" else m.kv_lens)
     assert up.get_device_error() == 0
-    assert out.tolist() == new and m.kv_lens.tolist() == [kv for _, kv in lens]
+    assert out.tolist() == new and m.kv_lens.tolist() == ([kv for _, kv in lens] if into == "new" else new)
     assert equal(m.kp, k) and equal(m.vp, v) and equal(m.pp, p)
 
 
@@ -423,14 +426,21 @@ def test_many_sequences_compact():
     m = Made(lens, 2, 64, 16, "bf16", seed=14)
     flags = flags_of(lens, 1, 0.5, 1)
     k, v, p, new = compacted(m, flags, 1)
-    out = up.compact_kv(m.cache, m.cu, torch.cat(flags).to(torch.uint8).cuda())
-    assert up.get_device_error() == 0 and out.tolist() == new
-    assert equal(m.kp, k) and equal(m.vp, v) and equal(m.pp, p)
+    was = [x.clone() for x in (m.kp, m.vp, m.pp)]
+    for into in (None, m.kv_lens):
+        for x, y in zip((m.kp, m.vp, m.pp), was):
+            x.copy_(y)
+        out = up.compact_kv(m.cache, m.cu, torch.cat(flags).to(torch.uint8).cuda(), kv_lens_out=into)
+        assert up.get_device_error() == 0 and out.tolist() == new
+        assert equal(m.kp, k) and equal(m.vp, v) and equal(m.pp, p)
 
 
 @pytest.mark.gpu
-def test_compaction_errors():
+@pytest.mark.parametrize("more", [0, 20000])
+def test_compaction_errors(more):
+    """Of few tokens a sequence and of many (max_tokens counts)."""
     lens = [(100, 300), (50, 90), (64, 64)]
+    most = dict(max_tokens=214 + more)
 
     def made():
         return Made(lens, 2, 64, 32, "bf16", seed=5)
@@ -439,17 +449,17 @@ def test_compaction_errors():
     keep = torch.cat(flags).to(torch.uint8).cuda()
     full = compacted(made(), flags, 1)
     # a malformed cu_seqlens: nothing moves
-    for cu in ([1, 100, 150, 214], [0, 100, 90, 214], [0, 100, 150, 215], [0, -1, 150, 214], [0, 100, 150, 1 << 30]):
+    for cu in ([1, 100, 150, 214], [0, 100, 90, 214], [0, 100, 150, 215 + more], [0, -1, 150, 214], [0, 100, 150, 1 << 30]):
         m = made()
         was = m.kp.clone()
-        out = up.compact_kv(m.cache, ints(cu), keep)
+        out = up.compact_kv(m.cache, ints(cu), keep, **most)
         assert up.get_device_error() == 1 and torch.equal(out, m.kv_lens) and equal(m.kp, was)
     # sequences that cannot be stay, the others do not
     for cb, kv in (([0, 100, 149, 214], None), ([0, 100, 100, 164], None), (None, 49), (None, -1), (None, 10 ** 6)):
         m = made()
         if kv is not None:
             m.kv_lens[1] = kv
-        out = up.compact_kv(m.cache, m.cu, keep, cu_blocks=None if cb is None else ints(cb))
+        out = up.compact_kv(m.cache, m.cu, keep, cu_blocks=None if cb is None else ints(cb), **most)
         assert up.get_device_error() == (0x10 if kv is None else 0x40)
         assert out.tolist()[1] == (90 if kv is None else kv) and out.tolist()[0] == full[3][0]
         at = m.table[1, :3].long()
@@ -460,13 +470,13 @@ def test_compaction_errors():
     out = up.compact_kv(m.cache, m.cu, keep[:200])  # flags that end too early
     assert up.get_device_error() in (1, 0x10)
     m = made()
-    out = up.compact_kv(m.cache, m.cu, keep[:200], max_tokens=214)
+    out = up.compact_kv(m.cache, m.cu, keep[:200], **most)
     assert up.get_device_error() == 0x10 and out.tolist() == full[3][:2] + [64]
     # a page outside the pool: its tokens, and those that would move there, stay
     m = made()
     was = [x.clone() for x in (m.kp, m.vp, m.pp)]
     m.table[0, 8] = -1
-    out = up.compact_kv(m.cache, m.cu, keep)
+    out = up.compact_kv(m.cache, m.cu, keep, **most)
     assert up.get_device_error() == 8 and out.tolist() == full[3]
     others = torch.ones(m.kp.shape[0], dtype=torch.bool, device="cuda")
     others[made().table[0, 8].long()] = False
