@@ -209,7 +209,6 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) kv_plan
         }
         rank += __popc(m);
     });
-    await_all();
     meet();
     if (blockIdx.x) return;
     // kept tokens of every sequence, and the tickets' numbers (many sequences in rounds)
@@ -318,11 +317,15 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const Params p
     pdl_wait();
     const int all = p.head->tickets;
     if (all == 0) return;
-    int number = 0;  // thread 0: the next ticket
-    auto next_ticket = [&](int slot) {  // by warp 0
+    // The block's chains of loads run side by side: rows are looked up by the first warps, flags
+    // asked for by those behind them, tickets described by the last (all in the first: 54 us of 131072
+    // tokens, a third of it at the barrier).
+    constexpr int kLast = kMoveThreads - 32;
+    int number = 0;  // the last warp's first thread: the next ticket
+    auto next_ticket = [&](int slot) {  // by the last warp
         int at = 0, seq = 0;
         const Ticket k = describe(p, __shfl_sync(0xffffffffu, number, 0), all, &at, &seq);
-        if (tid == 0) {
+        if (tid == kLast) {
             s_ticket[slot] = k;
             s_list[slot] = at;
             s_seq[slot] = seq;
@@ -338,8 +341,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const Params p
             s_dst[slot][tid] = (int64_t)to * Hk * ps + dst % ps;
         }
     };
-    if (tid < 32) {
-        if (tid == 0) {
+    if (tid >= kLast) {
+        if (tid == kLast) {
             number = atomicAdd(&p.head->ticket, 1);
             s_stop = 0;
         }
@@ -375,9 +378,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const Params p
         int pos = 0;
         if (places) pos = a.kv.pos[pos_at(s_src[b][tid])];
         // most of those that this one has to wait for have long read their rows
-        int t = k.w0 + tid * k.step;
+        int t = k.w0 + (tid + kMoveThreads / 2) % kMoveThreads * k.step;
         while (t < k.w1 && load_acquire(p.flags + t)) t += kMoveThreads * k.step;
-        if (tid < 32) next_ticket(b == 0 ? 2 : b - 1);
+        if (tid >= kLast) next_ticket(b == 0 ? 2 : b - 1);
         look_up(b == 2 ? 0 : b + 1);
         // All rows of the block have come: the barrier and the release order the reads before whatever
         // a waiter writes, and the sum makes every thread hold its values before it arrives.  (A fence
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const Params p
 #pragma unroll
         for (int j = 0; j < kInFlight; ++j) sum ^= v[j].x ^ v[j].y ^ v[j].z ^ v[j].w;
         const bool some = __syncthreads_or((t < k.w1) | (sum == 0x9e3779b9u) | (pos == INT32_MIN));
-        if (tid == 0) store_release(p.flags + k.number, 1);
+        if (tid == kLast - 32) store_release(p.flags + k.number, 1);
         if (some) {
             const long long began = clock64();
             while (t < k.w1) {

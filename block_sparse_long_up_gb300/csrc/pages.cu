@@ -80,6 +80,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
         mine += __popc(__ballot_sync(0xffffffffu, wants(s, i + 32, r)));
     }
     int total, rank = before_warp(mine, &total);
+    arrive();
     for (int64_t k = runs.from; k < runs.to; ++k) {
         const int s = (int)(k / runs.per_row), i0 = (int)(k % runs.per_row) * kRun + lane;
         const int2 r = pages_in(t, have[s], want[s], pool.err);
@@ -142,6 +143,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
     each([&](int at, int pg) { mine += __popc(__ballot_sync(0xffffffffu, pg >= 0 && __ldcg(pool.refs + pg) == at - num)); });
     const int top = free_of(pool);
     int total, rank = before_warp(mine, &total);
+    arrive();
     // the first entry's page on top: reserving the same entries again gives the same pages
     each([&](int at, int pg) {
         const bool back = pg >= 0 && __ldcg(pool.refs + pg) == at - num;
@@ -224,7 +226,6 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) fork_ke
             a.copies[2 * n + i] = c.rows;
         }
     }
-    await_all();
     meet();
     const Runs runs(n, a.from.max_pages);
     for (int64_t k = runs.from; k < runs.to; ++k) {

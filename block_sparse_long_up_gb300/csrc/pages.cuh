@@ -78,8 +78,8 @@ __device__ __forceinline__ int read_other(const int *mine, int block) {
 }
 
 // Sum of `mine` (a warp's) over the warps before this one in the cluster; *total over all.  Every thread
-// of the cluster comes here once, with its warp's value, and calls await_all() later: nobody may leave
-// while another block reads its sum.
+// of the cluster comes here once, with its warp's value, and meets the others again before it
+// leaves: nobody may while another block reads its sum.
 __device__ __forceinline__ int before_warp(int mine, int *total) {
     __shared__ int s_warp[kWarps], s_block;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -101,7 +101,6 @@ __device__ __forceinline__ int before_warp(int mine, int *total) {
         if (b < (int)blockIdx.x) before += v;
         all += v;
     }
-    arrive();
     *total = all;
     return before + own;
 }
