@@ -212,7 +212,7 @@ up_status attend(const void *q, const int32_t *cu_seqlens, const int32_t *parent
     a.parents = parents;
     // without a window nothing lies between the first tokens and the others
     a.sinks = visible || kv_start ? sinks : 0;
-    const auto launch = a.sinks || tree ? up::launch_attend_set : up::launch_attend;
+    const auto launch = tree ? up::launch_attend_tree : a.sinks ? up::launch_attend_sinks : up::launch_attend;
     if (launch(a, di.sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return UP_ERR_CUDA;
     return UP_OK;
 }

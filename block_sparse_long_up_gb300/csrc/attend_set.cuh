@@ -1,4 +1,4 @@
-// attend_set.cu -- attention of new tokens that see more than one range of slots: a window and
+// attend_set.cuh -- attention of new tokens that see more than one range of slots: a window and
 // the first tokens of the cache that stay visible (sinks), or the cache and a tree of
 // drafted tokens at its end.  The plans, and the launches (see attend_tc.cuh for the kernel).
 //
@@ -6,6 +6,8 @@
 // each drafted token: its ancestors and itself.  A unit's key tiles are those of the first
 // slots and those of its rows' windows; between the two nothing is read.  Only tiles at the
 // windows' edges and in the tree take the masked path, where a row's 32 slots are one word.
+#pragma once
+
 #include "attend_tc.cuh"
 
 namespace up {
@@ -23,8 +25,9 @@ __device__ __forceinline__ void set_of(Unit &u, int first, int wend, int send, b
 
 // Block 0 lists the units.  With a tree the other blocks write each token's bits: a thread walks
 // its token's line of parents, whose numbers fall at every step.
-template <bool kTree>
+template <Mask kMask>
 __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Params p, uint32_t *bits, int tpu) {
+    constexpr bool kIsTree = kMask == kTree;
     __shared__ int64_t sh[32];
     __shared__ int bad, s_wrong, s_off[kPlanThreads];
     const AttendArgs &a = p.a;
@@ -33,7 +36,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
     pdl_wait();
     pdl_trigger();  // what came before is complete: the main kernel's set-up may overlap
     __syncthreads();
-    if (kTree && blockIdx.x > 0) {
+    if (kIsTree && blockIdx.x > 0) {
         const int t = ((int)blockIdx.x - 1) * kPlanThreads + tid;
         if (t >= a.T) return;
         const int s = seq_of_token(a.cu_seqlens, B, t, a.T, a.kv.err);
@@ -70,8 +73,8 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
             p.seq_off[s] = (int)(at < p.max_units ? at : p.max_units);
             if (s0 == 0) s_off[s] = p.seq_off[s];
             // (see Pieces::all)
-            const int past = kTree && n ? a.kv.kv_lens[s] - (a.cu_seqlens[s + 1] - a.cu_seqlens[s]) : 0;
-            p.seen[s] = kTree ? make_int4(a.kv_start ? max(past, 0) : 0, past + (a.cu_seqlens[s + 1] - a.cu_seqlens[s]),
+            const int past = kIsTree && n ? a.kv.kv_lens[s] - (a.cu_seqlens[s + 1] - a.cu_seqlens[s]) : 0;
+            p.seen[s] = kIsTree ? make_int4(a.kv_start ? max(past, 0) : 0, past + (a.cu_seqlens[s + 1] - a.cu_seqlens[s]),
                                           min(a.sinks, max(past, 0)), 0)
                               : make_int4(INT32_MAX, 0, 0, 0);
         }
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
         }
         return;
     }
-    if constexpr (kTree) {
+    if constexpr (kIsTree) {
         // a warp a sequence: every parent comes before its child
         for (int s = warp; s < B; s += kPlanThreads / 32) {
             const int c0 = a.cu_seqlens[s], n = a.cu_seqlens[s + 1] - c0;
@@ -112,14 +115,14 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
         u.tok0 = c0 + (int)(i - p.seq_off[lo]) * tpu;
         u.ntok = min(tpu, c1 - u.tok0);
         u.kv = kv_len_of(a.kv, lo, c1 - c0);
-        if (kTree && s_wrong && p.seen[lo].y < 0) u.kv = -1;
-        if (kTree && u.kv >= 0) {
+        if (kIsTree && s_wrong && p.seen[lo].y < 0) u.kv = -1;
+        if (kIsTree && u.kv >= 0) {
             u.hi0 = u.kv - (c1 - c0);
             set_of(u, 0, u.kv, min(a.sinks, u.hi0), false);
         }
         return u;
     };
-    if (kTree && !a.kv_start) {
+    if (kIsTree && !a.kv_start) {
         for (int64_t i = tid; i < units; i += kPlanThreads) p.units[i] = unit_at(i);
     } else {
         // A warp takes four units at once, a lane each to begin with, then its lanes at their tokens (one at a
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
 #pragma unroll
                 for (int k = 0; k < kSame; ++k) {
                     const int at = tok0[k] + min(t, max(ntok[k] - 1, 0));
-                    if constexpr (kTree) {
+                    if constexpr (kIsTree) {
                         v[k].x = a.kv_start[at];
                     } else {
                         const int2 *vis = reinterpret_cast<const int2 *>(a.visible) + at;
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
 #pragma unroll
                 for (int k = 0; k < kSame; ++k) {
                     if (t >= ntok[k]) continue;
-                    if constexpr (kTree) {
+                    if constexpr (kIsTree) {
                         first[k] = min(first[k], max(v[k].x, 0));
                     } else {
                         const int2 r = cut_range(v[k], kv[k]), before = cut_range(b[k], kv[k]);
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
                 const bool gap = __any_sync(0xffffffffu, gaps[k]), tear = __any_sync(0xffffffffu, torn[k]);
                 if (lane != k || i0 + k >= units) continue;
                 if (u.kv >= 0) {
-                    if constexpr (kTree) {
+                    if constexpr (kIsTree) {
                         set_of(u, min(lo, u.hi0), u.kv, min(a.sinks, u.hi0), false);
                         atomicMin(&p.seen[u.s].x, lo);
                     } else {
@@ -208,41 +211,37 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
     if (tid == 0) *p.plan = Plan{W, (int)units, 0, 0};
 }
 
-template <bool kFp16, int D>
+template <Mask kMask, bool kFp16, int D>
 cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     using C = Cfg<D>;
     Params p{};
     CUtensorMap qm, km, vm;
     const size_t used = params_of<D>(a, num_sms, p);
-    uint32_t *bits = a.parents ? reinterpret_cast<uint32_t *>(static_cast<char *>(a.workspace) + used) : nullptr;
+    uint32_t *bits = kMask == kTree ? reinterpret_cast<uint32_t *>(static_cast<char *>(a.workspace) + used) : nullptr;
     p.bits = bits;
     if (!encode_maps(a, p.tpt, p.box, &qm, &km, &vm)) return cudaErrorInvalidValue;
     const bool more = a.softcap > 0.f || a.slopes || !(a.scale > 0.f);
-    auto kernel = more ? attend_kernel<kFp16, D, true, kSet> : attend_kernel<kFp16, D, false, kSet>;
-    cudaError_t e = more ? allow_smem<attend_kernel<kFp16, D, true, kSet>>(C::kSmem)
-                         : allow_smem<attend_kernel<kFp16, D, false, kSet>>(C::kSmem);
+    auto kernel = more ? attend_kernel<kFp16, D, true, kMask> : attend_kernel<kFp16, D, false, kMask>;
+    cudaError_t e = more ? allow_smem<attend_kernel<kFp16, D, true, kMask>>(C::kSmem)
+                         : allow_smem<attend_kernel<kFp16, D, false, kMask>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    const unsigned blocks = a.parents ? 1 + (unsigned)((a.T + kPlanThreads - 1) / kPlanThreads) : 1;
-    e = launch_pdl(a.parents ? attend_set_plan_kernel<true> : attend_set_plan_kernel<false>, dim3(blocks),
-                   dim3(kPlanThreads), 0, st, p, bits, C::kTiles * p.tpt);
+    const unsigned blocks = kMask == kTree ? 1 + (unsigned)((a.T + kPlanThreads - 1) / kPlanThreads) : 1;
+    e = launch_pdl(attend_set_plan_kernel<kMask>, dim3(blocks), dim3(kPlanThreads), 0, st, p, bits, C::kTiles * p.tpt);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmem, st, qm, km, vm, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(attend_join_kernel<kFp16, D>, dim3((unsigned)p.grid * kJoinPerSm), dim3(kJoinThreads), 0, st, p);
 }
 
-}  // namespace
-
-size_t attend_tree_workspace(int64_t T, int num_seqs, int Hq, int Hk, int d) {
-    return layout_of(T, num_seqs, Hq, Hk, d).total + (size_t)T * kTreeWords * sizeof(uint32_t);
-}
-
-cudaError_t launch_attend_set(const AttendArgs &a, int num_sms, cudaStream_t st) {
+template <Mask kMask>
+cudaError_t launch_set(const AttendArgs &a, int num_sms, cudaStream_t st) {
     switch (a.kv.d) {
-        case 64: return a.kv.fp16 ? launch_type<true, 64>(a, num_sms, st) : launch_type<false, 64>(a, num_sms, st);
-        case 128: return a.kv.fp16 ? launch_type<true, 128>(a, num_sms, st) : launch_type<false, 128>(a, num_sms, st);
-        default: return a.kv.fp16 ? launch_type<true, 256>(a, num_sms, st) : launch_type<false, 256>(a, num_sms, st);
+        case 64: return a.kv.fp16 ? launch_type<kMask, true, 64>(a, num_sms, st) : launch_type<kMask, false, 64>(a, num_sms, st);
+        case 128: return a.kv.fp16 ? launch_type<kMask, true, 128>(a, num_sms, st) : launch_type<kMask, false, 128>(a, num_sms, st);
+        default: return a.kv.fp16 ? launch_type<kMask, true, 256>(a, num_sms, st) : launch_type<kMask, false, 256>(a, num_sms, st);
     }
 }
+
+}  // namespace
 
 }  // namespace up

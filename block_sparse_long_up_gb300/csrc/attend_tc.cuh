@@ -1,6 +1,6 @@
 // attend_tc.cuh -- attention of new tokens over the paged cache on the sm_103a tensor
 // cores (tcgen05 + TMEM + TMA): the main kernel and the join.  attend.cu lists the work of
-// calls whose queries see one range of slots each, attend_set.cu that of calls with first
+// calls whose queries see one range of slots each, attend_set.cuh that of calls with first
 // tokens that stay visible and of drafted trees.
 //
 // out = softmax(logits) V with 4*d flops for every visible (query head, query, slot):
@@ -56,7 +56,9 @@ using namespace sm100;
 constexpr int kRows = 128;        // rows of a tile, keys of a step
 // What the rows of a unit see: a range of slots each whose union has no gaps; one with gaps;
 // any set of slots that a word of 32 bits can be asked for (see Row).
-enum Mask { kRanges, kGaps, kSet };
+enum Mask { kRanges, kGaps, kSinks, kTree };
+// the last two: the kernels of sets
+constexpr bool of_sets(Mask m) { return m == kSinks || m == kTree; }
 
 constexpr int kMinTiles = 4;      // shares are not cut finer than this: more parts cost
                                   // more to join than a step (128 tokens over 4K: 29.8,
@@ -103,7 +105,7 @@ struct Unit {
     // may be slots between first and end that no row of the unit sees.
     uint32_t edges;
     int64_t prefix;     // width of the units before this one
-    // In the kernel of sets (kSet) kt0 is the first slot of the rows' windows, complemented
+    // In the kernels of sets kt0 is the first slot of the rows' windows, complemented
     // where these leave gaps between them, `edges` the windows' end, and hi0 the end of the
     // first slots that some row sees -- or, with a tree, where the drafted tokens begin.
 
@@ -191,37 +193,45 @@ __device__ __forceinline__ uint32_t span_bits(int lo, int hi) {
 
 constexpr int kTreeWords = UP_TREE_MAX / 32;
 
-// What a row sees in the kernel of sets: the window [lo, hi), the slots below sinks and, from
-// slot tail on, those whose bits are set.
+// What a row sees in the kernels of sets: the window [lo, hi) and the slots below sinks; in a tree
+// also, from slot hi on, those whose bits are set.
+template <Mask kMask>
 struct Row {
-    int lo, hi, sinks, tail;
-    const uint32_t *bits;
+    int lo = 0, hi = INT32_MAX, sinks = 0;  // (of a row that nobody reads: all)
+    int token = 0;
 
     __device__ __forceinline__ bool all(int key) const {  // of the 128 slots at key
         return (lo <= key && hi >= key + kRows) || sinks >= key + kRows;
     }
     // the 32 slots at key, a bit each
-    __device__ __forceinline__ uint32_t word(int key) const {
+    __device__ __forceinline__ uint32_t word(const Params &p, int key) const {
         uint32_t m = span_bits(lo - key, hi - key) | span_bits(-key, sinks - key);
-        if (key > tail - 32) {
-            const int at = key - tail, i = at >> 5;  // -1: the word that begins before the tree
+        if (kMask == kTree && key > hi - 32) {
+            const uint32_t *bits = p.bits + (int64_t)token * kTreeWords;
+            const int at = key - hi, i = at >> 5;  // -1: the word that begins before the tree
             const uint32_t w0 = i >= 0 && i < kTreeWords ? bits[i] : 0u, w1 = i + 1 < kTreeWords ? bits[i + 1] : 0u;
             m |= __funnelshift_r(w0, w1, at & 31);
         }
         return m;
     }
+    __device__ __forceinline__ void set_range(int2 v, int kv, int first) {
+        lo = max(v.x, 0);
+        hi = min(v.y, kv);
+        sinks = min(first, hi);
+    }
+    // the row of the token tl tokens behind the unit's first one
+    __device__ __forceinline__ void set(const Params &p, const Unit &u, int tl) {
+        const int t = u.tok0 + tl;
+        if constexpr (kMask == kTree) {
+            lo = p.a.kv_start ? max(p.a.kv_start[t], 0) : 0;
+            hi = u.hi0;
+            sinks = min(p.a.sinks, hi);
+            token = t;
+        } else {
+            set_range(reinterpret_cast<const int2 *>(p.a.visible)[t], u.kv, p.a.sinks);
+        }
+    }
 };
-__device__ __forceinline__ Row row_of_range(int2 v, int kv, int sinks) {
-    const int hi = min(v.y, kv);
-    return Row{max(v.x, 0), hi, min(sinks, hi), INT32_MAX, nullptr};
-}
-// The row of the token tl tokens behind the unit's first one.
-__device__ __forceinline__ Row row_of(const Params &p, const Unit &u, int tl) {
-    const int t = u.tok0 + tl;
-    if (!p.bits) return row_of_range(reinterpret_cast<const int2 *>(p.a.visible)[t], u.kv, p.a.sinks);
-    return Row{p.a.kv_start ? max(p.a.kv_start[t], 0) : 0, u.hi0, min(p.a.sinks, u.hi0), u.hi0,
-               p.bits + (int64_t)t * kTreeWords};
-}
 
 // A unit's width in the work laid end to end: its key tiles, and in front of them what
 // beginning and ending it costs (queries, first logits, output).
@@ -264,8 +274,10 @@ __device__ __forceinline__ uint32_t seen_word(const Params &p, const Unit &u, in
     uint32_t m = 0;
 #pragma unroll 1
     for (int tl = threadIdx.x & 31; tl < u.ntok; tl += 32) {
-        if constexpr (kMask == kSet) {
-            m |= row_of(p, u, tl).word(key0);
+        if constexpr (of_sets(kMask)) {
+            Row<kMask> r;
+            r.set(p, u, tl);
+            m |= r.word(p, key0);
         } else {
             const int2 r = sees(p.a, u, tl);
             m |= span_bits(r.x - key0, r.y - key0);
@@ -296,12 +308,13 @@ struct Pieces {
     int after = -1;      // the index of `behind`
     int ta, tb;          // tiles [ta, tb) of the unit
     int64_t index = -1;  // pieces so far, less one
-    // kSet: the windows' first slot and their end, the end of the first slots that stay
+    // Of sets: the windows' first slot and their end, the end of the first slots that stay
     // visible and their tiles; the windows' tiles lie `shift` tiles on.  Of the sequence's tokens
     // together: their windows' first slot and end, the first slots' end, and whether the
     // windows leave gaps
     int wfirst, wend, send, stiles, shift;
     int4 all;
+    int turned;  // steps that the piece's last tiles come before its first ones (see next)
 
     __device__ explicit Pieces(const Params &pp) : p(pp) {
         const Plan pl = *pp.plan;
@@ -334,13 +347,21 @@ struct Pieces {
             at = min(end, first + u.tiles);
             if (ta >= tb) continue;  // the share ends before the unit's first tile
             ++index;
-            if constexpr (kMask == kSet) {
+            if constexpr (of_sets(kMask)) {
                 wfirst = u.kt0 < 0 ? ~u.kt0 : u.kt0;
                 wend = (int)u.edges;
-                send = p.bits ? min(p.a.sinks, u.hi0) : u.hi0;
+                send = kMask == kTree ? min(p.a.sinks, u.hi0) : u.hi0;
                 stiles = (send + kRows - 1) / kRows;
                 shift = max(wfirst / kRows - stiles, 0);
                 all = __ldg(p.seen + u.s);
+            }
+            if constexpr (kMask == kTree) {
+                // Where a share is a part of one unit, its tiles come in the order of their remainders by
+                // the share's length: the blocks that work on the units of a sequence's tree, whose shares begin
+                // anywhere, then read the same keys at the same time, once from memory.  (32 trees of up to 61
+                // tokens at head_dim 256, 4 units each: XX us and XX of 0.55 GB read, against 184 and 1.11.)
+                const int len = (int)(sh.W / sh.n), k = ta < stiles ? ta : ta + shift;
+                turned = !p.a.slopes && tb - ta >= len ? (len - k % len) % len : 0;
             }
             // the next unit's description, on its way while this one is worked on
             after = ui + 1 < n ? ui + 1 : 0;
@@ -355,8 +376,12 @@ struct Pieces {
     // with one the steps go from the last key tile to the first: the maximum is then
     // found at once, instead of growing past the slack at every step.
     __device__ int key0(int t) const {
-        const int i = p.a.slopes ? u.tiles - 1 - ta - t : ta + t;
-        if constexpr (kMask == kSet) return (i < stiles ? i : i + shift) * kRows;
+        int i = p.a.slopes ? u.tiles - 1 - ta - t : ta + t;
+        if (kMask == kTree && turned) {
+            i += turned;
+            if (i >= tb) i -= tb - ta;
+        }
+        if constexpr (of_sets(kMask)) return (i < stiles ? i : i + shift) * kRows;
         return (u.kt0 + i) * kRows;
     }
     // Of a unit of sets whose windows leave no gaps:
@@ -364,7 +389,7 @@ struct Pieces {
         return key < send || (key < wend && key > wfirst - box);
     }
     __device__ bool sees_all(int key) const {  // of the 128 slots at key, without asking for words
-        return (key >= wfirst && key + kRows <= (p.bits ? u.hi0 : wend)) || key + kRows <= send;
+        return (key >= wfirst && key + kRows <= (kMask == kTree ? u.hi0 : wend)) || key + kRows <= send;
     }
     __device__ bool gaps() const { return u.kt0 < 0; }
 };
@@ -492,10 +517,10 @@ __device__ void role_kv(const CUtensorMap *km, const CUtensorMap *vm, const Para
         auto page = [&](int t) {
             const int key = w.key0(t) + r;
             bool some = t < n && r < kRows;
-            if constexpr (kMask == kSet) some = some && w.sees_some(key, p.box);
+            if constexpr (of_sets(kMask)) some = some && w.sees_some(key, p.box);
             else some = some && key < end && key > from;
             if constexpr (kMask != kRanges) {
-                if ((kMask == kSet ? w.gaps() : w.u.gaps()) && t < n) {  // boxes in a gap are not looked up
+                if ((of_sets(kMask) ? w.gaps() : w.u.gaps()) && t < n) {  // boxes in a gap are not looked up
                     uint32_t box = 0;
 #pragma unroll 1
                     for (int k = 0; k < kRows; k += 32)
@@ -599,14 +624,6 @@ __device__ __forceinline__ void clear_gaps(uint32_t stage, int from, uint32_t m)
     __syncwarp();
 }
 
-// In the kernel of sets a piece of one row tile -- a few tokens over a long cache, where a step's
-// logits, softmax and product follow one another -- is two streams: the softmax warpgroups and the
-// two S buffers take its steps in turn, each with a reference, a sum and an output accumulator of
-// its own (that of the second row tile), joined at the piece's end.  (8 tokens over 128K of 8/2 heads of 64: XX us
-// instead of 45, of 32/8 heads of 128 XX instead of 99.)
-template <Mask kMask, int D>
-constexpr bool twin = kMask == kSet && Cfg<D>::kTiles == 2;
-
 // MMA issuer x (0: warp 1, 1: warp 3).  The whole warp walks the loop and one elected
 // lane issues.  With two row tiles both issuers read every stage and each releases
 // it; with one, the keys' issuer and the values' issuer each wait for their own stages and
@@ -682,7 +699,7 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
         for (int part = 0; part < C::kParts; ++part)
             if (!wait_stage(i + part)) return false;
         const int key0 = w.key0(t);
-        if constexpr (kMask == kSet) {
+        if constexpr (of_sets(kMask)) {
             if (!w.all.w) {
                 // what no token of the sequence sees: between the first slots and the windows, and behind these
                 const int from = max(w.all.z - key0, 0), to = min(w.all.x - key0, kRows);
@@ -695,7 +712,7 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
         }
         if constexpr (kMask != kRanges) {
             // all that the unit's own rows do not see
-            if (kMask == kSet ? !w.gaps() && w.sees_all(key0)
+            if (of_sets(kMask) ? !w.gaps() && w.sees_all(key0)
                               : !w.u.gaps() && key0 != w.u.kt0 * kRows && key0 != w.u.last_tile())
                 return true;
 #pragma unroll 1
@@ -786,8 +803,7 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
                     // (Where a tile is one stage, the ring's order puts only older keys there.)
                     if (P > 1 && !mbar_wait_warp(smem_u32(&sh.sfull[0][buf]), use.par(t, 1), ab, lim)) goto out;
                     if (!ready_v(i, t)) goto out;
-                    const bool twins = twin<kMask, D>;
-                    if (!pv(twins ? buf : 0, buf, i, t < (twins ? 2 : 1), 0, use.par(t, 1))) goto out;
+                    if (!pv(0, buf, i, t == 0, 0, use.par(t, 1))) goto out;
                     for (int part = 0; part < P; ++part) release(i + part, 2);
                 }
             }
@@ -821,8 +837,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
     using C = Cfg<D>;
     constexpr bool kSplit = C::kTiles == 1;      // the warpgroups share a row tile, 64 columns each
     constexpr int kCh = kSplit ? 2 : 4;          // chunks of 32 columns of a thread
-    constexpr bool kTwin = twin<kMask, D>;
-    const int et = kSplit ? 0 : e;               // row tile (of a piece of two), output accumulator
+    const int et = kSplit ? 0 : e;               // row tile
     const int ch0 = kSplit ? 2 * e : 0;          // first chunk
     const AttendArgs &a = p.a;
     const int tid = threadIdx.x & 127, lane = tid & 31, quarter = (threadIdx.x >> 5) & 3;
@@ -848,21 +863,18 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
     Pieces<kMask> w(p);
     while (w.next()) {
         const int n = w.steps(), used = kSplit ? 1 : w.tiles_used();
-        const bool twins = kTwin && used == 1;
-        if (et >= used && !twins) {
+        if (et >= used) {
             use.add(n, used);
             continue;
         }
-        const int every = twins ? 2 : 1, t_first = twins ? (int)((e - use.one) & 1u) : 0;  // this warpgroup's steps
-        const int rt = twins ? 0 : et;        // row tile
-        const int tok = rt * p.tpt + tl;  // of the unit
+        const int tok = et * p.tpt + tl;  // of the unit
         const bool valid = tl < p.tpt && tok < w.u.ntok;
         int2 vis = make_int2(INT32_MIN, INT32_MAX);  // a row nobody reads needs no mask
-        Row row{0, INT32_MAX, 0, INT32_MAX, nullptr};
-        if constexpr (kMask == kSet) {
+        Row<kMask> row;
+        if constexpr (of_sets(kMask)) {
             if (valid) {
-                if (!p.bits && w.u.tok0 + tok == ahead_tok) row = row_of_range(ahead, w.u.kv, a.sinks);
-                else row = row_of(p, w.u, tok);
+                if (kMask == kSinks && w.u.tok0 + tok == ahead_tok) row.set_range(ahead, w.u.kv, a.sinks);
+                else row.set(p, w.u, tok);
             }
         } else if (valid) {
             if (a.visible && w.u.tok0 + tok == ahead_tok) vis = cut_range(ahead, w.u.kv);
@@ -888,7 +900,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
         const int first = w.u.first(), end = w.u.end();
         auto position = [&](int key) {
             // (bad pages are reported where their keys are loaded; one in a gap is none)
-            const int pg = (kMask == kSet ? w.sees_some(key, 1) : key >= first && key < end) ? find_page(a.kv, w.u.s, key) : -1;
+            const int pg = (of_sets(kMask) ? w.sees_some(key, 1) : key >= first && key < end) ? find_page(a.kv, w.u.s, key) : -1;
             return pg < 0 ? 0 : a.kv.pos[(int64_t)pg * a.kv.page_size + key % a.kv.page_size];
         };
         auto fetch_pos = [&](int t) {
@@ -896,12 +908,12 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                 if (a.slopes && t < n) {
                     if (!kSplit || e == 0) kp = position(w.key0(t) + tid);
                     // (a set's positions are relative to its first query: a step's first slot may be in no row's set)
-                    kp0 = kMask == kSet ? a.q_pos[w.u.tok0] : position(max(w.key0(t), first));
+                    kp0 = of_sets(kMask) ? a.q_pos[w.u.tok0] : position(max(w.key0(t), first));
                 }
             }
         };
-        fetch_pos(t_first);
-        for (int t = t_first; t < n; t += every) {
+        fetch_pos(0);
+        for (int t = 0; t < n; ++t) {
             const int buf = use.buf(t, et, used), k0 = w.key0(t);
             float at = 0.f;  // this row's position relative to the step's first seen key
             const float *sp = s_pos + (2 * et + (pos_steps & 1)) * 128;
@@ -919,7 +931,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                     __syncwarp();
                     if (!__all_sync(0xffffffffu, ok)) return;
                     ++pos_steps;
-                    fetch_pos(t + every);
+                    fetch_pos(t + 1);
                 }
             }
             {
@@ -934,20 +946,20 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             for (int c = 0; c < kCh; ++c) tmem_ld32(sb + 32 * (ch0 + c), v[c]);
 #pragma unroll
             for (int c = 0; c < kCh; ++c) tmem_wait_ld_dep(v[c]);
-            uint32_t seen[kCh];  // kSet: a bit for each of the row's logits
+            uint32_t seen[kCh];  // of sets: a bit for each of the row's logits
             bool part = false;
-            if constexpr (kMask == kSet) {
+            if constexpr (of_sets(kMask)) {
                 part = !__all_sync(0xffffffffu, row.all(k0));
                 if (part) {
 #pragma unroll
-                    for (int c = 0; c < kCh; ++c) seen[c] = row.word(k0 + 32 * (ch0 + c));
+                    for (int c = 0; c < kCh; ++c) seen[c] = row.word(p, k0 + 32 * (ch0 + c));
                 }
             }
             if constexpr (kMore) {
                 if (a.softcap > 0.f) {
                     // Only logits that count choose the form, so that the others' cannot change
                     // a bit: unseen ones are zeros for it, and rows nobody reads have no say.
-                    if constexpr (kMask == kSet) {
+                    if constexpr (of_sets(kMask)) {
                         if (part) {
 #pragma unroll
                             for (int c = 0; c < kCh; ++c)
@@ -1004,7 +1016,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                         }
                 }
             }
-            if constexpr (kMask == kSet) {
+            if constexpr (of_sets(kMask)) {
                 if (part) {
 #pragma unroll
                     for (int c = 0; c < kCh; ++c) {
@@ -1058,9 +1070,9 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                 const float f = grew ? exp2f(m - (mt - kLift<kFp16>)) : 1.f;
                 if (grew) m = mt - kLift<kFp16>;
                 l *= f;
-                if (t >= every) {
-                    const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t - every, et, used)]),
-                                              use.par(t - every, used), &sh.abort, a.wait_limit);
+                if (t > 0) {
+                    const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t - 1, et, used)]), use.par(t - 1, used),
+                                              &sh.abort, a.wait_limit);
                     __syncwarp();
                     if (!__all_sync(0xffffffffu, ok)) return;
                     tc_fence_after();
@@ -1117,39 +1129,13 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             unpack2(add2(sum[0], sum[1]), x, y);
             l += x + y;
         }
-        const int t_last = twins ? n - 1 - ((n - 1 - t_first) & 1) : n - 1;  // before t_first: no step
-        if (t_last >= t_first) {
-            const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(t_last, et, used)]), use.par(t_last, used),
+        {
+            const bool ok = mbar_wait(smem_u32(&sh.pdone[used - 1][use.buf(n - 1, et, used)]), use.par(n - 1, used),
                                       &sh.abort, a.wait_limit);
             __syncwarp();
             if (!__all_sync(0xffffffffu, ok)) return;
         }
         tc_fence_after();
-        float f0 = 1.f, f1 = 0.f;  // what the first and the second stream count
-        if constexpr (kTwin) {
-            if (twins) {
-                // the second warpgroup hands its reference and sum over (each warp where it lays out output
-                // rows), then waits until its accumulator has been read
-                float2 *x = reinterpret_cast<float2 *>(s_out + (4 + quarter) * 4096);
-                if (e == 1) {
-                    x[lane] = make_float2(m, l);
-                    tc_fence_before();
-                    if (!meet()) return;
-                    if (!meet()) return;
-                    use.add(n, used);
-                    continue;
-                }
-                tc_fence_before();
-                if (!meet()) return;
-                tc_fence_after();
-                const float2 y = x[lane];
-                const float both = fmaxf(m, y.x), at = both == -INFINITY ? 0.f : both;
-                f0 = exp2f(m - at);
-                f1 = exp2f(y.x - at);
-                m = both;
-                l = fmaf(f0, l, f1 * y.y);
-            }
-        }
         if constexpr (kSplit) {  // the row's sum is both threads'
             float *x = reinterpret_cast<float *>(s_xch);
             x[e * 128 + tid] = l;
@@ -1160,7 +1146,7 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
         const bool whole = w.ta == 0 && w.tb == w.u.tiles;
         const int64_t orow = (int64_t)(w.u.tok0 + tok) * a.Hq + head;
         float *part = p.parts + (int64_t)(2 * blockIdx.x + (w.index ? 1 : 0)) * C::kUnitRows * (D + 4);
-        const int prow = rt * kRows + tid;
+        const int prow = et * kRows + tid;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (valid && (!kSplit || e == 0)) {
             if (!whole) {
@@ -1180,27 +1166,6 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             tmem_ld32(ocol + c + 32, o[1]);
             tmem_wait_ld_dep(o[0]);
             tmem_wait_ld_dep(o[1]);
-            if constexpr (kTwin) {
-                if (twins) {
-                    // (of a piece of one step one accumulator holds nothing of it)
-                    const bool some0 = t_last >= t_first, some1 = n > 1 || !some0;
-                    if (some1) {
-                        float o1[2][32];
-                        tmem_ld32(ocol + D + c, o1[0]);
-                        tmem_ld32(ocol + D + c + 32, o1[1]);
-                        tmem_wait_ld_dep(o1[0]);
-                        tmem_wait_ld_dep(o1[1]);
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) {
-                            const float first = some0 ? f0 * o[i >> 5][i & 31] : 0.f;
-                            o[i >> 5][i & 31] = fmaf(f1, o1[i >> 5][i & 31], first);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) o[i >> 5][i & 31] *= f0;
-                    }
-                }
-            }
             if (whole) {
                 uint4 pc[8];
 #pragma unroll
@@ -1266,9 +1231,6 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             }
         }
         tc_fence_before();  // the reads end before the next piece's first product is let in
-        if constexpr (kTwin) {
-            if (twins && !meet()) return;
-        }
         use.add(n, used);
     }
 }

@@ -105,8 +105,10 @@ size_t attend_workspace(int64_t T, int num_seqs, int Hq, int Hk, int d);
 size_t decode_workspace(int num_seqs, int Hq, int Hk, int d);
 size_t attend_tree_workspace(int64_t T, int num_seqs, int Hq, int Hk, int d);
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
-// with a.sinks and a.visible, or with a.parents
-cudaError_t launch_attend_set(const AttendArgs &a, int num_sms, cudaStream_t st);
+// with a.visible and a.sinks
+cudaError_t launch_attend_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);
+// with a.parents
+cudaError_t launch_attend_tree(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_decode(const AttendArgs &a, int num_sms, cudaStream_t st);
 
 }  // namespace up
