@@ -79,8 +79,8 @@ bool overlap(const int32_t *a, int64_t na, const int32_t *b, int64_t nb) {
     return x < y + 4 * (uint64_t)nb && y < x + 4 * (uint64_t)na;
 }
 
-// the tiles of a compaction (64 rows and more each, of every head's keys and values) have 32-bit numbers
-bool few_tiles(int64_t T, int num_seqs, int Hk) { return (T / 64 + num_seqs) * 2 * Hk <= INT32_MAX; }
+// the tiles of a compaction (32 rows and more each, of every head's keys and values) have 32-bit numbers
+bool few_tiles(int64_t T, int num_seqs, int Hk) { return (T / 32 + num_seqs) * 2 * Hk <= INT32_MAX; }
 
 up_status check_sinks(int sinks) {
     return sinks < 0 ? UP_ERR_INVALID_ARG : sinks > UP_SINKS_MAX ? UP_ERR_UNSUPPORTED : UP_OK;

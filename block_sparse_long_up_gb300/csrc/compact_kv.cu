@@ -23,7 +23,7 @@ namespace {
 
 using namespace books;
 
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128, kMovePerSm = 8;
 constexpr int kInFlight = 8;  // 16-byte pieces a thread holds of a tile
 constexpr int kTileBytes = kMoveThreads * kInFlight * 16;
 
@@ -151,24 +151,22 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) kv_plan
     const int w = cluster_warp();
     const int from = (int)((int64_t)T * w / kAllWarps), to = (int)((int64_t)T * (w + 1) / kAllWarps);
     const int s_first = last_of(B, [&](int s) { return a.cu_seqlens[s] <= from; });  // of token `from`
-    // f(token, sequence, its first token and end, whether it is kept, the ballot of that) for the run's tokens
-    auto each = [&](auto &&f) {
-        auto block_of = [&](int i) { return p.g_log2 >= 0 ? i >> p.g_log2 : i / a.G; };
+    // The warp's tokens in groups: kept, a bit of 32 tokens for each step of a group, one(s, r, g0, kept) for a
+    // group of one sequence's, some(t, s, r, kept) for the 32 of any.
+    auto block_of = [&](int i) { return p.g_log2 >= 0 ? i >> p.g_log2 : i / a.G; };
+    auto each = [&](auto &&one, auto &&some) {
         int s = s_first;
         Region r = from < to ? region_of(a, s, false) : Region{-1, 0, 0};
         for (int g0 = from; g0 < to; g0 += 32 * kAhead) {
-            if (g0 + 32 * kAhead <= r.end || (to <= r.end)) {
-                // one sequence's: the loads do not wait for one another
+            if (min(g0 + 32 * kAhead, to) <= r.end) {
                 const int c0 = a.cu_seqlens[s];
                 uint32_t kept = 0;
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
+                for (int k = 0; k < kAhead; ++k) {  // the loads do not wait for one another
                     const int t = g0 + 32 * k + lane;
                     if (t < to && r.base >= 0 && a.keep[r.flags + block_of(t - c0)]) kept |= 1u << k;
                 }
-#pragma unroll 1
-                for (int k = 0; k < kAhead && g0 + 32 * k < to; ++k)
-                    f(g0 + 32 * k + lane, s, c0, r.end, kept >> k & 1u, __ballot_sync(0xffffffffu, kept >> k & 1u));
+                one(s, c0, r.end, g0, kept);
                 continue;
             }
 #pragma unroll 1
@@ -182,7 +180,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) kv_plan
                     }
                     kept = r.base >= 0 && a.keep[r.flags + block_of(t - a.cu_seqlens[s])];
                 }
-                f(t, s, a.cu_seqlens[s], r.end, kept, __ballot_sync(0xffffffffu, kept));
+                some(t, s, r.end, kept);
             }
             // the lanes go on from the last one's sequence
             s = __reduce_max_sync(0xffffffffu, s);
@@ -190,25 +188,50 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) kv_plan
         }
     };
     int mine = 0;
-    each([&](int, int, int, int, bool, unsigned m) { mine += __popc(m); });
+    each([&](int, int, int, int, uint32_t kept) { mine += __reduce_add_sync(0xffffffffu, __popc(kept)); },
+         [&](int, int, int, bool kept) { mine += __popc(__ballot_sync(0xffffffffu, kept)); });
     int total, rank = before_warp(mine, &total);
     int told = -1;  // the sequence whose first dropped token this warp has told of
-    each([&](int t, int s, int c0, int end, bool kept, unsigned m) {
-        // sequences rise over the lanes: of each, the first dropped token (a lane each, and 8192 of them
-        // on one address, took 15 us of 131072 tokens' 27)
-        const unsigned gone = __ballot_sync(0xffffffffu, t < to && !kept), below = gone & ((1u << lane) - 1u);
-        const int before = __shfl_sync(0xffffffffu, s, below ? 31 - __clz(below) : 0);
-        if (t < to && !kept && s != (below ? before : told)) atomicMin(&p.seqs[s].stay, t - c0);
-        if (gone) told = __shfl_sync(0xffffffffu, s, 31 - __clz(gone));
-        if (t < to) {
-            const int r = rank + __popc(m & ((1u << lane) - 1u)), i = t - c0;
-            if (i == 0) p.seqs[s].at = r;
-            if (t + 1 == end) p.seqs[s].kept = r + kept;  // `at` comes off below
-            if ((i & (p.R - 1)) == 0) p.edges[(c0 >> p.r_log2) + s + (i >> p.r_log2)] = r;  // (see edges_of) of all; the sequence's share comes off later
-            if (kept) p.list[r] = i;
-        }
-        rank += __popc(m);
-    });
+    each(
+        [&](int s, int c0, int end, int g0, uint32_t kept) {
+            const int n = min(32 * kAhead, to - g0), e0 = (c0 >> p.r_log2) + s;  // (see edges_of)
+            const uint32_t there = lane < n ? (2u << ((n - 1 - lane) >> 5)) - 1u : 0u, gone = there & ~kept;
+            // (a lane each, and 8192 of them on one address, took 15 us of 131072 tokens' 27)
+            const int first = __reduce_min_sync(0xffffffffu, gone ? 32 * (__ffs(gone) - 1) + lane : INT32_MAX);
+            if (first != INT32_MAX && told != s) {
+                if (lane == 0) atomicMin(&p.seqs[s].stay, g0 + first - c0);
+                told = s;
+            }
+            if (lane == 0 && g0 == c0) p.seqs[s].at = rank;
+#pragma unroll 4
+            for (int k = 0; k < kAhead; ++k) {
+                if (32 * k >= n) break;
+                const bool keep = kept >> k & 1u;
+                const unsigned m = __ballot_sync(0xffffffffu, keep);
+                const int r = rank + __popc(m & ((1u << lane) - 1u)), i = g0 + 32 * k + lane - c0;
+                if (keep) p.list[r] = i;
+                // of all kept tokens; the sequence's share comes off later
+                if ((i & (p.R - 1)) == 0 && there >> k & 1u) p.edges[e0 + (i >> p.r_log2)] = r;
+                rank += __popc(m);
+            }
+            if (lane == 0 && g0 + n == end) p.seqs[s].kept = rank;  // `at` comes off below
+        },
+        [&](int t, int s, int end, bool kept) {
+            const unsigned m = __ballot_sync(0xffffffffu, kept);
+            // sequences rise over the lanes: of each, the first dropped token
+            const unsigned gone = __ballot_sync(0xffffffffu, t < to && !kept), below = gone & ((1u << lane) - 1u);
+            const int before = __shfl_sync(0xffffffffu, s, below ? 31 - __clz(below) : 0);
+            if (t < to) {
+                const int r = rank + __popc(m & ((1u << lane) - 1u)), c0 = a.cu_seqlens[s], i = t - c0;
+                if (!kept && s != (below ? before : told)) atomicMin(&p.seqs[s].stay, i);
+                if (i == 0) p.seqs[s].at = r;
+                if (t + 1 == end) p.seqs[s].kept = r + kept;
+                if ((i & (p.R - 1)) == 0) p.edges[(c0 >> p.r_log2) + s + (i >> p.r_log2)] = r;
+                if (kept) p.list[r] = i;
+            }
+            if (gone) told = __shfl_sync(0xffffffffu, s, 31 - __clz(gone));
+            rank += __popc(m);
+        });
     meet();
     if (blockIdx.x) return;
     // kept tokens of every sequence, and the tickets' numbers (many sequences in rounds)
@@ -305,7 +328,7 @@ __device__ Ticket describe(const Params &p, int number, int all, int *list_at, i
 // next and all look up the next one's rows (each a chain of loads as long as the rows' own: 131072
 // tokens of which a quarter stay take 54 us, 3.3 + 3.3 TB/s less what the cache keeps; 62 with one ticket looked up whole).  It tells that
 // its rows are there, waits for whoever still has to read the slots that they go to, and writes them.
-__global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const Params p) {
+__global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const Params p) {
     constexpr int kMaxRows = tile_rows(64);
     static_assert(kMaxRows <= kMoveThreads, "a thread a row");
     __shared__ int64_t s_src[3][kMaxRows], s_dst[3][kMaxRows];
@@ -426,13 +449,12 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_move_kernel(const Params p
 // 6-9 us (by tickets 22-23), 256 of 64 14-21 (23-50), one of 256 4-10 (17); but 16384 tokens 142-519 (23-46)
 // where all are one sequence's, and 4096 38-122 (20-24).  Which it is the host does not know: up to 1024
 // tokens times the root of the number of sequences.
-constexpr int kRun = 256;
-static_assert(kRun == kMoveThreads, "a thread a flag");
+constexpr int kFewThreads = 256, kRun = kFewThreads;  // a thread a flag
 bool few_tokens(int64_t T, int64_t num_seqs) { return T * T <= num_seqs << 20; }
 
-__global__ void __launch_bounds__(kMoveThreads) kv_few_kernel(const Params p) {
+__global__ void __launch_bounds__(kFewThreads) kv_few_kernel(const Params p) {
     __shared__ int64_t s_src[kRun], s_dst[kRun];
-    __shared__ int s_warp[kMoveThreads / 32], s_bad;
+    __shared__ int s_warp[kFewThreads / 32], s_bad;
     const KvCompactArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int j = blockIdx.x % a.kv.Hk, s = blockIdx.x / a.kv.Hk, Hk = a.kv.Hk, ps = a.kv.page_size, d2 = a.kv.d * 2;
@@ -441,7 +463,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_few_kernel(const Params p) {
     pdl_wait();
     __syncthreads();
     // a malformed cu_seqlens is one for all sequences
-    for (int x = tid; x < a.kv.num_seqs; x += kMoveThreads) {
+    for (int x = tid; x < a.kv.num_seqs; x += kFewThreads) {
         const int c0 = a.cu_seqlens[x], c1 = a.cu_seqlens[x + 1];
         if (c0 < 0 || c1 < c0 || c1 > a.T || (x == 0 && c0 != 0)) s_bad = 1;
     }
@@ -466,7 +488,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_few_kernel(const Params p) {
         __syncthreads();
         int before = 0, rows = 0;
 #pragma unroll
-        for (int w = 0; w < kMoveThreads / 32; ++w) {
+        for (int w = 0; w < kFewThreads / 32; ++w) {
             if (w == warp) before = rows;
             rows += s_warp[w];
         }
@@ -482,7 +504,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_few_kernel(const Params p) {
         const int pieces = rows << shift;  // of the keys; the values' follow
         // kept tokens of this run go to slots of this run and of those before: read in order, they can be
         // written in order
-        for (int x0 = 0; x0 < 2 * pieces; x0 += kInFlight * kMoveThreads) {
+        for (int x0 = 0; x0 < 2 * pieces; x0 += kInFlight * kFewThreads) {
             uint4 v[kInFlight];
             auto at = [&](int x, const int64_t *row) {
                 const bool value = x >= pieces;
@@ -492,13 +514,13 @@ __global__ void __launch_bounds__(kMoveThreads) kv_few_kernel(const Params p) {
             auto moves = [&](int x) { return x < 2 * pieces && s_src[(x >= pieces ? x - pieces : x) >> shift] >= 0; };
 #pragma unroll
             for (int k = 0; k < kInFlight; ++k) {
-                const int x = x0 + tid + k * kMoveThreads;
+                const int x = x0 + tid + k * kFewThreads;
                 if (moves(x)) v[k] = *reinterpret_cast<const uint4 *>(at(x, s_src));
             }
             __syncthreads();
 #pragma unroll
             for (int k = 0; k < kInFlight; ++k) {
-                const int x = x0 + tid + k * kMoveThreads;
+                const int x = x0 + tid + k * kFewThreads;
                 if (moves(x)) *reinterpret_cast<uint4 *>(at(x, s_dst)) = v[k];
             }
             __syncthreads();
@@ -538,11 +560,11 @@ cudaError_t launch_kv_compact(const KvCompactArgs &a, int num_sms, cudaStream_t 
     const int32_t *lens = a.kv.kv_lens;
     const bool apart = a.lens_out + a.kv.num_seqs <= lens || lens + a.kv.num_seqs <= a.lens_out;
     if (apart && few_tokens(a.T, a.kv.num_seqs) && (int64_t)a.kv.num_seqs * a.kv.Hk <= INT32_MAX)
-        return launch_pdl(kv_few_kernel, dim3((unsigned)a.kv.num_seqs * (unsigned)a.kv.Hk), dim3(kMoveThreads), 0, st, p);
+        return launch_pdl(kv_few_kernel, dim3((unsigned)a.kv.num_seqs * (unsigned)a.kv.Hk), dim3(kFewThreads), 0, st, p);
     cudaError_t e = launch_pdl(kv_plan_kernel, dim3(kBlocks), dim3(kThreads), 0, st, p);
     if (e != cudaSuccess) return e;
     const int64_t most = ((int64_t)a.T / p.R + a.kv.num_seqs) * 2 * a.kv.Hk;
-    const int64_t grid = most < (int64_t)num_sms * 4 ? most : (int64_t)num_sms * 4;
+    const int64_t grid = most < (int64_t)num_sms * kMovePerSm ? most : (int64_t)num_sms * kMovePerSm;
     return launch_pdl(kv_move_kernel, dim3((unsigned)grid), dim3(kMoveThreads), 0, st, p);
 }
 
