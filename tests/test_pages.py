@@ -601,3 +601,141 @@ def test_expired_wait_stops_the_move():
     up.compact_kv(m.cache, m.cu, keep)
     assert up.get_device_error() == 0
     assert equal(m.kp, want[0]) and equal(m.vp, want[1]) and equal(m.pp, want[2])
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,Hq,Hk,dtype", [(64, 8, 2, "bf16"), (128, 12, 4, "fp16"), (256, 16, 2, "bf16")])
+def test_a_tree_is_verified_accepted_and_cut_back(d, Hq, Hk, dtype):
+    """A forked sequence drafts a tree, keeps one path and lets the rest go: its cache then holds what
+    appending the path's tokens one by one leaves, and a decode step over it gives the same."""
+    ps, B, n = 16, 3, 9
+    parents = [-1, 0, 0, 1, 1, 2, 3, 6, 4]
+    path = [0, 1, 3, 6, 7]
+    depth = [0, 1, 1, 2, 2, 2, 3, 4, 3]
+    lens = [37, 16, 95]
+    g = torch.Generator(device="cuda").manual_seed(d)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float16
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(dt)
+
+    pool, width = up.PagePool.full(60), 8
+    kp, vp = normal(60, Hk, ps, d), normal(60, Hk, ps, d)
+    pp = torch.zeros(60, ps, dtype=torch.int32, device="cuda")
+    freq = 10000.0 ** -(torch.arange(0, d, 2, device="cuda") / d)
+    cu0 = ints([0, 37, 53, 148])
+    x = [normal(148, h, d) for h in (Hq, Hk, Hk)]
+    table, kv = ints([[-1] * width] * B), ints(lens)
+    up.reserve_pages(pool, table, ps, ints([0] * B), kv)
+    pos = torch.cat([torch.arange(m, device="cuda") for m in lens]).to(torch.int32)
+    up.append_kv(None, x[1], x[2], pos, cu0, up.PagedKV(kp, vp, table, kv, pp), freq)
+    # two continuations of the same prompts: one drafts, the other gets the path's tokens one at a time
+    both, l2, copies = up.fork_pages(pool, table, kv, ps, ints([0, 1, 2, 0, 1, 2]))
+    up.copy_pages(up.PagedKV(kp, vp, both, l2, pp), copies)
+    up.release_pages(pool, table, ps, None, kv)
+    tree, line = both[:B].contiguous(), both[B:].contiguous()
+    tl, ll = l2[:B].clone(), l2[B:].clone()
+    q, k, v = (normal(B * n, h, d) for h in (Hq, Hk, Hk))
+    old = tl.clone()
+    up.reserve_pages(pool, tree, ps, old, old + n)
+    tl += n
+    cache = up.PagedKV(kp, vp, tree, tl, pp)
+    cu = ints([0, n, 2 * n, 3 * n])
+    tpos = (old[:, None] + ints(depth)[None]).flatten().contiguous()
+    qr = up.append_kv(q, k, v, tpos, cu, cache, freq)
+    out, lse = up.attend_tree(qr, cu, ints(parents * B), cache)
+    flags = torch.zeros(B, n, dtype=torch.uint8, device="cuda")
+    flags[:, path] = 1
+    new = up.compact_kv(cache, cu, flags.view(-1))
+    up.release_pages(pool, tree, ps, new, tl)
+    assert torch.equal(new, old + len(path))
+    tl.copy_(new)
+    one = ints([0, 1, 2, 3])
+    for j in path:
+        up.reserve_pages(pool, line, ps, ll, ll + 1)
+        ll += 1
+        at = torch.arange(B, device="cuda") * n + j
+        c = up.PagedKV(kp, vp, line, ll, pp)
+        qj = up.append_kv(q[at], k[at], v[at], (ll - 1), one, c, freq)
+        o, l = up.decode_attend(qj, c)
+        # (each rounds its weights its own way: a step of the type on values of a few units)
+        assert float((o.float() - out[at].float()).abs().max()) <= 2.0 ** (-5 if dtype == "bf16" else -8)
+        assert torch.allclose(l, lse[at], atol=1e-4)
+    assert torch.equal(tl, ll)
+    for s in range(B):
+        i = torch.arange(int(ll[s]), device="cuda")
+        for y in (kp, vp):
+            assert equal(y[tree[s].long()[i // ps], :, i % ps], y[line[s].long()[i // ps], :, i % ps])
+        assert torch.equal(pp[tree[s].long()[i // ps], i % ps], pp[line[s].long()[i // ps], i % ps])
+    a = up.decode_attend(qr[:B].contiguous(), cache)
+    b = up.decode_attend(qr[:B].contiguous(), up.PagedKV(kp, vp, line, ll, pp))
+    assert all(torch.equal(u, w) for u, w in zip(a, b))
+    for t, m in ((tree, tl), (line, ll)):
+        up.release_pages(pool, t, ps, None, m)
+    assert int(pool.num_free) == 60 and not pool.refs.any() and up.get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_pages_between_first_tokens_and_window_are_released():
+    """A decode loop with a sliding window: the pages that fall behind it go back to the pool, and
+    what is seen does not change."""
+    ps, sinks, span, Hq, Hk, d = 16, 5, 70, 8, 2, 64
+    pool, g = up.PagePool.full(16), torch.Generator(device="cuda").manual_seed(1)
+    full = up.PagePool.full(64)
+
+    def store(n):
+        return (torch.zeros(n, Hk, ps, d, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(n, Hk, ps, d, dtype=torch.bfloat16, device="cuda"))
+
+    lens = ints([0, 0])
+    few, all_ = ints([[-1] * 32] * 2), ints([[-1] * 32] * 2)
+    small = up.PagedKV(*store(16), few, lens)
+    large = up.PagedKV(*store(64), all_, lens)
+    one = ints([0, 1, 2])
+    for t in range(300):
+        old = lens.clone()
+        for p, table in ((pool, few), (full, all_)):
+            up.reserve_pages(p, table, ps, old, old + 1)
+        lens += 1
+        q, k, v = (torch.randn(2, h, d, generator=g, device="cuda").bfloat16() for h in (Hq, Hk, Hk))
+        start = (lens - span).contiguous()
+        up.release_pages(pool, few, ps, torch.full_like(start, sinks), start - (ps - 1))
+        res = []
+        for c in (small, large):
+            up.append_kv(None, k, v, old, one, c, None)
+            res.append(up.decode_attend(q, c, kv_start=start, sinks=sinks))
+        assert all(torch.equal(x, y) for x, y in zip(*res)), t
+        assert int((few >= 0).sum()) <= 2 * (2 + span // ps + 1)
+    assert up.get_device_error() == 0 and int(pool.num_free) == 16 - int((few >= 0).sum())
+
+
+@pytest.mark.gpu
+def test_blocks_that_the_selection_keeps_stay_in_the_cache():
+    """score -> select -> compact_kv: a prompt's cache keeps the selected blocks, in place."""
+    lens = [(700, 700), (3000, 3000)]
+    m = Made(lens, 2, 64, 128, "bf16", seed=3)
+    q = m.normal(256, 8, 64)
+    scores, cb = up.score_blocks_paged(q, m.kp.nan_to_num_(0.0), m.table, m.cu, 3700, 128, 64)
+    keep, kept = up.select_topp(scores, cb, m.cu, 64, 0.5)
+    nb = [-(-n // 64) for n, _ in lens]
+    flags = [keep[int(cb[s]):int(cb[s]) + nb[s]].bool().cpu() for s in range(2)]
+    k, v, p, new = compacted(m, flags, 64)
+    out = up.compact_kv(m.cache, m.cu, keep, cu_blocks=cb, G=64)
+    assert up.get_device_error() == 0
+    assert out.tolist() == new == kept.tolist()
+    assert equal(m.kp, k) and equal(m.vp, v) and equal(m.pp, p)
+
+
+@pytest.mark.gpu
+def test_example_decodes_trees():
+    """Twice the same tokens, at least one a step, and no page lost (the example checks that)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "tree_decode.py")
+    spec = importlib.util.spec_from_file_location("tree_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    a, b = (ex.main(["--prompt", "200", "77", "--children", "3", "--steps", "5"]) for _ in range(2))
+    assert a == b and len(a) == 6 and all(len(t) >= 6 for t in a)
