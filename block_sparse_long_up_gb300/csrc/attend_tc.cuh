@@ -308,13 +308,10 @@ struct Pieces {
     int after = -1;      // the index of `behind`
     int ta, tb;          // tiles [ta, tb) of the unit
     int64_t index = -1;  // pieces so far, less one
-    // Of sets: the windows' first slot and their end, the end of the first slots that stay
-    // visible and their tiles; the windows' tiles lie `shift` tiles on.  Of the sequence's tokens
-    // together: their windows' first slot and end, the first slots' end, and whether the
-    // windows leave gaps
-    int wfirst, wend, send, stiles, shift;
+    // Of sets, of the sequence's tokens together: their windows' first slot and end, the first slots' end,
+    // and whether the windows leave gaps (of a tree only the first is asked for)
     int4 all;
-    int turned;  // steps that the piece's last tiles come before its first ones (see next)
+    int turned;  // steps that a tree's last tiles of the piece come before its first ones (see next)
 
     __device__ explicit Pieces(const Params &pp) : p(pp) {
         const Plan pl = *pp.plan;
@@ -347,21 +344,15 @@ struct Pieces {
             at = min(end, first + u.tiles);
             if (ta >= tb) continue;  // the share ends before the unit's first tile
             ++index;
-            if constexpr (of_sets(kMask)) {
-                wfirst = u.kt0 < 0 ? ~u.kt0 : u.kt0;
-                wend = (int)u.edges;
-                send = kMask == kTree ? min(p.a.sinks, u.hi0) : u.hi0;
-                stiles = (send + kRows - 1) / kRows;
-                shift = max(wfirst / kRows - stiles, 0);
-                all = __ldg(p.seen + u.s);
-            }
+            if constexpr (kMask == kSinks) all = __ldg(p.seen + u.s);
             if constexpr (kMask == kTree) {
                 // Where a share is a part of one unit, its tiles come in the order of their remainders by
                 // the share's length: the blocks that work on the units of a sequence's tree, whose shares begin
                 // anywhere, then read the same keys at the same time, once from memory.  (32 trees of up to 61
                 // tokens at head_dim 256, 4 units each: XX us and XX of 0.55 GB read, against 184 and 1.11.)
-                const int len = (int)(sh.W / sh.n), k = ta < stiles ? ta : ta + shift;
+                const int len = (int)(sh.W / sh.n), k = tile_of(ta);
                 turned = !p.a.slopes && tb - ta >= len ? (len - k % len) % len : 0;
+                all.x = p.a.kv_start ? __ldg(&p.seen[u.s].x) : 0;
             }
             // the next unit's description, on its way while this one is worked on
             after = ui + 1 < n ? ui + 1 : 0;
@@ -381,17 +372,26 @@ struct Pieces {
             i += turned;
             if (i >= tb) i -= tb - ta;
         }
-        if constexpr (of_sets(kMask)) return (i < stiles ? i : i + shift) * kRows;
+        if constexpr (of_sets(kMask)) return tile_of(i) * kRows;
         return (u.kt0 + i) * kRows;
     }
-    // Of a unit of sets whose windows leave no gaps:
+    // Of a unit of sets: the windows' first slot and their end, the end of the first slots that stay visible,
+    // and the i-th of its tiles -- those of the first slots, then those of the windows behind them.
+    __device__ int wfirst() const { return kMask == kSinks && u.kt0 < 0 ? ~u.kt0 : u.kt0; }
+    __device__ int wend() const { return (int)u.edges; }
+    __device__ int send() const { return kMask == kTree ? min(p.a.sinks, u.hi0) : u.hi0; }
+    __device__ int tile_of(int i) const {
+        const int st = (send() + kRows - 1) / kRows;
+        return i < st ? i : i + max(wfirst() / kRows - st, 0);
+    }
+    // Where the windows leave no gaps:
     __device__ bool sees_some(int key, int box) const {  // of the box's slots
-        return key < send || (key < wend && key > wfirst - box);
+        return key < send() || (key < wend() && key > wfirst() - box);
     }
     __device__ bool sees_all(int key) const {  // of the 128 slots at key, without asking for words
-        return (key >= wfirst && key + kRows <= (kMask == kTree ? u.hi0 : wend)) || key + kRows <= send;
+        return (key >= wfirst() && key + kRows <= (kMask == kTree ? u.hi0 : wend())) || key + kRows <= send();
     }
-    __device__ bool gaps() const { return u.kt0 < 0; }
+    __device__ bool gaps() const { return kMask == kSinks && u.kt0 < 0; }
 };
 
 // ---------------------------------------------------------------- shared state
@@ -519,7 +519,7 @@ __device__ void role_kv(const CUtensorMap *km, const CUtensorMap *vm, const Para
             bool some = t < n && r < kRows;
             if constexpr (of_sets(kMask)) some = some && w.sees_some(key, p.box);
             else some = some && key < end && key > from;
-            if constexpr (kMask != kRanges) {
+            if constexpr (kMask != kRanges && kMask != kTree) {
                 if ((of_sets(kMask) ? w.gaps() : w.u.gaps()) && t < n) {  // boxes in a gap are not looked up
                     uint32_t box = 0;
 #pragma unroll 1
@@ -700,17 +700,18 @@ __device__ void role_mma(const Params &p, Shared &sh, uint32_t q, uint32_t ring,
             if (!wait_stage(i + part)) return false;
         const int key0 = w.key0(t);
         if constexpr (of_sets(kMask)) {
-            if (!w.all.w) {
+            if (kMask == kTree || !w.all.w) {
                 // what no token of the sequence sees: between the first slots and the windows, and behind these
-                const int from = max(w.all.z - key0, 0), to = min(w.all.x - key0, kRows);
-                const int end = max(max(w.all.y, w.all.z) - key0, 0);
+                const int some = kMask == kTree ? w.send() : w.all.z;
+                const int from = max(some - key0, 0), to = min(w.all.x - key0, kRows);
+                const int end = max((kMask == kTree ? w.wend() : max(w.all.y, some)) - key0, 0);
                 if (from >= to && end >= kRows) return true;
                 for (int part = 0; part < C::kParts; ++part)
                     clear_rows<D>(ring + ((i + part) % C::kStages) * C::kStageBytes, from, min(to, end), end);
                 return true;
             }
         }
-        if constexpr (kMask != kRanges) {
+        if constexpr (kMask != kRanges && kMask != kTree) {
             // all that the unit's own rows do not see
             if (of_sets(kMask) ? !w.gaps() && w.sees_all(key0)
                               : !w.u.gaps() && key0 != w.u.kt0 * kRows && key0 != w.u.last_tile())
@@ -946,15 +947,8 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
             for (int c = 0; c < kCh; ++c) tmem_ld32(sb + 32 * (ch0 + c), v[c]);
 #pragma unroll
             for (int c = 0; c < kCh; ++c) tmem_wait_ld_dep(v[c]);
-            uint32_t seen[kCh];  // of sets: a bit for each of the row's logits
-            bool part = false;
-            if constexpr (of_sets(kMask)) {
-                part = !__all_sync(0xffffffffu, row.all(k0));
-                if (part) {
-#pragma unroll
-                    for (int c = 0; c < kCh; ++c) seen[c] = row.word(p, k0 + 32 * (ch0 + c));
-                }
-            }
+            bool part = false;  // of sets: some row does not see all of the tile
+            if constexpr (of_sets(kMask)) part = !__all_sync(0xffffffffu, row.all(k0));
             if constexpr (kMore) {
                 if (a.softcap > 0.f) {
                     // Only logits that count choose the form, so that the others' cannot change
@@ -962,10 +956,12 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                     if constexpr (of_sets(kMask)) {
                         if (part) {
 #pragma unroll
-                            for (int c = 0; c < kCh; ++c)
+                            for (int c = 0; c < kCh; ++c) {
+                                const uint32_t seen = row.word(p, k0 + 32 * (ch0 + c));
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    if (!(seen[c] >> i & 1u)) v[c][i] = 0.f;
+                                    if (!(seen >> i & 1u)) v[c][i] = 0.f;
+                            }
                         }
                     } else if (!__all_sync(0xffffffffu, vis.x <= k0 && vis.y >= k0 + kRows)) {
 #pragma unroll
@@ -1020,10 +1016,11 @@ __device__ void role_softmax(const Params &p, Shared &sh, uint8_t *s_out, float 
                 if (part) {
 #pragma unroll
                     for (int c = 0; c < kCh; ++c) {
-                        if (__all_sync(0xffffffffu, seen[c] == 0xffffffffu)) continue;
+                        const uint32_t seen = row.word(p, k0 + 32 * (ch0 + c));
+                        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!(seen[c] >> i & 1u)) v[c][i] = -INFINITY;
+                            if (!(seen >> i & 1u)) v[c][i] = -INFINITY;
                     }
                 }
             } else if (!__all_sync(0xffffffffu, vis.x <= k0 && vis.y >= k0 + kRows)) {
@@ -1441,11 +1438,12 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attend_join_kernel(const Para
     if (m >> lane & 1u) s_cut[before + __popc(m & ((1u << lane) - 1u))] = tid;
     __syncthreads();
     const bool split = cuts * kRowGroups * (D / 32) <= (int)gridDim.x;
-    const int pieces = kRowGroups * (split ? D / 32 : 1);
+    constexpr int kWide = D < 128 ? D / 32 : 4;  // fours of columns a warp
+    const int pieces = kRowGroups * (split ? D / 32 : D / 32 / kWide);
     for (int x = blockIdx.x; x < cuts * pieces; x += gridDim.x) {
         const int c0 = s_cut[x / pieces], y = x % pieces, rows0 = y % kRowGroups * kJoinRows;
         if (split) join_piece<kFp16, D, 1>(p, pl, sh, c0, rows0, y / kRowGroups * 32);
-        else join_piece<kFp16, D, D / 32>(p, pl, sh, c0, rows0, 0);
+        else join_piece<kFp16, D, kWide>(p, pl, sh, c0, rows0, y / kRowGroups * 32 * kWide);
     }
 }
 
