@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_set_plan_kernel(const Par
         for (int64_t i = tid; i < units; i += kPlanThreads) p.units[i] = unit_at(i);
     } else {
         // A warp takes four units at once, a lane each to begin with, then its lanes at their tokens (one at a
-        // time 250 units took 14 us; XX so).
+        // time 250 units took 14 us; 10 so).
         constexpr int kSame = 4;
         for (int64_t i0 = warp * kSame; i0 < units; i0 += kPlanThreads / 32 * kSame) {
             Unit u = unit_at(min(i0 + (lane & (kSame - 1)), units - 1));

@@ -307,11 +307,11 @@ struct Pieces {
     Unit u, behind;
     int after = -1;      // the index of `behind`
     int ta, tb;          // tiles [ta, tb) of the unit
-    int64_t index = -1;  // pieces so far, less one
+    int64_t index = -1;  // pieces so far, less one; of a tree 1 where the unit begins behind the share's first place
     // Of sets, of the sequence's tokens together: their windows' first slot and end, the first slots' end,
     // and whether the windows leave gaps (of a tree only the first is asked for)
     int4 all;
-    int turned;  // steps that a tree's last tiles of the piece come before its first ones (see next)
+    int turned;  // steps that the last tiles of a tree's piece come before its first ones (see next_back)
 
     __device__ explicit Pieces(const Params &pp) : p(pp) {
         const Plan pl = *pp.plan;
@@ -323,12 +323,53 @@ struct Pieces {
         if ((int)blockIdx.x >= sh.n) return;
         at = share_begin(sh, blockIdx.x);
         end = share_begin(sh, blockIdx.x + 1);
-        j = (int)(at / W1);
+        const int64_t from = kMask == kTree ? end - 1 : at;
+        j = (int)(from / W1);
         base = (int64_t)j * W1;
-        ui = find_unit(pp.units, n, at - base);
+        ui = find_unit(pp.units, n, from - base);
         u = pp.units[ui];
     }
+    // A tree's pieces, from the share's end to its beginning; their tiles are placed so that the blocks
+    // that work on the units of a sequence, whose shares begin anywhere, read the same keys at about the
+    // same time, once from memory: tile i is worked on kUnitCost + i steps after the share's
+    // beginning, modulo the share's length, in the first half of a unit, and as far before a share's end as it lies
+    // before the unit's end in the second.  A unit's beginning comes first and its end last, and
+    // a share that is a part of one unit turns its tiles.  (32 trees of up to 61 tokens at head_dim 256, 4 units
+    // each: 151 us and 0.66 of 0.55 GB read; without any of it 184 us and 1.11 GB.)
+    __device__ bool next_back() {
+        while (at < end) {
+            while (base + u.prefix >= end || !u.tiles) {
+                if (ui == 0) {
+                    ui = n;
+                    --j;
+                    base -= W1;
+                }
+                --ui;
+                u = ui == after ? behind : p.units[ui];
+            }
+            const int64_t unit = base + u.prefix, first = unit + kUnitCost;
+            ta = (int)max(at - first, (int64_t)0);
+            tb = (int)min((int64_t)u.tiles, end - first);
+            const bool only = unit <= at && end == share_begin(sh, blockIdx.x + 1);
+            end = unit;
+            if (ta >= tb) continue;  // the share ends before the unit's first tile
+            index = unit > at;
+            turned = 0;
+            if (only && ta > 0 && !p.a.slopes) {
+                const int len = (int)(sh.W / sh.n);
+                const int slot = (ta + tb < u.tiles ? ta + kUnitCost : (ta - u.tiles) % len + len) % len;
+                turned = (len - slot) % len;
+                if (turned >= tb - ta) turned = 0;
+            }
+            all.x = p.a.kv_start ? __ldg(&p.seen[u.s].x) : 0;
+            after = ui > 0 ? ui - 1 : n - 1;
+            behind = p.units[after];
+            return true;
+        }
+        return false;
+    }
     __device__ bool next() {
+        if constexpr (kMask == kTree) return next_back();
         while (at < end) {
             while (at - base >= u.prefix + width_of(u)) {  // units without tiles, or the last one done
                 if (++ui == n) {
@@ -345,15 +386,6 @@ struct Pieces {
             if (ta >= tb) continue;  // the share ends before the unit's first tile
             ++index;
             if constexpr (kMask == kSinks) all = __ldg(p.seen + u.s);
-            if constexpr (kMask == kTree) {
-                // Where a share is a part of one unit, its tiles come in the order of their remainders by
-                // the share's length: the blocks that work on the units of a sequence's tree, whose shares begin
-                // anywhere, then read the same keys at the same time, once from memory.  (32 trees of up to 61
-                // tokens at head_dim 256, 4 units each: XX us and XX of 0.55 GB read, against 184 and 1.11.)
-                const int len = (int)(sh.W / sh.n), k = tile_of(ta);
-                turned = !p.a.slopes && tb - ta >= len ? (len - k % len) % len : 0;
-                all.x = p.a.kv_start ? __ldg(&p.seen[u.s].x) : 0;
-            }
             // the next unit's description, on its way while this one is worked on
             after = ui + 1 < n ? ui + 1 : 0;
             behind = p.units[after];
@@ -559,7 +591,7 @@ __device__ void role_q(const CUtensorMap *qm, const Params &p, Shared &sh, uint3
     Pieces<kMask> w(p);
     Cut cut{0, 0, 0, 0};
     while (w.next()) {
-        cut = Cut{w.ta == 0 && w.tb < w.u.tiles, w.j, w.ui, 0};
+        if (kMask != kTree || n == 0) cut = Cut{w.ta == 0 && w.tb < w.u.tiles, w.j, w.ui, 0};
         ok = mbar_wait(smem_u32(&sh.qempty), (n & 1) ^ 1, &sh.abort, p.a.wait_limit);
         if (!ok) break;
         const int used = C::kTiles == 1 ? 1 : w.tiles_used();
@@ -570,7 +602,7 @@ __device__ void role_q(const CUtensorMap *qm, const Params &p, Shared &sh, uint3
                 tma_load_3d(q + e * C::kQTile + pn * kPanel, qm, pn * 64, w.j * p.a.g, w.u.tok0 + e * p.tpt, bar);
         ++n;
     }
-    p.cuts[blockIdx.x] = cut;  // of the last piece
+    p.cuts[blockIdx.x] = cut;  // of the piece at the share's end
     if (*(volatile int *)&sh.abort && n) drain(smem_u32(&sh.qfull), (n - 1) & 1);
 }
 
@@ -1397,7 +1429,7 @@ __device__ __forceinline__ void join_piece(const Params &p, const Plan &pl, cons
 // Joins the units that a share's end cuts, named by the first share that does, 32 rows at a time, and where
 // there are blocks enough 32 of their columns at a time too.  (A block for each 32 rows of each
 // share, most of them without any, took 8.8 us of a call of 128 tokens over 1K and 19 of 64 drafted ones
-// over 128K, whose 8 units are in 19 parts each; XX and XX so.)  All blocks together also write the rows of the
+// over 128K, whose 8 units are in 19 parts each; 7 and 13 so.)  All blocks together also write the rows of the
 // units without a visible slot, or of all tokens when the batch is malformed.
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kJoinThreads, 3) attend_join_kernel(const Params p) {
