@@ -14,7 +14,11 @@
 // the number of blocks on the GPU.
 //
 // Two launches: a plan (one cluster of blocks: the scan of the flags, which lists the kept slots and
-// ranks the tiles' edges) and the move.
+// ranks the tiles' edges) and the move.  131072 tokens of 8 heads of 128 that keep a quarter of their blocks of
+// 64: 62 us in a graph, of it 51 the move of 134 MB each way at 5.3 TB/s together, where a plain copy would
+// take 40 (latency: a tile's tickets, slots and pages are looked up while the one before it is read, but a block
+// of 16 KB still waits for its loads, its flags and its stores in turn).  Where the sequences have few flagged
+// tokens one launch does both.
 #include "pages.cuh"
 
 namespace up {
@@ -78,7 +82,7 @@ struct Region {
     int base, flags, end;  // base: -1 for a sequence that is left out; end: of its tokens
 };
 __device__ __forceinline__ Region region_of(const KvCompactArgs &a, int s, bool tell) {
-    const int c0 = a.cu_seqlens[s], c1 = a.cu_seqlens[s + 1], n = c1 - c0, nb = (n + a.G - 1) / a.G;
+    const int c0 = a.cu_seqlens[s], c1 = a.cu_seqlens[s + 1], n = c1 - c0, nb = n ? (n - 1) / a.G + 1 : 0;
     const int b0 = a.cu_blocks[s], b1 = a.cu_blocks[s + 1], kv = a.kv.kv_lens[s];
     Region r{kv - n, b0, c1};
     if (tell) kv_len_of(a.kv, s, n);  // (its error bit)
@@ -325,9 +329,10 @@ __device__ Ticket describe(const Params &p, int number, int all, int *list_at, i
 }
 
 // A block reads a tile's rows into registers, and while they come one warp describes the ticket after
-// next and all look up the next one's rows (each a chain of loads as long as the rows' own: 131072
-// tokens of which a quarter stay take 54 us, 3.3 + 3.3 TB/s less what the cache keeps; 62 with one ticket looked up whole).  It tells that
-// its rows are there, waits for whoever still has to read the slots that they go to, and writes them.
+// next and all look up the next one's rows (each a chain of loads as long as the rows' own; with one ticket
+// looked up whole at a time 131072 tokens took 62 us).  It tells that its rows are there, waits for whoever still
+// has to read the slots that they go to, and writes them.  Eight blocks of 128 threads an SM: 51 us; four of
+// 256: 54.
 __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const Params p) {
     constexpr int kMaxRows = tile_rows(64);
     static_assert(kMaxRows <= kMoveThreads, "a thread a row");
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const
         int pos = 0;
         if (places) pos = a.kv.pos[pos_at(s_src[b][tid])];
         // most of those that this one has to wait for have long read their rows
-        int t = k.w0 + (tid + kMoveThreads / 2) % kMoveThreads * k.step;
+        int64_t t = k.w0 + (int64_t)((tid + kMoveThreads / 2) % kMoveThreads) * k.step;
         while (t < k.w1 && load_acquire(p.flags + t)) t += kMoveThreads * k.step;
         if (tid >= kLast) next_ticket(b == 0 ? 2 : b - 1);
         look_up(b == 2 ? 0 : b + 1);

@@ -548,7 +548,7 @@ up_status up_attend_tree(const void *q, const int32_t *cu_seqlens, const int32_t
  *               or reach past num_flags, sets UP_DEVERR_BAD_CU_BLOCKS.
  *   G           tokens of a flag, positive.
  *   kv_lens_out int32 [num_seqs]: the cached tokens that remain, kv_lens[s] - n_s + kept (kv_lens
- *               itself is allowed).
+ *               itself is allowed; other overlaps with it, cu_seqlens or cu_blocks are refused).
  *   workspace   up_compact_kv_workspace(...) bytes, 256-byte aligned; its contents on entry do
  *               not matter.
  * Pages that hold kept tokens of the n_s, or the slots that they move to, must not be shared between

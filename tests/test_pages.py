@@ -35,7 +35,7 @@ def _copy(L, cache=None, copies=256, n=3):
     return L.up_copy_pages(cache or _cache(), copies, n, None)
 
 
-def _compact(L, cache=None, cu=256, T=10, keep=256, nf=10, cb=None, G=1, out=256, ws=256, wsb=1 << 40):
+def _compact(L, cache=None, cu=512, T=10, keep=256, nf=10, cb=None, G=1, out=1024, ws=256, wsb=1 << 40):
     return L.up_compact_kv(cache or _cache(), cu, T, keep, nf, cb, G, out, ws, wsb, None)
 
 
@@ -70,7 +70,8 @@ def test_cache_refusals(L):  # noqa: F811
     assert _copy(L, n=0) == 0
     for bad in (dict(cu=None), dict(keep=None), dict(out=None), dict(T=-1), dict(T=1 << 31), dict(nf=-1), dict(G=0),
                 dict(G=-5), dict(G=2), dict(cu=258), dict(cb=258), dict(out=258),
-                dict(T=2 ** 31 - 1, cache=_cache(Hk=64))):
+                dict(T=2 ** 31 - 1, cache=_cache(Hk=64)), dict(out=260), dict(out=252), dict(out=520), dict(out=508),
+                dict(out=1028, cb=1024)):
         assert _compact(L, **bad) == 1, bad
     for bad in (dict(ws=None), dict(ws=272), dict(wsb=0)):
         assert _compact(L, **bad) == 3
@@ -469,6 +470,11 @@ def test_compaction_errors(more):
     m = made()
     out = up.compact_kv(m.cache, m.cu, keep[:200])  # flags that end too early
     assert up.get_device_error() in (1, 0x10)
+    # one flag for all of a sequence, however large its blocks; none for the last
+    for G in (100, 300, 2 ** 31 - 1):
+        m = made()
+        out = up.compact_kv(m.cache, m.cu, keep[:2] * 0, cu_blocks=ints([0, 1, 2, 2]), G=G, **most)
+        assert up.get_device_error() == 0x10 and out.tolist() == [200, 40, 64]
     m = made()
     out = up.compact_kv(m.cache, m.cu, keep[:200], **most)
     assert up.get_device_error() == 0x10 and out.tolist() == full[3][:2] + [64]
