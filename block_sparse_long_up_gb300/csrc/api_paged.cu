@@ -310,7 +310,7 @@ up_status up_compact_kv(const up_paged_kv *cache, const int32_t *cu_seqlens, int
         !few_tiles(max_tokens, cache->num_seqs, cache->Hk))
         return UP_ERR_INVALID_ARG;
     if (cache->num_seqs == 0) return UP_OK;
-    if (!cu_seqlens || !kv_lens_out || (max_tokens > 0 && !keep)) return UP_ERR_INVALID_ARG;
+    if (!cu_seqlens || !kv_lens_out || (num_flags > 0 && !keep)) return UP_ERR_INVALID_ARG;
     if (!aligned(cu_seqlens, 4) || !aligned(cu_blocks, 4) || !aligned(kv_lens_out, 4)) return UP_ERR_INVALID_ARG;
     const int64_t n = cache->num_seqs;
     if ((kv_lens_out != cache->kv_lens && overlap(kv_lens_out, n, cache->kv_lens, n)) ||

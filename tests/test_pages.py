@@ -406,6 +406,17 @@ def test_compaction(into, d, Hk, dtype, share, lens, G):
 
 
 @pytest.mark.gpu
+def test_nothing_flagged():
+    m = Made([(0, 50), (0, 0)], 2, 64, 16, "bf16", seed=1)
+    none = torch.zeros(0, dtype=torch.uint8, device="cuda")
+    for most in (None, 0, 1, 50000):
+        for into in (None, m.kv_lens):
+            was = m.kp.clone()
+            assert up.compact_kv(m.cache, m.cu, none, max_tokens=most, kv_lens_out=into).tolist() == [50, 0]
+            assert equal(m.kp, was) and up.get_device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n,first,share", [(40000, 0, 1.0), (40000, 1, 1.0), (40000, 20000, 1.0), (60000, 100, 0.999),
                                            (131072, 0, 0.3)])
 def test_every_tile_waits_for_its_neighbour(n, first, share):
