@@ -57,9 +57,9 @@ constexpr int kAllWarps = kBlocks * kWarps;
 
 __device__ __forceinline__ int cluster_warp() { return blockIdx.x * kWarps + (threadIdx.x >> 5); }
 
-// All threads of the cluster meet; what each wrote before is there for all (read through L2: __ldcg).
+// All threads of the cluster meet; what each wrote before is there for all (released and acquired at
+// the cluster's scope, and read through L2: __ldcg).
 __device__ __forceinline__ void arrive() {
-    __threadfence();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void await_all() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
