@@ -15,7 +15,7 @@
 //
 // Two launches: a plan (one cluster of blocks: the scan of the flags, which lists the kept slots and
 // ranks the tiles' edges) and the move.  131072 tokens of 8 heads of 128 that keep a quarter of their blocks of
-// 64: 62 us in a graph, of it 51 the move of 134 MB each way at 5.3 TB/s together, where a plain copy would
+// 64: 58 us in a graph, of it 47 the move of 134 MB each way at 5.7 TB/s together, where a plain copy would
 // take 40 (latency: a tile's tickets, slots and pages are looked up while the one before it is read, but a block
 // of 16 KB still waits for its loads, its flags and its stores in turn).  Where the sequences have few flagged
 // tokens one launch does both.
@@ -65,7 +65,7 @@ Layout layout_of(int64_t T, int num_seqs, int Hk, int d) {
 
 struct Params {
     KvCompactArgs a;
-    int r_log2, g_log2;  // of R, and of G (-1: G is no power of two)
+    int r_log2, g_log2, p_log2;  // of R, G and the page size (-1: no power of two)
     Head *head;
     Moved *seqs;
     int32_t *list;   // the kept tokens' numbers among their sequence's flagged ones
@@ -75,7 +75,7 @@ struct Params {
 };
 
 // where the edges of sequence s begin: every sequence before it may have a partial one
-__device__ __forceinline__ int64_t edges_of(const Params &p, int s) { return p.a.cu_seqlens[s] / p.R + (int64_t)s; }
+__device__ __forceinline__ int64_t edges_of(const Params &p, int s) { return (p.a.cu_seqlens[s] >> p.r_log2) + (int64_t)s; }
 
 // The slot before sequence s's flagged tokens, where its flags begin, and whether they can be.
 struct Region {
@@ -316,10 +316,10 @@ __device__ Ticket describe(const Params &p, int number, int all, int *list_at, i
     // The tiles that read what this one is about to write over: those of the kept tokens in slots
     // [r0, r0 + rows), by the ranks at the edges around them.
     const int64_t e = edges_of(p, lo);
-    const int len = a.cu_seqlens[lo + 1] - a.cu_seqlens[lo], next = (k.r0 + k.rows - 1) / p.R + 1;
-    const int ea = __ldg(p.edges + e + k.r0 / p.R) - q.at;
-    const int eb = next < (len + p.R - 1) / p.R ? __ldg(p.edges + e + next) - q.at : q.kept;
-    const int t0 = max(ea - q.stay, 0) / p.R, t1 = min((max(eb - q.stay, 0) + p.R - 1) / p.R, i);
+    const int len = a.cu_seqlens[lo + 1] - a.cu_seqlens[lo], next = ((k.r0 + k.rows - 1) >> p.r_log2) + 1;
+    const int ea = __ldg(p.edges + e + (k.r0 >> p.r_log2)) - q.at;
+    const int eb = next < (len + p.R - 1) >> p.r_log2 ? __ldg(p.edges + e + next) - q.at : q.kept;
+    const int t0 = max(ea - q.stay, 0) >> p.r_log2, t1 = min((max(eb - q.stay, 0) + p.R - 1) >> p.r_log2, i);
     k.w0 = q.ticket0 + t0 * per + group;
     k.w1 = q.ticket0 + t1 * per + group;
     k.step = per;
@@ -331,17 +331,17 @@ __device__ Ticket describe(const Params &p, int number, int all, int *list_at, i
 // A block reads a tile's rows into registers, and while they come one warp describes the ticket after
 // next and all look up the next one's rows (each a chain of loads as long as the rows' own; with one ticket
 // looked up whole at a time 131072 tokens took 62 us).  It tells that its rows are there, waits for whoever still
-// has to read the slots that they go to, and writes them.  Eight blocks of 128 threads an SM: 51 us; four of
-// 256: 54.
+// has to read the slots that they go to, and writes them.  (Eight blocks of 128 threads an SM took 51 us where
+// four of 256 took 54, before the addresses were cut down: 47.)
+template <int D>
 __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const Params p) {
-    constexpr int kMaxRows = tile_rows(64);
-    static_assert(kMaxRows <= kMoveThreads, "a thread a row");
-    __shared__ int64_t s_src[3][kMaxRows], s_dst[3][kMaxRows];
+    constexpr int kMaxRows = tile_rows(D), kRowPieces = D / 8;  // of 16 bytes
+    static_assert(kMaxRows <= kMoveThreads && kMoveThreads % kRowPieces == 0, "a thread a row, whole rows at a time");
+    __shared__ int64_t s_src[3][kMaxRows], s_dst[3][kMaxRows];  // bytes behind the head's first row
     __shared__ Ticket s_ticket[3];
     __shared__ int s_list[3], s_seq[3], s_stop;
     const KvCompactArgs &a = p.a;
-    const int tid = threadIdx.x, Hk = a.kv.Hk, ps = a.kv.page_size, d2 = a.kv.d * 2;
-    const int shift = a.kv.d == 64 ? 3 : a.kv.d == 128 ? 4 : 5;  // 16-byte pieces of a row, log2
+    const int tid = threadIdx.x, Hk = a.kv.Hk, ps = a.kv.page_size;
     pdl_wait();
     const int all = p.head->tickets;
     if (all == 0) return;
@@ -364,9 +364,13 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const
         if (s_ticket[slot].number >= 0 && tid < s_ticket[slot].rows) {
             const int base = s_ticket[slot].base;
             const int src = base + __ldg(p.list + s_list[slot] + tid), dst = base + s_ticket[slot].r0 + tid;
-            const int from = page_of(a.kv, s_seq[slot], src), to = page_of(a.kv, s_seq[slot], dst);
-            s_src[slot][tid] = from < 0 || to < 0 ? -1 : (int64_t)from * Hk * ps + src % ps;
-            s_dst[slot][tid] = (int64_t)to * Hk * ps + dst % ps;
+            const int32_t *table = a.kv.block_table + (int64_t)s_seq[slot] * a.kv.max_pages;
+            const int i = p.p_log2 >= 0 ? src >> p.p_log2 : src / ps, j = p.p_log2 >= 0 ? dst >> p.p_log2 : dst / ps;
+            const int from = table[i], to = table[j];
+            const bool ok = from >= 0 && from < a.kv.num_pages && to >= 0 && to < a.kv.num_pages;
+            if (!ok) atomicOr(a.kv.err, kErrPage);
+            s_src[slot][tid] = ok ? ((int64_t)from * Hk * ps + src - i * ps) * (2 * D) : -1;
+            s_dst[slot][tid] = ((int64_t)to * Hk * ps + dst - j * ps) * (2 * D);
         }
     };
     if (tid >= kLast) {
@@ -383,25 +387,40 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const
     for (int b = 0;; b = b == 2 ? 0 : b + 1) {
         const Ticket k = s_ticket[b];
         if (k.number < 0) return;
-        const int pieces = k.rows << shift;  // of a chain
-        uint4 v[kInFlight];
-        // piece x of the tile: its row, and where its chain's row 0 of page 0 lies
-        auto row_of = [&](int x) { return (k.chains == 1 ? x : x % pieces) >> shift; };
-        auto base_of = [&](int x) {
-            const int c = k.chains == 1 ? k.chain : k.chain + x / pieces;
-            return static_cast<char *>(c & 1 ? a.kv.v : a.kv.k) + (int64_t)(c >> 1) * ps * d2 + (x & ((1 << shift) - 1)) * 16;
+        // The tile's pieces, kMoveThreads at a time: of one chain's rows, where each thread keeps its place in a
+        // row (addresses worked out from x alone took half of the block's time), or of several chains'.
+        const int per = k.rows * kRowPieces;  // pieces of a chain
+        const int col = tid % kRowPieces * 16, row0 = tid / kRowPieces;
+        auto head_of = [&](int c) {
+            return static_cast<char *>(c & 1 ? a.kv.v : a.kv.k) + (int64_t)(c >> 1) * ps * (2 * D) + col;
         };
-#pragma unroll
-        for (int j = 0; j < kInFlight; ++j) {
-            const int x = tid + j * kMoveThreads;
-            v[j] = make_uint4(0, 0, 0, 0);
-            if (x < pieces * k.chains) {
-                const int64_t src = s_src[b][row_of(x)];
-                if (src >= 0) v[j] = *reinterpret_cast<const uint4 *>(base_of(x) + src * d2);
+        char *const head = head_of(k.chain);
+        auto at = [&](int i, const int64_t *rows, char *&p16) {
+            int r = row0 + i * (kMoveThreads / kRowPieces);
+            char *h = head;
+            if (k.chains > 1) {
+                const int x = tid + i * kMoveThreads, c = x / per;
+                if (c >= k.chains) return false;
+                r -= c * k.rows;
+                h = head_of(k.chain + c);
+            } else if (r >= k.rows) {
+                return false;
             }
+            p16 = h + rows[r];
+            return s_src[b][r] >= 0;
+        };
+        uint4 v[kInFlight];
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) {
+            char *src;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (at(i, s_src[b], src)) v[i] = *reinterpret_cast<const uint4 *>(src);
         }
         // the first chains' ticket moves the positions too: row (page * Hk) * ps + slot, less the heads
-        auto pos_at = [&](int64_t row) { return row / ((int64_t)Hk * ps) * ps + row % ((int64_t)Hk * ps); };
+        auto pos_at = [&](int64_t bytes) {
+            const int64_t row = bytes / (2 * D);
+            return row / ((int64_t)Hk * ps) * ps + row % ((int64_t)Hk * ps);
+        };
         const bool places = k.places && tid < k.rows && s_src[b][tid] >= 0;
         int pos = 0;
         if (places) pos = a.kv.pos[pos_at(s_src[b][tid])];
@@ -436,10 +455,9 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const
             }
         }
 #pragma unroll
-        for (int j = 0; j < kInFlight; ++j) {
-            const int x = tid + j * kMoveThreads;
-            if (x < pieces * k.chains && s_src[b][row_of(x)] >= 0)
-                *reinterpret_cast<uint4 *>(base_of(x) + s_dst[b][row_of(x)] * d2) = v[j];
+        for (int i = 0; i < kInFlight; ++i) {
+            char *dst;
+            if (at(i, s_dst[b], dst)) *reinterpret_cast<uint4 *>(dst) = v[i];
         }
         if (places) a.kv.pos[pos_at(s_dst[b][tid])] = pos;
         // (of the three slots the next pass writes the one that no thread reads any more)
@@ -451,8 +469,8 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const
 // Block (j, s): the keys and values of head j of sequence s, in one launch.  It scans the sequence's flags
 // kRun at a time and moves what they keep itself, a tile of rows read into registers before it is
 // written; so nothing waits for another block.  In a graph, 8 heads of 128: 64 sequences of 64 tokens
-// 6-9 us (by tickets 22-23), 256 of 64 14-21 (23-50), one of 256 4-10 (17); but 16384 tokens 142-519 (23-46)
-// where all are one sequence's, and 4096 38-122 (20-24).  Which it is the host does not know: up to 1024
+// 6-9 us (by tickets 16-17), 256 of 64 14-21 (18-28), one of 256 4-9 (14-16); but 16384 tokens 142-519 (20-39)
+// where all are one sequence's, and 4096 37-122 (16-21).  Which it is the host does not know: up to 1024
 // tokens times the root of the number of sequences.
 constexpr int kFewThreads = 256, kRun = kFewThreads;  // a thread a flag
 bool few_tokens(int64_t T, int64_t num_seqs) { return T * T <= num_seqs << 20; }
@@ -554,6 +572,8 @@ cudaError_t launch_kv_compact(const KvCompactArgs &a, int num_sms, cudaStream_t 
     while (1 << p.r_log2 < p.R) ++p.r_log2;
     while (p.g_log2 < 30 && 1 << p.g_log2 < a.G) ++p.g_log2;
     if (1 << p.g_log2 != a.G) p.g_log2 = -1;
+    while (p.p_log2 < 30 && 1 << p.p_log2 < a.kv.page_size) ++p.p_log2;
+    if (1 << p.p_log2 != a.kv.page_size) p.p_log2 = -1;
     const Layout L = layout_of(a.T, a.kv.num_seqs, a.kv.Hk, a.kv.d);
     char *ws = static_cast<char *>(a.workspace);
     p.head = reinterpret_cast<Head *>(ws + L.head);
@@ -570,7 +590,8 @@ cudaError_t launch_kv_compact(const KvCompactArgs &a, int num_sms, cudaStream_t 
     if (e != cudaSuccess) return e;
     const int64_t most = ((int64_t)a.T / p.R + a.kv.num_seqs) * 2 * a.kv.Hk;
     const int64_t grid = most < (int64_t)num_sms * kMovePerSm ? most : (int64_t)num_sms * kMovePerSm;
-    return launch_pdl(kv_move_kernel, dim3((unsigned)grid), dim3(kMoveThreads), 0, st, p);
+    auto move = a.kv.d == 64 ? kv_move_kernel<64> : a.kv.d == 128 ? kv_move_kernel<128> : kv_move_kernel<256>;
+    return launch_pdl(move, dim3((unsigned)grid), dim3(kMoveThreads), 0, st, p);
 }
 
 }  // namespace up
