@@ -229,7 +229,7 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
         e = launch_pdl(attend_kernel<kFp16, D, true, kGaps>, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmem, st, qm,
                        km, vm, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attend_join_kernel<kFp16, D>, dim3((unsigned)p.grid * kJoinPerSm), dim3(kJoinThreads), 0, st, p);
+    return launch_pdl(attend_join_kernel<kFp16, D, kRanges>, dim3((unsigned)p.grid * kJoinPerSm), dim3(kJoinThreads), 0, st, p);
 }
 
 }  // namespace

@@ -230,7 +230,7 @@ cudaError_t launch_type(const AttendArgs &a, int num_sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmem, st, qm, km, vm, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attend_join_kernel<kFp16, D>, dim3((unsigned)p.grid * kJoinPerSm), dim3(kJoinThreads), 0, st, p);
+    return launch_pdl(attend_join_kernel<kFp16, D, kMask>, dim3((unsigned)p.grid * kJoinPerSm), dim3(kJoinThreads), 0, st, p);
 }
 
 template <Mask kMask>

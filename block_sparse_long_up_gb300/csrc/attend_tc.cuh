@@ -1426,12 +1426,88 @@ __device__ __forceinline__ void join_piece(const Params &p, const Plan &pl, cons
     __syncthreads();
 }
 
+// The same for 32 rows and 32 columns of a unit in many parts: a warp takes every eighth part, and the eight
+// warps' sums are added in their order.  (8 drafted tokens over 128K, 76 parts a unit: with 8/2 heads of 64 33 us a
+// call, 44 with one part after another; with 16/2 of 256 64 and 71.  19 parts a unit, 32/8 heads of 128: 95 and 98.)
+template <bool kFp16, int D>
+__device__ __forceinline__ void join_many(const Params &p, const Plan &pl, const Shares &sh, int c0, int rows0, int col0) {
+    using C = Cfg<D>;
+    constexpr int kWarps = kJoinThreads / 32;
+    __shared__ float s_m[kWarps][32], s_l[kWarps][32];
+    __shared__ __align__(16) float s_o[kWarps][32][36];  // rows 144 bytes apart: 4 banks on
+    const AttendArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Cut cut = p.cuts[c0];
+    const Unit u = p.units[cut.unit];
+    const int j = cut.j;
+    // row r of the unit: its token and output row, or -1
+    auto out_row = [&](int r) {
+        const int e = r / kRows, rr = r % kRows, tl = rr / a.g, tok = e * p.tpt + tl;
+        return tl < p.tpt && tok < u.ntok ? (u.tok0 + tok) * a.Hq + j * a.g + rr - tl * a.g : -1;
+    };
+    const int r = rows0 + lane;
+    const bool valid = out_row(r) >= 0;
+    if (!__any_sync(0xffffffffu, valid)) return;  // all warps do
+    const int64_t ub = (int64_t)j * pl.W + u.prefix, ue = ub + width_of(u);
+    const int n = share_of(sh, ue - 1) - c0 + 1;
+    const int slot0 = 2 * c0 + (share_begin(sh, c0) < ub);
+    auto part = [&](int i) { return p.parts + (int64_t)(i == 0 ? slot0 : 2 * (c0 + i)) * C::kUnitRows * (D + 4); };
+    float M = -INFINITY, L = 0.f;
+    if (valid)
+        for (int i = warp; i < n; i += kWarps) M = fmaxf(M, part(i)[r]);
+    s_m[warp][lane] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][lane]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float4 O[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) O[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (valid) {
+        for (int i = warp; i < n; i += kWarps) {
+            const float *src = part(i);
+            const float4 *o = reinterpret_cast<const float4 *>(src + 4 * C::kUnitRows) + r + col0 / 4 * C::kUnitRows;
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = o[k * C::kUnitRows];
+            const float w = exp2f(src[r] - ref);
+            L = fmaf(w, src[C::kUnitRows + r], L);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                O[k].x = fmaf(w, v[k].x, O[k].x); O[k].y = fmaf(w, v[k].y, O[k].y);
+                O[k].z = fmaf(w, v[k].z, O[k].z); O[k].w = fmaf(w, v[k].w, O[k].w);
+            }
+        }
+    }
+    s_l[warp][lane] = L;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) *reinterpret_cast<float4 *>(&s_o[warp][lane][4 * k]) = O[k];
+    __syncthreads();
+    // a thread adds four columns of one row
+    const int row = tid / 8, c = tid % 8 * 4, at = out_row(rows0 + row);
+    if (at >= 0) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f, most = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4 *>(&s_o[w][row][c]);
+            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+            sum += s_l[w][row];
+            most = fmaxf(most, s_m[w][row]);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        store_row4<kFp16>(a.out, (int64_t)at * D + col0 + c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        if (a.lse && col0 == 0 && c == 0) a.lse[at] = ((most == -INFINITY ? 0.f : most) + log2f(sum)) * kLn2;
+    }
+    __syncthreads();
+}
+
 // Joins the units that a share's end cuts, named by the first share that does, 32 rows at a time, and where
 // there are blocks enough 32 of their columns at a time too.  (A block for each 32 rows of each
 // share, most of them without any, took 8.8 us of a call of 128 tokens over 1K and 19 of 64 drafted ones
 // over 128K, whose 8 units are in 19 parts each; 7 and 13 so.)  All blocks together also write the rows of the
 // units without a visible slot, or of all tokens when the batch is malformed.
-template <bool kFp16, int D>
+template <bool kFp16, int D, Mask kMask>
 __global__ void __launch_bounds__(kJoinThreads, 3) attend_join_kernel(const Params p) {
     using C = Cfg<D>;
     constexpr int kRowGroups = C::kUnitRows / kJoinRows;
@@ -1474,7 +1550,8 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attend_join_kernel(const Para
     const int pieces = kRowGroups * (split ? D / 32 : D / 32 / kWide);
     for (int x = blockIdx.x; x < cuts * pieces; x += gridDim.x) {
         const int c0 = s_cut[x / pieces], y = x % pieces, rows0 = y % kRowGroups * kJoinRows;
-        if (split) join_piece<kFp16, D, 1>(p, pl, sh, c0, rows0, y / kRowGroups * 32);
+        if (of_sets(kMask) && split) join_many<kFp16, D>(p, pl, sh, c0, rows0, y / kRowGroups * 32);
+        else if (split) join_piece<kFp16, D, 1>(p, pl, sh, c0, rows0, y / kRowGroups * 32);
         else join_piece<kFp16, D, kWide>(p, pl, sh, c0, rows0, y / kRowGroups * 32 * kWide);
     }
 }
