@@ -16,9 +16,9 @@
 // Two launches: a plan (one cluster of blocks: the scan of the flags, which lists the kept slots and
 // ranks the tiles' edges) and the move.  131072 tokens of 8 heads of 128 that keep a quarter of their blocks of
 // 64: 58 us in a graph, of it 47 the move of 134 MB each way at 5.7 TB/s together, where a plain copy would
-// take 40 (latency: a tile's tickets, slots and pages are looked up while the one before it is read, but a block
-// of 16 KB still waits for its loads, its flags and its stores in turn).  Where the sequences have few flagged
-// tokens one launch does both.
+// take 40 (what is left is the beginning -- a ticket, its description, its rows' pages, one after another -- and the
+// last tickets' end: with a ring of three tiles in shared memory, loaded two ahead, it took 50).  Where the
+// sequences have few flagged tokens one launch does both.
 #include "pages.cuh"
 
 namespace up {
