@@ -295,7 +295,7 @@ def attend_paged(q, cu_seqlens, cache, scale=None, softcap=0.0, slopes=None, q_p
         _given(out, lse, workspace, cache, q.shape)
     with _on(stream):
         if out is None:
-            out = torch.empty((T, Hq, d), dtype=cache.dtype, device=dev)
+            out = torch.empty_like(q)  # (contiguous; quicker than naming its shape, type and device)
         if lse is None:
             lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
         if workspace is None:
@@ -342,7 +342,7 @@ def attend_tree(q, cu_seqlens, parents, cache, scale=None, softcap=0.0, slopes=N
         _given(out, lse, workspace, cache, q.shape)
     with _on(stream):
         if out is None:
-            out = torch.empty((T, Hq, d), dtype=cache.dtype, device=dev)
+            out = torch.empty_like(q)
         if lse is None:
             lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
         if workspace is None:
@@ -379,7 +379,7 @@ def decode_attend(q, cache, scale=None, softcap=0.0, slopes=None, q_pos=None, kv
         _given(out, lse, workspace, cache, q.shape)
     with _on(stream):
         if out is None:
-            out = torch.empty((B, Hq, d), dtype=cache.dtype, device=dev)
+            out = torch.empty_like(q)
         if lse is None:
             lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
         if workspace is None:
