@@ -300,6 +300,36 @@ def test_pool_errors():
 
 
 @pytest.mark.gpu
+def test_pool_calls_on_a_side_stream():
+    """All calls with stream=, ordered by it alone, and buffers that the caller brings."""
+    m = Made([(0, 70), (0, 48)], 2, 64, 16, "bf16", seed=3, extra=20)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    held = int((m.table >= 0).sum())
+    refs = torch.zeros(m.kp.shape[0], dtype=torch.int32, device="cuda")
+    refs[m.table[m.table >= 0].long()] = 1
+    order = torch.argsort(refs, stable=True).to(torch.int32)  # free pages first
+    pool = up.PagePool(refs, order, ints([refs.numel() - held]))
+    table, lens, copies = (ints([[-7] * m.table.shape[1]] * 3), ints([0] * 3), ints([[0] * 3] * 3))
+    par, more = ints([1, 0, 0]), ints([60, 80, 80])
+    torch.cuda.synchronize()
+    out = up.fork_pages(pool, m.table, m.kv_lens, 16, par, table_out=table, lens_out=lens, copies=copies, stream=side)
+    assert all(x is y for x, y in zip(out, (table, lens, copies)))
+    up.copy_pages(m.cache, copies, stream=side)
+    up.reserve_pages(pool, table, 16, lens, more, stream=side)
+    side.synchronize()
+    assert lens.tolist() == [48, 70, 70] and copies[2].tolist() == [0, 6, 6]
+    assert [(row >= 0).sum().item() for row in table] == [4, 5, 5]
+    for s, parent in enumerate(par.tolist()):
+        i = torch.arange(int(lens[s]), device="cuda")
+        for x in (m.kp, m.vp):
+            assert equal(x[table[s].long()[i // 16], :, i % 16], x[m.table[parent].long()[i // 16], :, i % 16])
+    up.release_pages(pool, table, 16, None, more, stream=side)
+    side.synchronize()
+    assert int(pool.num_free) == refs.numel() - held and int(refs.sum()) == held and up.get_device_error() == 0
+
+
+@pytest.mark.gpu
 def test_a_reserve_of_what_is_there_takes_nothing():
     """A decode step's reserve, captured once: a page only where a token begins one."""
     pool, table, lens = up.PagePool.full(64), ints([[-1] * 9] * 4), ints([1, 15, 16, 30])
