@@ -15,7 +15,7 @@
 //
 // Two launches: a plan (one cluster of blocks: the scan of the flags, which lists the kept slots and
 // ranks the tiles' edges) and the move.  131072 tokens of 8 heads of 128 that keep a quarter of their blocks of
-// 64: 58 us in a graph, of it 47 the move of 134 MB each way at 5.7 TB/s together, where a plain copy would
+// 64: 57 us in a graph, of it 46 the move of 134 MB each way at 5.8 TB/s together, where a plain copy would
 // take 40 (what is left is the beginning -- a ticket, its description, its rows' pages, one after another -- and the
 // last tickets' end: with a ring of three tiles in shared memory, loaded two ahead, it took 50).  Where the
 // sequences have few flagged tokens one launch does both.
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const
     static_assert(kMaxRows <= kMoveThreads && kMoveThreads % kRowPieces == 0, "a thread a row, whole rows at a time");
     __shared__ int64_t s_src[3][kMaxRows], s_dst[3][kMaxRows];  // bytes behind the head's first row
     __shared__ Ticket s_ticket[3];
-    __shared__ int s_list[3], s_seq[3], s_stop;
+    __shared__ int s_list[3], s_seq[3], s_stop, s_first, s_both;
     const KvCompactArgs &a = p.a;
     const int tid = threadIdx.x, Hk = a.kv.Hk, ps = a.kv.page_size;
     pdl_wait();
@@ -373,13 +373,26 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const
             s_dst[slot][tid] = ((int64_t)to * Hk * ps + dst - j * ps) * (2 * D);
         }
     };
+    if (tid == kLast) {
+        // two at once where there are enough for all, a describing warp each (1 us of a long move's beginning)
+        const int both = all >= 2 * (int)gridDim.x;
+        number = atomicAdd(&p.head->ticket, 1 + both);
+        s_first = number;
+        s_both = both;
+        s_stop = 0;
+    }
+    __syncthreads();
     if (tid >= kLast) {
-        if (tid == kLast) {
-            number = atomicAdd(&p.head->ticket, 1);
-            s_stop = 0;
-        }
         next_ticket(0);
-        next_ticket(1);
+        if (!s_both) next_ticket(1);
+    } else if (s_both && tid >= kLast - 32) {
+        int at = 0, seq = 0;
+        const Ticket k = describe(p, s_first + 1, all, &at, &seq);
+        if (tid == kLast - 32) {
+            s_ticket[1] = k;
+            s_list[1] = at;
+            s_seq[1] = seq;
+        }
     }
     __syncthreads();
     look_up(0);
