@@ -386,11 +386,13 @@ up_status up_fork_pages(const up_page_pool *pool, const int32_t *block_table,
     if (!aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(parents, 4) || !aligned(table_out, 4) ||
         !aligned(lens_out, 4) || !aligned(copies, 4))
         return UP_ERR_INVALID_ARG;
-    // a child's row must not be written over a parent's, nor its length over a parent's or another's parent
-    const int64_t row = (int64_t)max_pages;
-    if (overlap(table_out, num_children * row, block_table, num_seqs * row) ||
-        overlap(lens_out, num_children, kv_lens, num_seqs) || overlap(lens_out, num_children, parents, num_children))
-        return UP_ERR_INVALID_ARG;
+    // nothing is written over what other children, or other blocks, still read
+    const struct { const int32_t *at; int64_t n; } all[6] = {
+        {table_out, (int64_t)num_children * max_pages}, {lens_out, num_children}, {copies, (int64_t)num_children * 3},
+        {block_table, (int64_t)num_seqs * max_pages},   {kv_lens, num_seqs},      {parents, num_children}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 6; ++j)
+            if (overlap(all[i].at, all[i].n, all[j].at, all[j].n)) return UP_ERR_INVALID_ARG;
     up::DeviceInfo di{};
     if ((st = up::device_info(&di)) != UP_OK) return st;
     up::ForkArgs a{};

@@ -538,7 +538,7 @@ up_status up_attend_tree(const void *q, const int32_t *cu_seqlens, const int32_t
  * cached tokens of every sequence those that are kept move together, in order, right behind
  * the tokens before them -- the accepted path of a drafted tree, or the blocks of a
  * prompt that up_select_blocks kept.  Keys, values and positions move; the slots behind the
- * kept tokens hold what they held or copies.
+ * kept tokens hold what they held.
  *
  *   max_tokens  what cu_seqlens[num_seqs] is at most (above: UP_DEVERR_BAD_CU_SEQLENS); it sizes
  *               the workspace.
@@ -619,10 +619,11 @@ up_status up_release_pages(const up_page_pool *pool, int32_t *block_table, int n
  * page gets a free page of its own, whose rows up_copy_pages then copies in every layer's
  * cache.  Entries of the parent that are negative (released ones behind a window) stay -1, as
  * do those behind its kv_lens.
- *   table_out  int32 [num_children, max_pages], not overlapping block_table.
+ *   table_out  int32 [num_children, max_pages].
  *   lens_out   int32 [num_children]: the parent's length.
  *   copies     int32 [3, num_children]: source page, new page, rows (-1, -1 where there is nothing
  *              to copy).
+ * The three overlap neither one another nor block_table, kv_lens and parents (UP_ERR_INVALID_ARG).
  * A child whose parent is not in [0, num_seqs) (UP_DEVERR_BAD_TREE), has a length that cannot be
  * (UP_DEVERR_BAD_KV_LENS), or for which no free page is left (UP_DEVERR_NO_PAGES; earlier
  * children come first) is empty: length 0, no page.

@@ -52,7 +52,9 @@ def test_pool_refusals(L):  # noqa: F811
         assert _release(L, **bad) == 1
     for bad in (dict(lens=None), dict(parents=None), dict(out=None), dict(lout=None), dict(copies=None), dict(n=-1),
                 dict(B=0), dict(n=1 << 28), dict(out=(1 << 20) + 4), dict(out=(1 << 20) - 4), dict(lout=(1 << 21) + 4),
-                dict(lout=(1 << 22) + 8), dict(copies=258), dict(parents=258)):
+                dict(lout=(1 << 22) + 8), dict(copies=258), dict(parents=258), dict(copies=1 << 20), dict(copies=1 << 21),
+                dict(copies=(1 << 22) - 32), dict(copies=(1 << 23) + 4), dict(copies=(1 << 24) - 8), dict(out=1 << 21),
+                dict(out=(1 << 22) - 4), dict(lout=(1 << 23) + 92), dict(lout=(1 << 20) + 60)):
         assert _fork(L, **bad) == 1, bad
     assert _reserve(L, B=0) == 0 and _release(L, B=0) == 0 and _fork(L, n=0) == 0
     assert L.up_reserve_pages(None, 256, 2, 8, 16, 256, 256, None) == 1
