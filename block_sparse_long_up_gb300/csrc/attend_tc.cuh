@@ -60,9 +60,10 @@ enum Mask { kRanges, kGaps, kSinks, kTree };
 // the last two: the kernels of sets
 constexpr bool of_sets(Mask m) { return m == kSinks || m == kTree; }
 
-constexpr int kMinTiles = 4;      // shares are not cut finer than this: more parts cost
-                                  // more to join than a step (128 tokens over 4K: 29.8,
-                                  // 23.6, 22.4 and 26.5 us with 1, 2, 4 and 8)
+// Shares are not cut finer than this: more parts cost more to join than a step (128 tokens over 4K: 29.8,
+// 23.6, 22.4 and 26.5 us with 1, 2, 4 and 8).  The calls of sets join many parts in less time (128 tokens with a
+// window of 1K: 16.4, 17.7, 19.3 and 20.5 us with 1 to 4; 8 drafted over 16K of 2 heads 22.5, 21.6, 20.4 and 19.4).
+constexpr int min_tiles(Mask m) { return of_sets(m) ? 2 : 4; }
 constexpr int kPanel = 128 * 128; // 128 rows x 64 elements
 // Tiles' worth of time that a unit costs beside its tiles: without it a share of short
 // units takes far longer than one of long ones (three ragged sequences, 16/2 heads of
@@ -319,7 +320,7 @@ struct Pieces {
         n = pl.units;
         at = end = 0;
         if (W1 == 0) return;
-        sh = shares_of(W1 * pp.a.kv.Hk, pp.grid, kMinTiles);
+        sh = shares_of(W1 * pp.a.kv.Hk, pp.grid, min_tiles(kMask));
         if ((int)blockIdx.x >= sh.n) return;
         at = share_begin(sh, blockIdx.x);
         end = share_begin(sh, blockIdx.x + 1);
@@ -1529,7 +1530,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attend_join_kernel(const Para
             for (int64_t k = tid; k < nr; k += kJoinThreads) a.lse[r0 + k] = -INFINITY;
     }
     if (pl.W == 0) return;
-    const Shares sh = shares_of(pl.W * a.kv.Hk, p.grid, kMinTiles);
+    const Shares sh = shares_of(pl.W * a.kv.Hk, p.grid, min_tiles(kMask));
     // the shares whose ends are the first to cut a unit
     uint32_t m = 0;
     if (tid < kMaxSms) {
