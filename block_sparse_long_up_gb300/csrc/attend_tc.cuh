@@ -217,7 +217,7 @@ struct Row {
     }
     __device__ __forceinline__ void set_range(int2 v, int kv, int first) {
         lo = max(v.x, 0);
-        hi = min(v.y, kv);
+        hi = max(min(v.y, kv), 0);  // (a far negative end less a slot's number would pass 32 bits in word())
         sinks = min(first, hi);
     }
     // the row of the token tl tokens behind the unit's first one

@@ -190,6 +190,31 @@ def test_chunks_with_sinks(logits, kind, sinks, Hq, Hk, d, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk,d,dtype", [(8, 2, 64, "bf16"), (32, 8, 128, "fp16"), (16, 1, 256, "bf16")])
+@pytest.mark.parametrize("sinks", [1, 40, 300])
+@pytest.mark.parametrize("logits", ["plain", "both"])
+def test_windows_that_end_before_the_cache(logits, sinks, Hq, Hk, d, dtype):
+    """Entries whose end is any negative number leave a row empty, first tokens included, beside rows of the
+    same tile that see several key tiles."""
+    lens = [(60, 900), (7, 300)]
+    m = Made(lens, Hk, d, 64, dtype, seed=sinks)
+    q = m.normal(m.T, Hq, d) * 3
+    vis = masks("window", lens, 5)
+    low = -2 ** 31
+    for t, (lo, hi) in enumerate([(0, low), (5, low), (2 ** 31 - 1, low), (low, low), (0, -1), (3, low + 100), (700, low + 600)]):
+        vis[2 + 3 * t] = torch.tensor([lo, hi], dtype=torch.int32)
+    vis[62] = torch.tensor([0, low], dtype=torch.int32)
+    kw = logits_of(logits, m, Hq)
+    seen = sink_sets(lens, vis[:, 0], vis[:, 1], sinks)
+    was = held(m)
+    poison(m, seen)
+    out, lse = up.attend_paged(q, m.cu, m.cache, visible=vis, sinks=sinks, **kw)
+    assert up.get_device_error() == 0
+    # (far keys are biased by hundreds, see test_tokens_with_sinks)
+    (check if logits == "plain" else check_at)(m, out, lse, oracle(was, q, seen, d ** -0.5, **kw))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("sinks", [1, 5, 16, 64, 65, 200])
 @pytest.mark.parametrize("Hq,Hk,d,dtype,page", [(8, 2, 64, "bf16", 16), (32, 8, 128, "fp16", 48), (16, 1, 256, "bf16", 128),
                                                 (12, 4, 64, "fp16", 64), (5, 1, 128, "bf16", 384), (3, 3, 256, "fp16", 32)])
