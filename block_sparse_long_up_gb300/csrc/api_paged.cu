@@ -413,7 +413,8 @@ up_status up_copy_pages(const up_paged_kv *cache, const int32_t *copies, int num
     const up::CallRange range("up_copy_pages");
     up_status st = check_cache(cache, -1);
     if (st != UP_OK) return st;
-    if (num_copies < 0) return UP_ERR_INVALID_ARG;
+    // (the kernel's indexes into copies are 32-bit)
+    if (num_copies < 0 || (int64_t)num_copies * 3 > INT32_MAX) return UP_ERR_INVALID_ARG;
     if (num_copies == 0) return UP_OK;
     if (!copies || !aligned(copies, 4) || !cache->k_pages || !cache->v_pages || cache->num_pages < 1)
         return UP_ERR_INVALID_ARG;

@@ -640,7 +640,8 @@ up_status up_fork_pages(const up_page_pool *pool, const int32_t *block_table,
  * destination.  A page outside the pool, or rows outside [0, page_size], set
  * UP_DEVERR_BAD_PAGE and copy nothing.  Of the cache the table and the lengths are not used.
  * Errors: UP_ERR_INVALID_ARG for a cache that the calls above do not take, or for more copies
- * than one launch has blocks (2 * Hk * ceil(page_size * d / 8192) * n below 2^31).
+ * than one launch has blocks (2 * Hk * ceil(page_size * d / 8192) * n below 2^31) or 32-bit
+ * indexes reach (3 * n below 2^31).
  */
 up_status up_copy_pages(const up_paged_kv *cache, const int32_t *copies, int num_copies,
                         up_stream_t stream);

@@ -83,6 +83,12 @@ def test_cache_refusals(L):  # noqa: F811
         assert up.compact_kv_workspace(*bad) == 0
 
 
+@pytest.mark.parametrize("n", [715827883, 1 << 30, (1 << 30) - 1])
+def test_more_copies_than_indexes_reach_are_refused(L, n):  # noqa: F811
+    """(One head of small pages: one launch would have the blocks.)"""
+    assert _copy(L, cache=_cache(Hk=1, page=16), n=n) == 1
+
+
 def test_python_refuses_host_tensors():
     z = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError):
