@@ -41,12 +41,13 @@ __device__ __forceinline__ int2 pages_in(const PageTable &t, int first, int end,
     return make_int2(x, max(x, y));
 }
 
-// Free pages of the pool; none where their number cannot be (UP_DEVERR_BAD_REFS).
+// Free pages of the pool; -1 (UP_DEVERR_BAD_REFS set) where their number cannot be: the call then
+// takes and gives back none, since nothing tells which entries of the stack are free pages.
 __device__ __forceinline__ int free_of(const PagePool &p) {
     const int n = *p.num_free;
     if (n >= 0 && n <= p.num_pages) return n;
     atomicOr(p.err, kErrRefs);
-    return 0;
+    return -1;
 }
 // The page `rank` places below the stack's top (0 <= rank < top), held by its taker from now on; -1
 // when the stack holds no page there.
@@ -67,6 +68,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
     pdl_wait();
     const int top = free_of(pool);
+    if (top < 0) return;  // all blocks do
     const Runs runs(t.num_seqs, t.max_pages);
     // does entry i of row s want a page?
     auto wants = [&](int s, int i, int2 r) {
@@ -106,6 +108,8 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
     release_kernel(const PagePool pool, const PageTable t, const int32_t *first, const int32_t *end) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
+    const int top = free_of(pool);
+    if (top < 0) return;  // all blocks do
     const Runs runs(t.num_seqs, t.max_pages);
     const int num = t.num_seqs * t.max_pages;
     auto each = [&](auto &&f) {
@@ -141,7 +145,6 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
     meet();
     int mine = 0;
     each([&](int at, int pg) { mine += __popc(__ballot_sync(0xffffffffu, pg >= 0 && __ldcg(pool.refs + pg) == at - num)); });
-    const int top = free_of(pool);
     int total, rank = before_warp(mine, &total);
     arrive();
     // the first entry's page on top: reserving the same entries again gives the same pages
@@ -163,12 +166,14 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- fork
 
-// What child i takes over from its parent: full pages shared, and the rows of a last one that is copied.
+// What child i takes over from its parent: full pages shared, and the rows of a last one that is copied.  Nothing
+// where the pool cannot be (top < 0).
 struct Child {
     int parent, len, full, rows;
 };
-__device__ __forceinline__ Child child_of(const ForkArgs &a, int i) {
+__device__ __forceinline__ Child child_of(const ForkArgs &a, int i, int top) {
     Child c{a.parents[i], 0, 0, 0};
+    if (top < 0) return c;
     if (c.parent < 0 || c.parent >= a.from.num_seqs) {
         atomicOr(a.pool.err, kErrTree);
         return c;
@@ -200,7 +205,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) fork_ke
         const int i = i0 + lane;
         bool need = false;
         if (i < to) {
-            const Child c = child_of(a, i);
+            const Child c = child_of(a, i, top);
             need = c.rows && entry_of(a, c.parent, c.full) >= 0;
         }
         mine += __popc(__ballot_sync(0xffffffffu, need));
@@ -211,7 +216,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) fork_ke
         Child c{-1, 0, 0, 0};
         int src = -1, dst = -1;
         if (i < to) {
-            c = child_of(a, i);
+            c = child_of(a, i, top);
             if (c.rows) src = entry_of(a, c.parent, c.full);
         }
         const unsigned m = __ballot_sync(0xffffffffu, src >= 0);
@@ -244,8 +249,8 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1) fork_ke
         }
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        if (total > top) atomicOr(a.pool.err, kErrNoPages);
-        if (total) *a.pool.num_free = max(top - total, 0);
+        if (total > max(top, 0)) atomicOr(a.pool.err, kErrNoPages);
+        if (total) *a.pool.num_free = max(top - total, 0);  // (none is asked for where top < 0)
     }
 }
 

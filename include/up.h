@@ -574,8 +574,9 @@ up_status up_compact_kv(const up_paged_kv *cache, const int32_t *cu_seqlens, int
  *   num_free    int32 [1].
  * A new pool has no holders, all pages on the stack and block tables of -1.  Calls on one pool
  * (or one block table) are ordered by the caller: one stream, or events.  Tables and stack
- * come out the same in every run.  A num_free outside [0, num_pages], or a stack entry that
- * is no page, sets UP_DEVERR_BAD_REFS.
+ * come out the same in every run.  A num_free outside [0, num_pages] sets UP_DEVERR_BAD_REFS, and the
+ * call changes neither pool nor table (a fork's children are all empty).  A stack entry that is no
+ * page sets it too, and whoever takes it goes without.
  */
 typedef struct {
     int32_t *refs;

@@ -308,6 +308,36 @@ def test_pool_errors():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wrong", [-1, 21, 2 ** 31 - 1, -2 ** 31])
+def test_a_count_that_cannot_be_changes_nothing(wrong):
+    """A number of free pages that cannot be is reported by every call and stays, like the stack, the holders and the
+    tables: once it is put right the pool is as it was."""
+    pool, table = up.PagePool.full(20), ints([[-1] * 8] * 3)
+    lens = ints([50, 20, 128])
+    up.reserve_pages(pool, table, 16, ints([0, 0, 0]), lens)
+    free = int(pool.num_free)
+    was = [x.clone() for x in (pool.refs, pool.free_pages, table)]
+    pool.num_free.fill_(wrong)
+
+    def stays():
+        assert up.get_device_error() == 0x200
+        assert int(pool.num_free) == wrong
+        for x, y in zip(was, (pool.refs, pool.free_pages, table)):
+            assert torch.equal(x, y)
+
+    up.reserve_pages(pool, table, 16, lens, ints([60, 70, 128]))
+    stays()
+    up.release_pages(pool, table, 16, None, lens)
+    stays()
+    t2, l2, copies = up.fork_pages(pool, table, lens, 16, ints([0, 1, 2]))
+    stays()
+    assert bool((t2 == -1).all()) and l2.tolist() == [0] * 3 and copies.tolist() == [[-1] * 3, [-1] * 3, [0] * 3]
+    pool.num_free.fill_(free)
+    up.release_pages(pool, table, 16, None, lens)
+    assert up.get_device_error() == 0 and int(pool.num_free) == 20 and not pool.refs.any() and bool((table == -1).all())
+
+
+@pytest.mark.gpu
 def test_pool_calls_on_a_side_stream():
     """All calls with stream=, ordered by it alone, and buffers that the caller brings."""
     m = Made([(0, 70), (0, 48)], 2, 64, 16, "bf16", seed=3, extra=20)
