@@ -68,11 +68,10 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
     pdl_wait();
     const int top = free_of(pool);
-    if (top < 0) return;  // all blocks do
     const Runs runs(t.num_seqs, t.max_pages);
     // does entry i of row s want a page?
     auto wants = [&](int s, int i, int2 r) {
-        return i >= r.x && i < r.y && t.entries[(int64_t)s * t.max_pages + i] < 0;
+        return top >= 0 && i >= r.x && i < r.y && t.entries[(int64_t)s * t.max_pages + i] < 0;
     };
     int mine = 0;
     for (int64_t k = runs.from; k < runs.to; ++k) {
@@ -97,7 +96,7 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
     await_all();
     // (all blocks have read the count: they met in the scan)
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        if (total > top) atomicOr(pool.err, kErrNoPages);
+        if (total > max(top, 0)) atomicOr(pool.err, kErrNoPages);
         if (total) *pool.num_free = max(top - total, 0);
     }
 }
@@ -106,16 +105,19 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
 
 __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
     release_kernel(const PagePool pool, const PageTable t, const int32_t *first, const int32_t *end) {
+    __shared__ int s_over;  // in the cluster some entry has found its page without a holder
     const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) s_over = 0;
     pdl_wait();
     const int top = free_of(pool);
-    if (top < 0) return;  // all blocks do
+    __syncwarp();
+    arrive();
     const Runs runs(t.num_seqs, t.max_pages);
     const int num = t.num_seqs * t.max_pages;
     auto each = [&](auto &&f) {
         for (int64_t k = runs.from; k < runs.to; ++k) {
             const int s = (int)(k / runs.per_row), i0 = (int)(k % runs.per_row) * kRun + lane;
-            const int2 r = pages_in(t, first ? first[s] : 0, end[s], pool.err);
+            const int2 r = top < 0 ? make_int2(0, 0) : pages_in(t, first ? first[s] : 0, end[s], pool.err);
             if (i0 - lane >= r.y || i0 - lane + kRun <= r.x) continue;
             for (int i = i0; i < i0 + kRun; i += 32) {
                 const int at = s * t.max_pages + i;
@@ -123,33 +125,61 @@ __global__ void __cluster_dims__(kBlocks) __launch_bounds__(kThreads, 1)
             }
         }
     };
-    // one holder less for each entry; an entry of a page that nobody holds leaves the table
+    // One holder less for each entry.  Where more entries name a page than hold it, which of them find no holder is
+    // chance; they stay in the table as kOver + page, so that the page still goes back with the first of all.
+    constexpr int kOver = INT32_MIN;
+    bool over = false;
     each([&](int at, int pg) {
         if (pg < 0) return;
-        bool ok = pg < pool.num_pages;
-        if (!ok) {
+        if (pg >= pool.num_pages) {
             atomicOr(pool.err, kErrPage);
+            t.entries[at] = -1;
         } else if (atomicSub(pool.refs + pg, 1) <= 0) {
             atomicAdd(pool.refs + pg, 1);
             atomicOr(pool.err, kErrRefs);
-            ok = false;
+            t.entries[at] = kOver + pg;
+            over = true;
         }
-        if (!ok) t.entries[at] = -1;
     });
+    __syncwarp();
+    await_all();  // every block's s_over has its 0
+    if (over)
+        for (int b = 0; b < kBlocks; ++b) write_other(&s_over, b, 1);
+    __syncwarp();
     meet();
+    const bool some_over = s_over;
+    // the page of an entry that has found no holder, -1 for any other
+    auto page_over = [&](int pg) { return some_over && pg < -1 && pg - kOver < pool.num_pages ? pg - kOver : -1; };
+    if (some_over) {  // (two more passes, after an error)
+        // a count below zero is one that cannot be, and its page does not go back
+        each([&](int at, int pg) {
+            const int o = page_over(pg);
+            if (o >= 0 && __ldcg(pool.refs + o) < 0) t.entries[at] = -1;
+        });
+        meet();
+    }
     // a page without a holder goes back with the first entry that let it go: its count becomes that
     // entry's number, less the number of all
     each([&](int at, int pg) {
         if (pg >= 0 && __ldcg(pool.refs + pg) <= 0) atomicMin(pool.refs + pg, at - num);
     });
     meet();
+    if (some_over) {
+        each([&](int at, int pg) {
+            const int o = page_over(pg);
+            if (o >= 0 && __ldcg(pool.refs + o) < 0) atomicMin(pool.refs + o, at - num);
+        });
+        meet();
+    }
+    auto goes_back = [&](int at, int pg) { return pg >= 0 && __ldcg(pool.refs + pg) == at - num; };
     int mine = 0;
-    each([&](int at, int pg) { mine += __popc(__ballot_sync(0xffffffffu, pg >= 0 && __ldcg(pool.refs + pg) == at - num)); });
+    each([&](int at, int pg) { mine += __popc(__ballot_sync(0xffffffffu, goes_back(at, max(pg, page_over(pg))))); });
     int total, rank = before_warp(mine, &total);
     arrive();
     // the first entry's page on top: reserving the same entries again gives the same pages
-    each([&](int at, int pg) {
-        const bool back = pg >= 0 && __ldcg(pool.refs + pg) == at - num;
+    each([&](int at, int entry) {
+        const int pg = max(entry, page_over(entry));
+        const bool back = goes_back(at, pg);
         const unsigned m = __ballot_sync(0xffffffffu, back);
         if (back) {
             const int to = top + total - 1 - rank - __popc(m & ((1u << lane) - 1u));

@@ -77,6 +77,12 @@ __device__ __forceinline__ int read_other(const int *mine, int block) {
     return v;
 }
 
+__device__ __forceinline__ void write_other(int *mine, int block, int v) {
+    uint32_t at = (uint32_t)__cvta_generic_to_shared(mine), there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(block));
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
+}
+
 // Sum of `mine` (a warp's) over the warps before this one in the cluster; *total over all.  Every thread
 // of the cluster comes here once, with its warp's value, and meets the others again before it
 // leaves: nobody may while another block reads its sum.

@@ -338,6 +338,50 @@ def test_a_count_that_cannot_be_changes_nothing(wrong):
 
 
 @pytest.mark.gpu
+def test_a_page_named_too_often_goes_back_with_its_first_entry():
+    """The first entry of a page is looked at after the second one: at the end of a run of the table, and at the
+    beginning of the next."""
+    B, mp = 512, 64
+    rows = [[-1] * mp for _ in range(B)]
+    rows[1][10] = rows[2][0] = 3
+    rows[1][40], rows[1][50] = 5, 4
+    for _ in range(20):
+        model, table = Model(9), ints(rows)
+        model.refs, model.free = [0, 0, 0, 1, 1, 1, 0, 0, 0], [0, 1, 2]
+        pool = up.PagePool(ints(model.refs), ints(model.free + [8] * 6), ints([3]))
+        mine, end = [list(r) for r in rows], [mp * 16] * B
+        up.release_pages(pool, table, 16, None, ints(end))
+        assert model.release(mine, 16, [0] * B, end) == up.get_device_error() == 0x200
+        same(model, pool, table, mine)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,mp,pages", [(512, 64, 3000), (3, 700, 300), (900, 130, 70000), (1, 40, 4)])
+def test_pages_named_more_often_than_held(B, mp, pages):
+    """Entries of pages with fewer holders than entries, with none, and with a count that cannot be: the same tables and
+    stack as in order."""
+    r = random.Random(B)
+    for _ in range(3):
+        model, rows = Model(pages), [[-1] * mp for _ in range(B)]
+        for row in rows:
+            for i in range(mp):
+                row[i] = r.choice([-1, -5, r.randrange(pages), r.randrange(pages)])
+        named = [0] * pages
+        for row in rows:
+            for p in row:
+                if p >= 0:
+                    named[p] += 1
+        model.refs = [r.choice([n, n, max(n - 1, 0), n + 1, 0, -3]) if n else 0 for n in named]
+        model.free = [p for p in range(pages) if not named[p]]
+        pool = up.PagePool(ints(model.refs), ints(model.free + [0] * (pages - len(model.free))), ints([len(model.free)]))
+        table = ints(rows)
+        first, end = [r.randint(-5, mp * 4) for _ in range(B)], [r.randint(mp * 4, mp * 16) for _ in range(B)]
+        up.release_pages(pool, table, 16, ints(first), ints(end))
+        assert up.get_device_error() == model.release(rows, 16, first, end)
+        same(model, pool, table, rows)
+
+
+@pytest.mark.gpu
 def test_pool_calls_on_a_side_stream():
     """All calls with stream=, ordered by it alone, and buffers that the caller brings."""
     m = Made([(0, 70), (0, 48)], 2, 64, 16, "bf16", seed=3, extra=20)
