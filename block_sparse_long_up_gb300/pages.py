@@ -161,7 +161,8 @@ def compact_kv(cache, cu_seqlens, keep, cu_blocks=None, G=1, max_tokens=None, kv
     set move together behind the tokens before them; returns the lengths that remain, int32
     [num_seqs] (see up_compact_kv).
 
-    max_tokens: at most cu_seqlens[num_seqs] (default: what keep's flags stand for); kv_lens_out may be the cache's own kv_lens."""
+    max_tokens: what cu_seqlens[num_seqs] is at most (default: what keep's flags stand for, as far as the
+    block table goes); kv_lens_out may be the cache's own kv_lens."""
     if not isinstance(cache, PagedKV):
         raise TypeError("cache must be a PagedKV")
     dev, B = cache.device, cache.num_seqs
@@ -170,8 +171,9 @@ def compact_kv(cache, cu_seqlens, keep, cu_blocks=None, G=1, max_tokens=None, kv
     if cu_blocks is not None:
         _need(cu_blocks, "cu_blocks", torch.int32, dev, (B + 1,))
     G = _int32(operator.index(G))
-    if max_tokens is None:  # every token has a slot of its own
-        max_tokens = min(keep.numel() * max(G, 1), cache.k_pages.shape[0] * cache.page_size)
+    if max_tokens is None:
+        # (tokens may be more than the pool's slots: sequences share pages, and let some go)
+        max_tokens = min(keep.numel() * max(G, 1), cache.block_table.numel() * cache.page_size, 2 ** 31 - 1)
     T = max(-1, min(operator.index(max_tokens), 2 ** 62))
     with _on(stream):
         if kv_lens_out is None:

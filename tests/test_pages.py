@@ -646,6 +646,27 @@ def test_compaction_in_a_graph_and_on_a_side_stream():
 
 
 @pytest.mark.gpu
+def test_more_tokens_than_the_pool_has_slots():
+    """Sequences that share pages, or have let pages go, count more tokens than there are slots; none of them is kept,
+    so nothing moves."""
+    pool, table = up.PagePool.full(60), ints([[-1] * 64])
+    lens = ints([900])
+    up.reserve_pages(pool, table, 16, ints([0]), lens)
+    kp, vp = (torch.zeros(60, 2, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    t3, l3, copies = up.fork_pages(pool, table, lens, 16, ints([0, 0, 0]))
+    cache, cu = up.PagedKV(kp, vp, t3, l3), ints([0, 900, 1800, 2700])
+    none = torch.zeros(2700, dtype=torch.uint8, device="cuda")
+    assert l3.tolist() == [900] * 3
+    assert up.compact_kv(cache, cu, none).tolist() == [0] * 3
+    # a flag for all of a sequence
+    assert up.compact_kv(cache, cu, none[:3], cu_blocks=ints([0, 1, 2, 3]), G=2 ** 31 - 1).tolist() == [0] * 3
+    # pages behind a window that went back
+    gone = up.PagedKV(kp[:4].contiguous(), vp[:4].contiguous(), ints([[-1] * 300]), ints([4700]))
+    assert up.compact_kv(gone, ints([0, 4700]), torch.zeros(4700, dtype=torch.uint8, device="cuda")).tolist() == [0]
+    assert up.get_device_error() == 0
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits():
     page, Hk, d = 256, 8, 128
     n = (1 << 32) // (page * Hk * d) + 5
