@@ -362,7 +362,7 @@ struct Pieces {
                 turned = (len - slot) % len;
                 if (turned >= tb - ta) turned = 0;
             }
-            all.x = p.a.kv_start ? __ldg(&p.seen[u.s].x) : 0;
+            all.x = p.a.kv_start ? __ldcg(&p.seen[u.s].x) : 0;  // where the plan's atomics left it
             after = ui > 0 ? ui - 1 : n - 1;
             behind = p.units[after];
             return true;
@@ -386,7 +386,7 @@ struct Pieces {
             at = min(end, first + u.tiles);
             if (ta >= tb) continue;  // the share ends before the unit's first tile
             ++index;
-            if constexpr (kMask == kSinks) all = __ldg(p.seen + u.s);
+            if constexpr (kMask == kSinks) all = __ldcg(p.seen + u.s);  // where the plan's atomics left it
             // the next unit's description, on its way while this one is worked on
             after = ui + 1 < n ? ui + 1 : 0;
             behind = p.units[after];

@@ -348,6 +348,30 @@ def test_malformed_trees():
         assert bool((out == 0).all()) and bool((lse == -math.inf).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,Hq,Hk", [(64, 8, 2), (128, 32, 8), (256, 16, 1)])
+def test_a_malformed_tree_leaves_other_windows_alone(d, Hq, Hk):
+    """The window of each sequence's tokens, beside a sequence whose parents are wrong."""
+    lens = [(20, 700), (6, 300), (33, 1500), (9, 640)]
+    m = Made(lens, Hk, d, 32, "bf16", seed=4)
+    q = m.normal(m.T, Hq, d)
+    parents = grow(lens, 1)
+    start = torch.cat([torch.randint(kv - n - 400, kv - n, (n,), generator=torch.Generator().manual_seed(n)) for n, kv in lens])
+    start = start.clamp(min=0).to(torch.int32)
+    seen = tree_sets(lens, parents, start, 5)
+    was = held(m)
+    poison(m, seen)
+    want = oracle(was, q, seen, d ** -0.5)
+    bad = parents.clone()
+    bad[22] = 2
+    for x in want[:3]:
+        x[20:26] = 0.0 if x is not want[2] else -math.inf
+    for _ in range(50):
+        out, lse = up.attend_tree(q, m.cu, bad.cuda(), m.cache, kv_start=start.cuda(), sinks=5)
+        assert up.get_device_error() == 0x80
+        check(m, out, lse, want)
+
+
 # ------------------------------------------------------------------ how calls are made
 
 @pytest.mark.gpu
