@@ -1508,8 +1508,14 @@ __device__ __forceinline__ void join_many(const Params &p, const Plan &pl, const
 // share, most of them without any, took 8.8 us of a call of 128 tokens over 1K and 19 of 64 drafted ones
 // over 128K, whose 8 units are in 19 parts each; 7 and 13 so.)  All blocks together also write the rows of the
 // units without a visible slot, or of all tokens when the batch is malformed.
+//
+// Rows of 256 dims are joined in halves by three blocks an SM, in the calls of ranges whole by two (three ragged
+// sequences of 16/2 heads, capped and biased, where most shares end inside a unit: 317 us a call, 320.5 in halves).
+template <int D>
+constexpr bool whole_rows(Mask m) { return D == 256 && !of_sets(m); }
+
 template <bool kFp16, int D, Mask kMask>
-__global__ void __launch_bounds__(kJoinThreads, 3) attend_join_kernel(const Params p) {
+__global__ void __launch_bounds__(kJoinThreads, whole_rows<D>(kMask) ? 2 : 3) attend_join_kernel(const Params p) {
     using C = Cfg<D>;
     constexpr int kRowGroups = C::kUnitRows / kJoinRows;
     __shared__ int s_cut[kMaxSms], s_count[kMaxSms / 32];
@@ -1547,7 +1553,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) attend_join_kernel(const Para
     if (m >> lane & 1u) s_cut[before + __popc(m & ((1u << lane) - 1u))] = tid;
     __syncthreads();
     const bool split = cuts * kRowGroups * (D / 32) <= (int)gridDim.x;
-    constexpr int kWide = D < 128 ? D / 32 : 4;  // fours of columns a warp
+    constexpr int kWide = D == 256 && !whole_rows<D>(kMask) ? 4 : D / 32;  // fours of columns a warp
     const int pieces = kRowGroups * (split ? D / 32 : D / 32 / kWide);
     for (int x = blockIdx.x; x < cuts * pieces; x += gridDim.x) {
         const int c0 = s_cut[x / pieces], y = x % pieces, rows0 = y % kRowGroups * kJoinRows;
