@@ -421,8 +421,8 @@ struct Pieces {
     __device__ bool sees_some(int key, int box) const {  // of the box's slots
         return key < send() || (key < wend() && key > wfirst() - box);
     }
-    __device__ bool sees_all(int key) const {  // of the 128 slots at key, without asking for words
-        return (key >= wfirst() && key + kRows <= (kMask == kTree ? u.hi0 : wend())) || key + kRows <= send();
+    __device__ bool sees_all(int key) const {  // of the 128 slots at key, without asking for words (not of a tree)
+        return (key >= wfirst() && key + kRows <= wend()) || key + kRows <= send();
     }
     __device__ bool gaps() const { return kMask == kSinks && u.kt0 < 0; }
 };
