@@ -481,12 +481,14 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) kv_move_kernel(const
 
 // Block (j, s): the keys and values of head j of sequence s, in one launch.  It scans the sequence's flags
 // kRun at a time and moves what they keep itself, a tile of rows read into registers before it is
-// written; so nothing waits for another block.  In a graph, 8 heads of 128: 64 sequences of 64 tokens
-// 6-9 us (by tickets 16-17), 256 of 64 14-21 (18-28), one of 256 4-9 (14-16); but 16384 tokens 142-519 (20-39)
-// where all are one sequence's, and 4096 37-122 (16-21).  Which it is the host does not know: up to 1024
-// tokens times the root of the number of sequences.
+// written; so nothing waits for another block.  In a graph, 8 heads of 128 of which 10 to 97 % stay: 64 sequences
+// of 64 tokens 6-8 us (by tickets 16-17), 256 of 16 13-15 (17), one of 256 5-10 (13-15).  But a sequence that has most of
+// the tokens is one block's work for each head: 1024 take 11-34 us (14-16 by tickets), 4096 39-127 (18-24), 16384
+// 150-513 (23-47); and every block checks all of cu_seqlens: 1024 sequences of 4 tokens take 36-46 (18), 16384 of
+// one 1050-1160 (56).  The host knows how many tokens and sequences there are, not whose they are; so this is for 4096
+// tokens and 256 sequences at most, and for no more tokens than 1024 times the root of the sequences.
 constexpr int kFewThreads = 256, kRun = kFewThreads;  // a thread a flag
-bool few_tokens(int64_t T, int64_t num_seqs) { return T * T <= num_seqs << 20; }
+bool few_tokens(int64_t T, int64_t num_seqs) { return T <= 4096 && num_seqs <= 256 && T * T <= num_seqs << 20; }
 
 __global__ void __launch_bounds__(kFewThreads) kv_few_kernel(const Params p) {
     __shared__ int64_t s_src[kRun], s_dst[kRun];

@@ -560,6 +560,19 @@ def test_many_sequences_compact():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[(16, 20)] * 256, [(15, 20)] * 257, [(3841, 3900)] + [(1, 9)] * 255, [(3842, 3900)] + [(1, 9)] * 255,
+                                  [(4096, 4096)] + [(0, 3)] * 15, [(1024, 1100)], [(1025, 1100)]], ids=lambda x: f"{len(x)}-{x[0]}")
+def test_compaction_where_the_launches_change(lens):
+    """About as many tokens and sequences as one launch serves, and one more."""
+    m = Made(lens, 2, 64, 32, "bf16", seed=21)
+    flags = flags_of(lens, 1, 0.6, 4)
+    k, v, p, new = compacted(m, flags, 1)
+    out = up.compact_kv(m.cache, m.cu, torch.cat(flags).to(torch.uint8).cuda())
+    assert up.get_device_error() == 0 and out.tolist() == new
+    assert equal(m.kp, k) and equal(m.vp, v) and equal(m.pp, p)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("more", [0, 20000])
 def test_compaction_errors(more):
     """Of few tokens a sequence and of many (max_tokens counts)."""
