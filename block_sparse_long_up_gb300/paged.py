@@ -326,8 +326,9 @@ def attend_tree(q, cu_seqlens, parents, cache, scale=None, softcap=0.0, slopes=N
     [T, Hq]).  See up_attend_tree.
 
     parents int32 [T]: a parent's number among its sequence's drafted tokens, less than the
-    child's, or -1; kv_start int32 [T]: the first slot that each token sees, beside
-    the first `sinks` of its sequence; the other arguments are attend_paged's."""
+    child's, or -1; kv_start int32 [T]: the first slot that each token sees of those before the
+    drafted ones, beside the first `sinks` of its sequence (ancestors stay visible, however short
+    the window); the other arguments are attend_paged's."""
     sinks = operator.index(sinks)
     dev = cache.device
     if _rows(q, "q", cache) != q.shape[1] * cache.d:

@@ -162,7 +162,8 @@ def compact_kv(cache, cu_seqlens, keep, cu_blocks=None, G=1, max_tokens=None, kv
     [num_seqs] (see up_compact_kv).
 
     max_tokens: what cu_seqlens[num_seqs] is at most (default: what keep's flags stand for, as far as the
-    block table goes); kv_lens_out may be the cache's own kv_lens."""
+    block table goes); kv_lens_out may be the cache's own kv_lens, but where several layers' caches share
+    them in the last layer's call only: the other layers still need the old lengths."""
     if not isinstance(cache, PagedKV):
         raise TypeError("cache must be a PagedKV")
     dev, B = cache.device, cache.num_seqs

@@ -446,7 +446,10 @@ typedef struct {
  * empty mask.
  * A cached value that some query of the call may not see but another one may
  * has to be finite (its zero weight multiplies it).  Results are deterministic on
- * a given GPU model (the parts' boundaries depend on its number of SMs).
+ * a given GPU model (the parts' boundaries depend on its number of SMs).  Each weight of the
+ * softmax is rounded once to the cache's type before it multiplies a value; up_decode_attend keeps what
+ * that rounding leaves.  So a token's row here and the same token's row there differ by
+ * roundings of the type, which matters to whoever compares them bit by bit or breaks near ties.
  * Errors: as above; UP_ERR_INVALID_ARG for slopes without q_pos or pos_pages, a
  * softcap below 0 or between 0 and 1e-6, or a non-finite scale or softcap.
  */
@@ -517,11 +520,13 @@ up_status up_decode_sinks(const void *q, int Hq, const up_paged_kv *cache,
  *             other parent, or of more than UP_TREE_MAX drafted tokens, sets
  *             UP_DEVERR_BAD_TREE and its rows are those of an empty mask.
  *   kv_start  int32 [total_tokens] or NULL: the first slot that each token sees of those
- *             before the drafted ones (a window that moves with a token's depth).
+ *             before the drafted ones (a window that moves with a token's depth).  It hides no
+ *             ancestor, so a model's window that is shorter than the tree is deep is not
+ *             reproduced.
  *   sinks     as in up_attend_sinks.
  *   workspace up_attend_tree_workspace(...) bytes, 256-byte aligned; its contents on entry
  *             do not matter.
- * Values, determinism and errors are as in up_attend_paged.
+ * Values, determinism, the weights' rounding and errors are as in up_attend_paged.
  */
 #define UP_TREE_MAX 256
 
@@ -549,6 +554,9 @@ up_status up_attend_tree(const void *q, const int32_t *cu_seqlens, const int32_t
  *   G           tokens of a flag, positive.
  *   kv_lens_out int32 [num_seqs]: the cached tokens that remain, kv_lens[s] - n_s + kept (kv_lens
  *               itself is allowed; other overlaps with it, cu_seqlens or cu_blocks are refused).
+ *               Where the caches of several layers share kv_lens, only the last layer's call may
+ *               write it: an earlier one would have the others compact the wrong slots, and no
+ *               error would tell.
  *   workspace   up_compact_kv_workspace(...) bytes, 256-byte aligned; its contents on entry do
  *               not matter.
  * Pages that hold kept tokens of the n_s, or the slots that they move to, must not be shared between
